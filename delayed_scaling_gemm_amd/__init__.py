@@ -8,7 +8,9 @@ built or cannot be loaded, every call raises.
 
 Functions keep the C names: ``fp8ds_amax``, ``fp8ds_cast``, ``fp8ds_cast_health``,
 ``fp8ds_cast_batched``, ``fp8ds_scale_update``, ``fp8ds_gemm``, ``fp8ds_gemm_batched``,
-``fp8ds_linear_batched``, ``fp8ds_adamw``.
+``fp8ds_linear_batched``, ``fp8ds_adamw``; around the Linear ``fp8ds_rmsnorm`` (``_rowwise``,
+``_mx``, ``_bwd``), ``fp8ds_grad_norm``, ``fp8ds_grad_clip``, ``fp8ds_cast_mxfp4``,
+``fp8ds_dequant_mxfp4``, ``fp8ds_gemm_mxfp4``.
 """
 
 from __future__ import annotations
@@ -20,7 +22,7 @@ import threading
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libfp8ds.so")
 
-E4M3, E5M2 = 0, 1
+E4M3, E5M2, E2M1 = 0, 1, 2
 F32, BF16 = 0, 1
 ALGO_MAX, ALGO_MOST_RECENT = 0, 1
 OP_N, OP_T = 0, 1
@@ -93,6 +95,34 @@ def _declare(lib):
     lib.fp8ds_linear_batched.argtypes = [i64, i64, i64, i64, i32, vp, i64, i32, vp, i64, i32, i32,
                                          vp, vp, i32, i32, vp, vp, vp, vp, vp, i64, vp, i64, vp,
                                          i64, vp, vp]
+    norm_in = [vp, i32, i64, vp, i64, i32, vp, i32, i64, i64, f, vp, i64, vp, i32, i64, vp, i32]
+    lib.fp8ds_rmsnorm.restype = i32
+    lib.fp8ds_rmsnorm.argtypes = norm_in + [vp, vp, i64, vp, vp, vp, vp]
+    lib.fp8ds_rmsnorm_rowwise.restype = i32
+    lib.fp8ds_rmsnorm_rowwise.argtypes = norm_in + [i32, vp, i64, vp, vp, vp, vp]
+    lib.fp8ds_rmsnorm_mx.restype = i32
+    lib.fp8ds_rmsnorm_mx.argtypes = norm_in + [vp, i64, vp, i64, vp]
+    lib.fp8ds_rmsnorm_bwd_workspace.restype = i64
+    lib.fp8ds_rmsnorm_bwd_workspace.argtypes = [i64, i64]
+    lib.fp8ds_rmsnorm_bwd.restype = i32
+    lib.fp8ds_rmsnorm_bwd.argtypes = [vp, i32, i64, vp, i32, i64, vp, vp, i32, vp, i64, i64, i64,
+                                      vp, i64, vp, vp, i64, i32, vp, vp, i64, vp, vp, vp, vp]
+    lib.fp8ds_grad_norm_workspace.restype = i64
+    lib.fp8ds_grad_norm_workspace.argtypes = []
+    lib.fp8ds_grad_norm.restype = i32
+    lib.fp8ds_grad_norm.argtypes = [i32, vp, vp, vp, f, f, vp, vp, vp, i64, vp]
+    lib.fp8ds_grad_clip.restype = i32
+    lib.fp8ds_grad_clip.argtypes = [i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.fp8ds_adamw_clip.restype = i32
+    lib.fp8ds_adamw_clip.argtypes = [vp, vp, i32, vp, vp, i64, i64, f, f, f, f, f, f, vp, i64, vp,
+                                     i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.fp8ds_cast_mxfp4.restype = i32
+    lib.fp8ds_cast_mxfp4.argtypes = [vp, i32, i64, i64, vp, vp, vp, vp, vp]
+    lib.fp8ds_dequant_mxfp4.restype = i32
+    lib.fp8ds_dequant_mxfp4.argtypes = [vp, vp, i64, i64, vp, i32, vp]
+    lib.fp8ds_gemm_mxfp4.restype = i32
+    lib.fp8ds_gemm_mxfp4.argtypes = [i64, i64, i64, vp, i32, i64, vp, i64, vp, i64, vp, i64, vp,
+                                     i32, i64, vp, vp]
     return lib
 
 
@@ -448,13 +478,15 @@ def fp8ds_linear_batched(x, w, fx, fw, history, cursor, algo, margin, scale, ama
 
 def fp8ds_adamw(w, g, m, v, lr, beta1, beta2, eps, weight_decay, step, grad_scale=1.0,
                 grad_amax=None, fmt=E4M3, scale=None, q=None, q_t=None, scale_used=None,
-                amax=None, sat_count=None, stream=None):
+                amax=None, sat_count=None, stream=None, grad_coef=None):
     """Fused AdamW step on the fp32 master weights ``w`` ([rows, cols] or 1-D),
     moments ``m``, ``v`` (fp32, in place) with gradient ``g`` (bf16 or fp32), step
     count ``step`` >= 1; with ``scale`` also the FP8 copy of the new weights into
     ``q`` (uint8; ``q_t`` transposed, ``scale_used``, ``amax``, ``sat_count`` as
     ``fp8ds_cast``).
-    ``grad_amax`` (fp32 device scalar): a non-finite value skips the update."""
+    ``grad_amax`` (fp32 device scalar): a non-finite value skips the update.
+    ``grad_coef`` (fp32 device scalar, e.g. from :func:`fp8ds_grad_norm`) also
+    multiplies the gradient (``fp8ds_adamw_clip``)."""
     import torch
 
     rows, cols = (w.shape[0], w.shape[1]) if w.dim() == 2 else (1, w.numel())
@@ -474,12 +506,16 @@ def fp8ds_adamw(w, g, m, v, lr, beta1, beta2, eps, weight_decay, step, grad_scal
     _need(scale_used, "scale_used", f32, 1)
     _need(amax, "amax", f32, 1)
     _need(sat_count, "sat_count", (torch.int64,), 1)
-    _call("fp8ds_adamw", _ptr(w), _ptr(g), _dtype_code(g), _ptr(m), _ptr(v), rows, cols,
-          float(lr), float(beta1), float(beta2), float(eps),
-          float(weight_decay), float(grad_scale), int(step), _ptr(grad_amax),
-          fmt, _ptr(scale), _ptr(q), _ptr(q_t), _ptr(scale_used), _ptr(amax),
-          _ptr(sat_count), _stream(stream))
-
+    hyper = (float(lr), float(beta1), float(beta2), float(eps), float(weight_decay),
+             float(grad_scale))
+    rest = (int(step), _ptr(grad_amax), fmt, _ptr(scale), _ptr(q), _ptr(q_t), _ptr(scale_used),
+            _ptr(amax), _ptr(sat_count), _stream(stream))
+    head = (_ptr(w), _ptr(g), _dtype_code(g), _ptr(m), _ptr(v), rows, cols)
+    if grad_coef is None:
+        _call("fp8ds_adamw", *head, *hyper, *rest)
+    else:
+        _need(grad_coef, "grad_coef", f32, 1)
+        _call("fp8ds_adamw_clip", *head, *hyper, _ptr(grad_coef), *rest)
 
 
 def fp8ds_cast_rowwise(x, fmt, margin, q, scale, scale_inv=None, amax=None, stream=None):
@@ -572,6 +608,248 @@ def fp8ds_gemm_mx(M, N, K, a, fa, lda, scales_a, ld_scales_a, b, fb, ldb, scales
     _call("fp8ds_gemm_mx", M, N, K, _ptr(a), fa, lda, _ptr(scales_a), ld_scales_a, _ptr(b), fb,
           ldb, _ptr(scales_b), ld_scales_b, _ptr(c), _dtype_code(c), ldc,
           _ptr(amax_c), mma, _stream(stream))
+
+
+def _rows2d(t, name, dtypes, rows, cols):
+    """Pointer, dtype code and row distance of a 2-D tensor whose rows are dense."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    # one row (or none) has no distance to the next, whatever its stride says
+    ld = t.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"{name}: rows overlap (stride {ld} for {cols} columns)")
+    return t.data_ptr(), ld
+
+
+_codes = {}
+
+
+def _high():
+    """{dtype: code} of the high-precision types."""
+    if not _codes:
+        import torch
+
+        _codes.update({torch.bfloat16: BF16, torch.float32: F32})
+    return _codes
+
+
+def _vec(t, name, dtypes, n):
+    """Pointer of a dense tensor of at least n elements, 0 for None."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
+    if not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name}: expected a contiguous tensor of at least {n} elements")
+    return t.data_ptr()
+
+
+def _norm_args(x, gamma, eps, residual, h, y, rstd, fmt):
+    import torch
+
+    high = _high()
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [rows, cols]")
+    rows, cols = x.shape
+    xp, ldx = _rows2d(x, "x", high, rows, cols)
+    stream_type = residual.dtype if residual is not None else h.dtype if h is not None else x.dtype
+    rp, ldr, hp, ldh, yp, ldy, yt = None, cols, None, cols, None, cols, BF16
+    if residual is not None:
+        rp, ldr = _rows2d(residual, "residual", high, rows, cols)
+    if h is not None:
+        hp, ldh = _rows2d(h, "h", (stream_type,), rows, cols)
+    if y is not None:
+        yp, ldy = _rows2d(y, "y", high, rows, cols)
+        yt = high[y.dtype]
+    if stream_type not in high:
+        raise TypeError(f"h: dtype {stream_type} not in {tuple(high)}")
+    return rows, cols, (xp, high[x.dtype], ldx, rp, ldr, high[stream_type],
+                        _vec(gamma, "gamma", high, cols), high[gamma.dtype], rows, cols,
+                        float(eps), hp, ldh, yp, yt, ldy,
+                        _vec(rstd, "rstd", (torch.float32,), rows), fmt)
+
+
+def fp8ds_rmsnorm(x, gamma, eps, residual=None, h=None, y=None, rstd=None, fmt=E4M3, scale=None,
+                  q=None, scale_used=None, amax=None, sat_count=None, stream=None):
+    """RMSNorm of the rows of ``x`` [rows, cols] (``+ residual``, the sum stored in ``h``) into
+    ``y`` and / or, with the per-tensor ``scale``, its FP8 copy ``q`` (uint8).  ``amax`` and
+    ``sat_count`` are combined into (as :func:`fp8ds_cast_acc`).  Rows may be strided;
+    ``h`` may be ``residual`` or ``x`` itself."""
+    import torch
+
+    rows, cols, args = _norm_args(x, gamma, eps, residual, h, y, rstd, fmt)
+    f32 = (torch.float32,)
+    qp, ldq = (None, cols) if q is None else _rows2d(q, "q", (torch.uint8,), rows, cols)
+    _call("fp8ds_rmsnorm", *args, _vec(scale, "scale", f32, 1), qp, ldq,
+          _vec(scale_used, "scale_used", f32, 1), _vec(amax, "amax", f32, 1),
+          _vec(sat_count, "sat_count", (torch.int64,), 1), _stream(stream))
+
+
+def fp8ds_rmsnorm_rowwise(x, gamma, eps, fmt, margin, q, scale, scale_inv=None, amax=None,
+                          residual=None, h=None, y=None, rstd=None, stream=None):
+    """:func:`fp8ds_rmsnorm` with a scale per row (``scale``, ``scale_inv``, ``amax`` [rows])."""
+    import torch
+
+    rows, cols, args = _norm_args(x, gamma, eps, residual, h, y, rstd, fmt)
+    f32 = (torch.float32,)
+    qp, ldq = _rows2d(q, "q", (torch.uint8,), rows, cols)
+    _call("fp8ds_rmsnorm_rowwise", *args, int(margin), qp, ldq, _vec(scale, "scale", f32, rows),
+          _vec(scale_inv, "scale_inv", f32, rows), _vec(amax, "amax", f32, rows), _stream(stream))
+
+
+def fp8ds_rmsnorm_mx(x, gamma, eps, fmt, q, scales, residual=None, h=None, y=None, rstd=None,
+                     stream=None):
+    """:func:`fp8ds_rmsnorm` with E8M0 scales of blocks of 32: ``q`` uint8 [rows, cols] (``fmt``
+    E4M3 or E5M2) or [rows, cols / 2] (E2M1), ``scales`` uint8 [rows, cols / 32]."""
+    import torch
+
+    rows, cols, args = _norm_args(x, gamma, eps, residual, h, y, rstd, fmt)
+    u8 = (torch.uint8,)
+    qp, ldq = _rows2d(q, "q", u8, rows, cols // 2 if fmt == E2M1 else cols)
+    sp, lds = _rows2d(scales, "scales", u8, rows, cols // 32)
+    _call("fp8ds_rmsnorm_mx", *args, qp, ldq, sp, lds, _stream(stream))
+
+
+def fp8ds_rmsnorm_bwd_workspace(rows, cols) -> int:
+    """Bytes of workspace that :func:`fp8ds_rmsnorm_bwd` needs for this shape."""
+    n = lib().fp8ds_rmsnorm_bwd_workspace(rows, cols)
+    if n < 0:
+        _check(int(n))
+    return n
+
+
+def fp8ds_rmsnorm_bwd(dy, h, rstd, gamma, dx, dgamma, workspace, dres=None, fmt=E5M2, scale=None,
+                      q=None, scale_used=None, amax=None, sat_count=None, stream=None):
+    """Backward of :func:`fp8ds_rmsnorm`: ``dx`` (of ``h``'s type; ``+ dres``) and ``dgamma`` [cols]
+    fp32 from ``dy``, the stored ``h`` and ``rstd``; with ``scale`` also the FP8 copy of dx in
+    ``q``.  ``workspace``: uint8, :func:`fp8ds_rmsnorm_bwd_workspace` bytes."""
+    import torch
+
+    high, f32 = _high(), (torch.float32,)
+    if h.dim() != 2:
+        raise ValueError("h must be 2-D [rows, cols]")
+    rows, cols = h.shape
+    hp, ldh = _rows2d(h, "h", high, rows, cols)
+    yp, lddy = _rows2d(dy, "dy", high, rows, cols)
+    xp, lddx = _rows2d(dx, "dx", (h.dtype,), rows, cols)
+    rp, lddr = (None, cols) if dres is None else _rows2d(dres, "dres", (h.dtype,), rows, cols)
+    qp, ldq = (None, cols) if q is None else _rows2d(q, "q", (torch.uint8,), rows, cols)
+    wp = _vec(workspace, "workspace", (torch.uint8,), 0)
+    _call("fp8ds_rmsnorm_bwd", yp, high[dy.dtype], lddy, hp, high[h.dtype], ldh,
+          _vec(rstd, "rstd", f32, rows), _vec(gamma, "gamma", high, cols), high[gamma.dtype], rp,
+          lddr, rows, cols, xp, lddx, _vec(dgamma, "dgamma", f32, cols), wp,
+          0 if workspace is None else workspace.numel(), fmt, _vec(scale, "scale", f32, 1), qp,
+          ldq, _vec(scale_used, "scale_used", f32, 1), _vec(amax, "amax", f32, 1),
+          _vec(sat_count, "sat_count", (torch.int64,), 1), _stream(stream))
+
+
+def _tensor_list(ts, name):
+    """(addresses, dtype codes, counts) of dense high-precision tensors, as C arrays."""
+    high, n = _high(), len(ts)
+    for i, t in enumerate(ts):
+        if not t.is_cuda:
+            raise ValueError(f"{name}[{i}]: expected a CUDA tensor")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}]: expected a contiguous tensor")
+        if t.dtype not in high:
+            raise TypeError(f"{name}[{i}]: dtype {t.dtype} not in {tuple(high)}")
+    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in ts]),
+            (ctypes.c_int * n)(*[high[t.dtype] for t in ts]),
+            (ctypes.c_int64 * n)(*[t.numel() for t in ts]))
+
+
+def fp8ds_grad_norm_workspace() -> int:
+    """Bytes of workspace that :func:`fp8ds_grad_norm` needs."""
+    return lib().fp8ds_grad_norm_workspace()
+
+
+def fp8ds_grad_norm(grads, max_norm, norm, coef=None, workspace=None, grad_scale=1.0, stream=None):
+    """``norm`` (fp32 device scalar) = grad_scale times the 2-norm of all the tensors ``grads``,
+    ``coef`` = min(1, max_norm / (norm + 1e-6)).  ``workspace``: uint8,
+    :func:`fp8ds_grad_norm_workspace` bytes (needed above 65536 elements or 128 tensors)."""
+    import torch
+
+    p, ty, n = _tensor_list(grads, "grads")
+    f32 = (torch.float32,)
+    _call("fp8ds_grad_norm", len(grads), p, ty, n, float(grad_scale), float(max_norm),
+          _vec(norm, "norm", f32, 1), _vec(coef, "coef", f32, 1),
+          _vec(workspace, "workspace", (torch.uint8,), 0),
+          0 if workspace is None else workspace.numel(), _stream(stream))
+
+
+def fp8ds_grad_clip(grads, coef, out=None, stream=None):
+    """Multiply every tensor of ``grads`` by the device scalar ``coef``: in place, or into the
+    tensors ``out`` (of the same sizes; bf16 or fp32)."""
+    import torch
+
+    p, ty, n = _tensor_list(grads, "grads")
+    op = oty = None
+    if out is not None:
+        if len(out) != len(grads):
+            raise ValueError(f"out: {len(out)} tensors for {len(grads)} gradients")
+        op, oty, on = _tensor_list(out, "out")
+        for i in range(len(grads)):
+            if on[i] != n[i]:
+                raise ValueError(f"out[{i}]: {on[i]} elements for {n[i]}")
+    _call("fp8ds_grad_clip", len(grads), p, ty, n, op, oty, _vec(coef, "coef", (torch.float32,), 1),
+          _stream(stream))
+
+
+def fp8ds_cast_mxfp4(x, q, scales, q_t=None, scales_t=None, stream=None):
+    """MXFP4 cast of the 2-D ``x`` [rows, cols] (cols a multiple of 32) along its rows: packed
+    E2M1 codes ``q`` (uint8 [rows, cols / 2]) and E8M0 codes ``scales`` (uint8 [rows, cols / 32]);
+    optionally the transpose blocked along its own rows, ``q_t`` [cols, rows / 2] and
+    ``scales_t`` [cols, rows / 32] (rows a multiple of 32)."""
+    import torch
+
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [rows, cols]")
+    rows, cols = x.shape
+    n, u8, high = rows * cols, (torch.uint8,), _high()
+    _call("fp8ds_cast_mxfp4", _vec(x, "x", high, n), high[x.dtype], rows, cols,
+          _vec(q, "q", u8, n // 2), _vec(scales, "scales", u8, n // 32),
+          _vec(q_t, "q_t", u8, n // 2), _vec(scales_t, "scales_t", u8, n // 32), _stream(stream))
+
+
+def fp8ds_dequant_mxfp4(q, scales, y, stream=None):
+    """The values ``y`` [rows, cols] (bf16 or fp32) of MXFP4 codes ``q`` and ``scales``."""
+    import torch
+
+    if y.dim() != 2:
+        raise ValueError("y must be 2-D [rows, cols]")
+    rows, cols = y.shape
+    n, u8, high = rows * cols, (torch.uint8,), _high()
+    _call("fp8ds_dequant_mxfp4", _vec(q, "q", u8, n // 2), _vec(scales, "scales", u8, n // 32),
+          rows, cols, _vec(y, "y", high, n), high[y.dtype], _stream(stream))
+
+
+def fp8ds_gemm_mxfp4(M, N, K, a, fa, lda, scales_a, ld_scales_a, b, ldb, scales_b, ld_scales_b, c,
+                     ldc, amax_c=None, stream=None):
+    """``C = A B^T`` with B [N, K] in MXFP4 and A [M, K] in MXFP4 (``fa`` = E2M1) or MXFP8:
+    codes with E8M0 block scales [M, ld_scales_a] / [N, ld_scales_b] along K, a multiple of 32;
+    ``lda`` and ``ldb`` in elements."""
+    import torch
+
+    u8, high = (torch.uint8,), _high()
+    if K > 0:
+        pa, pb = (2 if fa == E2M1 else 1), 2
+        _need(a, "a", u8, _span(M, K // pa, lda // pa), contiguous=False)
+        _need(b, "b", u8, _span(N, K // pb, ldb // pb), contiguous=False)
+        _need(scales_a, "scales_a", u8, _span(M, K // 32, ld_scales_a), contiguous=False)
+        _need(scales_b, "scales_b", u8, _span(N, K // 32, ld_scales_b), contiguous=False)
+    _need(c, "c", high, _span(M, N, ldc), contiguous=False)
+    _need(amax_c, "amax_c", (torch.float32,), 1)
+    _call("fp8ds_gemm_mxfp4", M, N, K, _ptr(a), fa, lda, _ptr(scales_a), ld_scales_a, _ptr(b), ldb,
+          _ptr(scales_b), ld_scales_b, _ptr(c), _dtype_code(c), ldc, _ptr(amax_c),
+          _stream(stream))
 
 
 def abi_version() -> int:

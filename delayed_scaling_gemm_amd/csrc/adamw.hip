@@ -7,7 +7,7 @@
 // 精度与 FP8 的协同: gradient un-scaling, an FP32 AdamW step, then the updated
 // weights cast to FP8 with scaling for the next forward).  Per element, every
 // operation one rounded fp32 operation in this order, no fused multiply-add:
-//   g = grad * grad_scale
+//   g = grad * grad_scale          (times a device factor where one is given)
 //   m = beta1 * m + (1 - beta1) * g
 //   v = beta2 * v + ((1 - beta2) * g) * g
 //   w = (1 - lr * wd) * w - (lr / bc1) * (m / (sqrt(v) * (1 / sqrt(bc2)) + eps))
@@ -135,6 +135,7 @@ __device__ __forceinline__ uint32_t cast1(float w, float s, uint32_t& amax, uint
 template <bool GBF16, int FMT, bool CAST>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamWLaunch p) {
   __shared__ uint32_t red[2 * 4];
+  if (p.grad_coef) p.c.grad_scale *= *p.grad_coef;  // before g: g' = g * fl32(scale * coef)
   const int64_t n = p.rows * p.cols;
   const bool skip = adamw_skip(p);
   if (!CAST && skip) return;
@@ -175,6 +176,7 @@ __global__ __launch_bounds__(256) void adamw_transpose_kernel(AdamWLaunch p) {
   constexpr int T = 128;
   __shared__ __attribute__((aligned(16))) uint8_t tile[T * T];
   __shared__ uint32_t red[2 * 4];
+  if (p.grad_coef) p.c.grad_scale *= *p.grad_coef;
   const bool skip = adamw_skip(p);
   const float s = p.scale[0];
   const int64_t rows = p.rows, cols = p.cols;

@@ -57,6 +57,7 @@ int num_cus() {
 }
 
 bool valid_fmt(int f) { return f == FP8DS_E4M3 || f == FP8DS_E5M2; }
+bool valid_mx_fmt(int f) { return valid_fmt(f) || f == FP8DS_E2M1; }
 bool valid_dtype(int t) { return t == FP8DS_F32 || t == FP8DS_BF16; }
 
 }  // namespace
@@ -400,13 +401,13 @@ int fp8ds_linear_batched(int64_t batch, int64_t M, int64_t N, int64_t K, fp8ds_d
   return hip_status(fp8ds::launch_linear_batched(a, (int)fx, (int)fw, stream), who);
 }
 
-int fp8ds_adamw(float* w, const void* g, fp8ds_dtype gt, float* m, float* v, int64_t rows,
-                int64_t cols, float lr, float beta1, float beta2, float eps, float weight_decay,
-                float grad_scale, int64_t step, const float* grad_amax, fp8ds_format fmt,
-                const float* scale, uint8_t* q, uint8_t* q_t, float* scale_used, float* amax,
-                uint64_t* sat_count, hipStream_t stream) {
+static int adamw_common(const char* who, float* w, const void* g, fp8ds_dtype gt, float* m, float* v,
+                        int64_t rows, int64_t cols, float lr, float beta1, float beta2, float eps,
+                        float weight_decay, float grad_scale, const float* grad_coef, int64_t step,
+                        const float* grad_amax, fp8ds_format fmt, const float* scale, uint8_t* q,
+                        uint8_t* q_t, float* scale_used, float* amax, uint64_t* sat_count,
+                        hipStream_t stream) {
 #pragma clang fp contract(off)
-  const char* who = "fp8ds_adamw";
   if (!valid_dtype(gt)) return fail(FP8DS_ERR_ENUM, "%s: bad gradient dtype %d", who, (int)gt);
   if (rows < 0 || cols < 0 || (cols > 0 && rows > kMaxElems / cols))
     return fail(FP8DS_ERR_SHAPE, "%s: bad shape %lld x %lld", who, (long long)rows,
@@ -447,11 +448,33 @@ int fp8ds_adamw(float* w, const void* g, fp8ds_dtype gt, float* m, float* v, int
   c.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(b2, (double)step)));
   c.grad_scale = grad_scale;
   fp8ds::AdamWLaunch a{w, g, gt == FP8DS_BF16, m, v, rows, cols, c, grad_amax, (int)fmt, scale,
-                       cast ? q : nullptr, cast ? q_t : nullptr, amax, sat_count};
+                       cast ? q : nullptr, cast ? q_t : nullptr, amax, sat_count, grad_coef};
   hipError_t e = hipSuccess;
   if (cast) e = fp8ds::launch_prologue(1, scale, scale_used, amax, sat_count, stream);
   if (e == hipSuccess && n > 0) e = fp8ds::launch_adamw(a, stream);
   return hip_status(e, who);
+}
+
+int fp8ds_adamw(float* w, const void* g, fp8ds_dtype gt, float* m, float* v, int64_t rows,
+                int64_t cols, float lr, float beta1, float beta2, float eps, float weight_decay,
+                float grad_scale, int64_t step, const float* grad_amax, fp8ds_format fmt,
+                const float* scale, uint8_t* q, uint8_t* q_t, float* scale_used, float* amax,
+                uint64_t* sat_count, hipStream_t stream) {
+  return adamw_common("fp8ds_adamw", w, g, gt, m, v, rows, cols, lr, beta1, beta2, eps,
+                      weight_decay, grad_scale, nullptr, step, grad_amax, fmt, scale, q, q_t,
+                      scale_used, amax, sat_count, stream);
+}
+
+int fp8ds_adamw_clip(float* w, const void* g, fp8ds_dtype gt, float* m, float* v, int64_t rows,
+                     int64_t cols, float lr, float beta1, float beta2, float eps,
+                     float weight_decay, float grad_scale, const float* grad_coef, int64_t step,
+                     const float* grad_amax, fp8ds_format fmt, const float* scale, uint8_t* q,
+                     uint8_t* q_t, float* scale_used, float* amax, uint64_t* sat_count,
+                     hipStream_t stream) {
+  if (!grad_coef) return fail(FP8DS_ERR_NULL, "fp8ds_adamw_clip: grad_coef is null");
+  return adamw_common("fp8ds_adamw_clip", w, g, gt, m, v, rows, cols, lr, beta1, beta2, eps,
+                      weight_decay, grad_scale, grad_coef, step, grad_amax, fmt, scale, q, q_t,
+                      scale_used, amax, sat_count, stream);
 }
 
 int fp8ds_gemm_rowcol(fp8ds_op opa, fp8ds_op opb, int64_t M, int64_t N, int64_t K,
@@ -609,6 +632,444 @@ int fp8ds_gemm_mx(int64_t M, int64_t N, int64_t K, const uint8_t* A, fp8ds_forma
     p.batch = 1; p.stride_a = 0; p.stride_b = 0; p.stride_c = 0;
     p.sc_a = scales_a; p.sc_b = scales_b; p.ldsa = ld_scales_a; p.ldsb = ld_scales_b;
     e = fp8ds::launch_gemm_mx(p, mma == FP8DS_MMA_EXACT, num_cus(), stream);
+  }
+  return hip_status(e, who);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ RMSNorm
+
+namespace {
+
+// One matrix argument of the norm: rows of `cols` elements of `esz` bytes, `ld` apart.
+struct RowsArg {
+  const char* name;
+  const void* p;
+  int64_t ld;
+  int esz;
+};
+
+// Elementwise alignment of every matrix, ld >= cols; *vec: rows on 16-byte borders.
+int check_rows(const char* who, const RowsArg* args, int n, int64_t rows, int64_t cols, bool* vec) {
+  *vec = cols % 8 == 0;
+  for (int i = 0; i < n; ++i) {
+    const RowsArg& a = args[i];
+    if (!a.p) continue;
+    if (a.ld < cols || a.ld > kMaxElems || (rows > 1 && a.ld > kMaxElems / rows))
+      return fail(FP8DS_ERR_SHAPE, "%s: leading dimension %lld of %s (rows of %lld)", who,
+                  (long long)a.ld, a.name, (long long)cols);
+    if (reinterpret_cast<uintptr_t>(a.p) % a.esz)
+      return fail(FP8DS_ERR_ALIGN, "%s: %s is not aligned to its elements", who, a.name);
+    // 8 elements of one byte are stored as 8 bytes
+    const uintptr_t need = a.esz == 1 ? 8 : 16;
+    if (reinterpret_cast<uintptr_t>(a.p) % need || (rows > 1 && (a.ld * a.esz) % need)) *vec = false;
+  }
+  return FP8DS_OK;
+}
+
+int check_norm_shape(const char* who, int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31) ||
+      (cols > 0 && rows > kMaxElems / cols))
+    return fail(FP8DS_ERR_SHAPE, "%s: bad shape %lld x %lld", who, (long long)rows, (long long)cols);
+  return FP8DS_OK;
+}
+
+// What the three forward calls share: checks, and all of NormArgs but the quantised output.
+int norm_args(const char* who, fp8ds::NormArgs& a, const void* x, fp8ds_dtype xt, int64_t ldx,
+              const void* residual, int64_t ldr, fp8ds_dtype ht, const void* gamma, fp8ds_dtype gt,
+              int64_t rows, int64_t cols, float eps, void* h, int64_t ldh, void* y, fp8ds_dtype yt,
+              int64_t ldy, float* rstd, uint8_t* q, int64_t ldq, int64_t qcols) {
+  if (!valid_dtype(xt) || !valid_dtype(ht) || !valid_dtype(gt) || !valid_dtype(yt))
+    return fail(FP8DS_ERR_ENUM, "%s: bad dtype", who);
+  if (xt == FP8DS_F32 && ht == FP8DS_BF16)
+    return fail(FP8DS_ERR_UNSUPPORTED, "%s: an FP32 x with a BF16 residual stream", who);
+  if (!(std::isfinite(eps) && eps >= 0.0f)) return fail(FP8DS_ERR_VALUE, "%s: bad eps", who);
+  if (int e = check_norm_shape(who, rows, cols)) return e;
+  if (rows > 0 && cols > 0) {
+    if (!x || !gamma) return fail(FP8DS_ERR_NULL, "%s: x and gamma are required", who);
+    const int hs = ht == FP8DS_BF16 ? 2 : 4, gs = gt == FP8DS_BF16 ? 2 : 4;
+    const RowsArg m[] = {{"x", x, ldx, xt == FP8DS_BF16 ? 2 : 4},
+                         {"residual", residual, ldr, hs},
+                         {"h", h, ldh, hs},
+                         {"y", y, ldy, yt == FP8DS_BF16 ? 2 : 4}};
+    if (int e = check_rows(who, m, 4, rows, cols, &a.vec)) return e;
+    bool qvec = true;
+    const RowsArg qm[] = {{"q", q, ldq, 1}};
+    if (int e = check_rows(who, qm, 1, rows, qcols, &qvec)) return e;
+    // (q's own column count does not decide: packed rows are cols / 2 bytes long)
+    if (q && (reinterpret_cast<uintptr_t>(q) % 8 || (rows > 1 && ldq % 8))) a.vec = false;
+    if (reinterpret_cast<uintptr_t>(gamma) % gs)
+      return fail(FP8DS_ERR_ALIGN, "%s: gamma is not aligned to its elements", who);
+    if (reinterpret_cast<uintptr_t>(gamma) % 16) a.vec = false;
+  }
+  if (reinterpret_cast<uintptr_t>(rstd) % 4)
+    return fail(FP8DS_ERR_ALIGN, "%s: rstd is not aligned to its elements", who);
+  a.x = x; a.x_bf16 = xt == FP8DS_BF16; a.ldx = ldx;
+  a.res = residual; a.ldr = ldr; a.h_bf16 = ht == FP8DS_BF16;
+  a.gamma = gamma; a.gamma_bf16 = gt == FP8DS_BF16;
+  a.rows = rows; a.cols = cols; a.eps = eps;
+  a.h = h; a.ldh = ldh;
+  a.y = y; a.y_bf16 = yt == FP8DS_BF16; a.ldy = ldy;
+  a.rstd = rstd;
+  a.q = q; a.ldq = ldq;
+  return FP8DS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8ds_rmsnorm(const void* x, fp8ds_dtype xt, int64_t ldx, const void* residual, int64_t ldr,
+                  fp8ds_dtype ht, const void* gamma, fp8ds_dtype gt, int64_t rows, int64_t cols,
+                  float eps, void* h, int64_t ldh, void* y, fp8ds_dtype yt, int64_t ldy,
+                  float* rstd, fp8ds_format fmt, const float* scale, uint8_t* q, int64_t ldq,
+                  float* scale_used, float* amax, uint64_t* sat_count, hipStream_t stream) {
+  const char* who = "fp8ds_rmsnorm";
+  fp8ds::NormArgs a = {};
+  const bool cast = scale != nullptr;
+  if (cast && !valid_fmt(fmt)) return fail(FP8DS_ERR_ENUM, "%s: bad format %d", who, (int)fmt);
+  if (!cast && (q || scale_used || amax || sat_count))
+    return fail(FP8DS_ERR_NULL, "%s: q, scale_used, amax and sat_count need scale", who);
+  if (int e = norm_args(who, a, x, xt, ldx, residual, ldr, ht, gamma, gt, rows, cols, eps, h, ldh, y,
+                        yt, ldy, rstd, q, ldq, cols))
+    return e;
+  if (cast && rows > 0 && cols > 0 && !q) return fail(FP8DS_ERR_NULL, "%s: q is null", who);
+  if (rows == 0 || cols == 0)  // nothing to combine; the snapshot is still written
+    return scale_used ? hip_status(fp8ds::launch_prologue(1, scale, scale_used, nullptr, nullptr,
+                                                          stream), who)
+                      : ok();
+  a.mode = cast ? 1 : 0;
+  a.fmt = (int)fmt;
+  a.scale_in = scale; a.scale_used = scale_used; a.amax = amax; a.sat = sat_count;
+  return hip_status(fp8ds::launch_norm_fwd(a, stream), who);
+}
+
+int fp8ds_rmsnorm_rowwise(const void* x, fp8ds_dtype xt, int64_t ldx, const void* residual,
+                          int64_t ldr, fp8ds_dtype ht, const void* gamma, fp8ds_dtype gt,
+                          int64_t rows, int64_t cols, float eps, void* h, int64_t ldh, void* y,
+                          fp8ds_dtype yt, int64_t ldy, float* rstd, fp8ds_format fmt, int margin,
+                          uint8_t* q, int64_t ldq, float* scale, float* scale_inv, float* amax,
+                          hipStream_t stream) {
+  const char* who = "fp8ds_rmsnorm_rowwise";
+  fp8ds::NormArgs a = {};
+  if (!valid_fmt(fmt)) return fail(FP8DS_ERR_ENUM, "%s: bad format %d", who, (int)fmt);
+  if (margin < -126 || margin > 126)
+    return fail(FP8DS_ERR_SHAPE, "%s: margin %d not in [-126, 126]", who, margin);
+  if (int e = norm_args(who, a, x, xt, ldx, residual, ldr, ht, gamma, gt, rows, cols, eps, h, ldh, y,
+                        yt, ldy, rstd, q, ldq, cols))
+    return e;
+  if (rows == 0 || cols == 0) return ok();
+  if (!q || !scale) return fail(FP8DS_ERR_NULL, "%s: q and scale are required", who);
+  a.mode = 2;
+  a.fmt = (int)fmt; a.margin = margin;
+  a.scale_out = scale; a.scale_inv = scale_inv; a.amax = amax;
+  return hip_status(fp8ds::launch_norm_fwd(a, stream), who);
+}
+
+int fp8ds_rmsnorm_mx(const void* x, fp8ds_dtype xt, int64_t ldx, const void* residual, int64_t ldr,
+                     fp8ds_dtype ht, const void* gamma, fp8ds_dtype gt, int64_t rows, int64_t cols,
+                     float eps, void* h, int64_t ldh, void* y, fp8ds_dtype yt, int64_t ldy,
+                     float* rstd, fp8ds_format fmt, uint8_t* q, int64_t ldq, uint8_t* scales,
+                     int64_t ld_scales, hipStream_t stream) {
+  const char* who = "fp8ds_rmsnorm_mx";
+  fp8ds::NormArgs a = {};
+  if (!valid_mx_fmt(fmt)) return fail(FP8DS_ERR_ENUM, "%s: bad format %d", who, (int)fmt);
+  if (cols > 0 && cols % 32 != 0)
+    return fail(FP8DS_ERR_SHAPE, "%s: the row length %lld is not a multiple of the block (32)", who,
+                (long long)cols);
+  if (int e = norm_args(who, a, x, xt, ldx, residual, ldr, ht, gamma, gt, rows, cols, eps, h, ldh, y,
+                        yt, ldy, rstd, q, ldq, fmt == FP8DS_E2M1 ? cols / 2 : cols))
+    return e;
+  if (rows == 0 || cols == 0) return ok();
+  if (!q || !scales) return fail(FP8DS_ERR_NULL, "%s: q and scales are required", who);
+  if (ld_scales < cols / 32 || ld_scales > kMaxElems / rows)
+    return fail(FP8DS_ERR_SHAPE, "%s: ld_scales %lld for %lld blocks a row", who,
+                (long long)ld_scales, (long long)(cols / 32));
+  if (!a.vec)
+    return fail(FP8DS_ERR_ALIGN, "%s: the rows of x, residual, h, y and gamma must be 16-byte "
+                "aligned, those of q 8-byte", who);
+  a.mode = 3;
+  a.fmt = (int)fmt;
+  a.mx_scales = scales; a.ldms = ld_scales;
+  return hip_status(fp8ds::launch_norm_fwd(a, stream), who);
+}
+
+int64_t fp8ds_rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
+  if (check_norm_shape("fp8ds_rmsnorm_bwd_workspace", rows, cols)) return FP8DS_ERR_SHAPE;
+  ok();
+  return rows == 0 ? 0 : (int64_t)fp8ds::norm_bwd_parts(rows, cols) * cols * (int64_t)sizeof(float);
+}
+
+int fp8ds_rmsnorm_bwd(const void* dy, fp8ds_dtype dt, int64_t lddy, const void* h, fp8ds_dtype ht,
+                      int64_t ldh, const float* rstd, const void* gamma, fp8ds_dtype gt,
+                      const void* dres, int64_t lddr, int64_t rows, int64_t cols, void* dx,
+                      int64_t lddx, float* dgamma, void* workspace, int64_t workspace_bytes,
+                      fp8ds_format fmt, const float* scale, uint8_t* q, int64_t ldq,
+                      float* scale_used, float* amax, uint64_t* sat_count, hipStream_t stream) {
+  const char* who = "fp8ds_rmsnorm_bwd";
+  fp8ds::NormBwdArgs a = {};
+  if (!valid_dtype(dt) || !valid_dtype(ht) || !valid_dtype(gt))
+    return fail(FP8DS_ERR_ENUM, "%s: bad dtype", who);
+  if (dt == FP8DS_F32 && ht == FP8DS_BF16)
+    return fail(FP8DS_ERR_UNSUPPORTED, "%s: an FP32 dy with a BF16 residual stream", who);
+  const bool cast = scale != nullptr;
+  if (cast && !valid_fmt(fmt)) return fail(FP8DS_ERR_ENUM, "%s: bad format %d", who, (int)fmt);
+  if (!cast && (q || scale_used || amax || sat_count))
+    return fail(FP8DS_ERR_NULL, "%s: q, scale_used, amax and sat_count need scale", who);
+  if (int e = check_norm_shape(who, rows, cols)) return e;
+  if (cols == 0)
+    return scale_used ? hip_status(fp8ds::launch_prologue(1, scale, scale_used, nullptr, nullptr,
+                                                          stream), who)
+                      : ok();
+  if (!dgamma) return fail(FP8DS_ERR_NULL, "%s: dgamma is required", who);
+  if (reinterpret_cast<uintptr_t>(dgamma) % 4 || reinterpret_cast<uintptr_t>(rstd) % 4)
+    return fail(FP8DS_ERR_ALIGN, "%s: dgamma and rstd are fp32", who);
+  if (rows > 0) {
+    if (!dy || !h || !rstd || !gamma || !dx)
+      return fail(FP8DS_ERR_NULL, "%s: dy, h, rstd, gamma and dx are required", who);
+    if (cast && !q) return fail(FP8DS_ERR_NULL, "%s: q is null", who);
+    const int hs = ht == FP8DS_BF16 ? 2 : 4;
+    const RowsArg m[] = {{"dy", dy, lddy, dt == FP8DS_BF16 ? 2 : 4}, {"h", h, ldh, hs},
+                         {"dres", dres, lddr, hs}, {"dx", dx, lddx, hs}, {"q", q, ldq, 1}};
+    if (int e = check_rows(who, m, 5, rows, cols, &a.vec)) return e;
+    if (reinterpret_cast<uintptr_t>(gamma) % (gt == FP8DS_BF16 ? 2 : 4))
+      return fail(FP8DS_ERR_ALIGN, "%s: gamma is not aligned to its elements", who);
+    if (reinterpret_cast<uintptr_t>(gamma) % 16) a.vec = false;
+    const int64_t need = fp8ds_rmsnorm_bwd_workspace(rows, cols);
+    if (!workspace || workspace_bytes < need)
+      return fail(workspace ? FP8DS_ERR_SHAPE : FP8DS_ERR_NULL, "%s: workspace of %lld bytes, %lld "
+                  "needed", who, (long long)(workspace ? workspace_bytes : 0), (long long)need);
+    if (!aligned16(workspace))
+      return fail(FP8DS_ERR_ALIGN, "%s: workspace not 16-byte aligned", who);
+  }
+  a.dy = dy; a.x_bf16 = dt == FP8DS_BF16; a.lddy = lddy;
+  a.h = h; a.h_bf16 = ht == FP8DS_BF16; a.ldh = ldh;
+  a.dres = dres; a.lddr = lddr;
+  a.rstd = rstd; a.gamma = gamma; a.gamma_bf16 = gt == FP8DS_BF16;
+  a.rows = rows; a.cols = cols;
+  a.dx = dx; a.lddx = lddx; a.dgamma = dgamma; a.work = static_cast<float*>(workspace);
+  a.fmt = (int)fmt; a.scale_in = scale; a.q = q; a.ldq = ldq;
+  a.scale_used = scale_used; a.amax = amax; a.sat = sat_count;
+  hipError_t e = hipSuccess;
+  if (rows == 0 && scale_used)
+    e = fp8ds::launch_prologue(1, scale, scale_used, nullptr, nullptr, stream);
+  if (e == hipSuccess) e = fp8ds::launch_norm_bwd(a, stream);
+  return hip_status(e, who);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ gradient norm, clip
+
+namespace {
+
+constexpr int kMaxGrads = 4096;
+constexpr int kNormBlocks = 1024;                      // partial sums per launch
+constexpr int64_t kSingleElems = 65536;                // up to here one workgroup takes the norm
+
+int check_grads(const char* who, int n, const void* const* grads, const fp8ds_dtype* types,
+                const int64_t* counts, void* const* out, const fp8ds_dtype* out_types) {
+  int64_t total = 0;  // bounds a launch's chunk numbers too (2^40 elements: 2^27 chunks)
+  if (n < 0 || n > kMaxGrads)
+    return fail(FP8DS_ERR_SHAPE, "%s: n_tensors %d not in [0, %d]", who, n, kMaxGrads);
+  if (n > 0 && (!grads || !types || !counts || (out && !out_types)))
+    return fail(FP8DS_ERR_NULL, "%s: the arrays of addresses, types and counts are required", who);
+  for (int i = 0; i < n; ++i) {
+    if (!valid_dtype(types[i]) || (out && !valid_dtype(out_types[i])))
+      return fail(FP8DS_ERR_ENUM, "%s: bad dtype of tensor %d", who, i);
+    if (counts[i] < 0 || counts[i] > kMaxElems)
+      return fail(FP8DS_ERR_SHAPE, "%s: bad count %lld of tensor %d", who, (long long)counts[i], i);
+    total += counts[i];
+    if (total > kMaxElems) return fail(FP8DS_ERR_SHAPE, "%s: too many elements", who);
+    if (counts[i] == 0) continue;
+    if (!grads[i] || (out && !out[i]))
+      return fail(FP8DS_ERR_NULL, "%s: tensor %d is null", who, i);
+    if (reinterpret_cast<uintptr_t>(grads[i]) % (types[i] == FP8DS_BF16 ? 2 : 4) ||
+        (out && reinterpret_cast<uintptr_t>(out[i]) % (out_types[i] == FP8DS_BF16 ? 2 : 4)))
+      return fail(FP8DS_ERR_ALIGN, "%s: tensor %d is not aligned to its elements", who, i);
+    if (out && out[i] == grads[i] && out_types[i] != types[i])
+      return fail(FP8DS_ERR_UNSUPPORTED, "%s: tensor %d in place with another type", who, i);
+  }
+  return FP8DS_OK;
+}
+
+// Fills a table from tensor *i on (empty tensors left out) and advances *i.
+void fill_table(fp8ds::TensorTable& tb, int* i, int n, const void* const* grads,
+                const fp8ds_dtype* types, const int64_t* counts, void* const* out,
+                const fp8ds_dtype* out_types) {
+  std::memset(&tb, 0, sizeof(tb));
+  int64_t chunks = 0;
+  for (; *i < n && tb.count < fp8ds::kTensors; ++*i) {
+    if (counts[*i] == 0) continue;
+    const int64_t c = fp8ds::table_chunks(counts[*i]);
+    const int k = tb.count++;
+    tb.src[k] = grads[*i];
+    tb.dst[k] = out ? out[*i] : const_cast<void*>(grads[*i]);
+    tb.n[k] = counts[*i];
+    tb.start[k] = (uint32_t)chunks;
+    if (types[*i] == FP8DS_BF16) tb.src_bf16[k >> 5] |= 1u << (k & 31);
+    if ((out ? out_types[*i] : types[*i]) == FP8DS_BF16) tb.dst_bf16[k >> 5] |= 1u << (k & 31);
+    chunks += c;
+    tb.start[k + 1] = (uint32_t)chunks;
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+// one row of partial sums per launch
+int64_t fp8ds_grad_norm_workspace(void) {
+  return (int64_t)(kMaxGrads / fp8ds::kTensors) * kNormBlocks * (int64_t)sizeof(double);
+}
+
+int fp8ds_grad_norm(int n_tensors, const void* const* grads, const fp8ds_dtype* types,
+                    const int64_t* counts, float grad_scale, float max_norm, float* norm,
+                    float* coef, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  const char* who = "fp8ds_grad_norm";
+  if (int e = check_grads(who, n_tensors, grads, types, counts, nullptr, nullptr)) return e;
+  if (!norm) return fail(FP8DS_ERR_NULL, "%s: norm is required", who);
+  if (!(std::isfinite(grad_scale) && grad_scale > 0.0f))
+    return fail(FP8DS_ERR_VALUE, "%s: grad_scale must be finite and > 0", who);
+  if (coef && !(max_norm > 0.0f)) return fail(FP8DS_ERR_VALUE, "%s: max_norm must be > 0", who);
+  if (reinterpret_cast<uintptr_t>(norm) % 4 || reinterpret_cast<uintptr_t>(coef) % 4)
+    return fail(FP8DS_ERR_ALIGN, "%s: norm and coef are fp32", who);
+  int64_t total = 0;
+  for (int i = 0; i < n_tensors; ++i) total += counts[i];
+  fp8ds::TensorTable tb;
+  int i = 0;
+  fill_table(tb, &i, n_tensors, grads, types, counts, nullptr, nullptr);
+  if (i == n_tensors && total <= kSingleElems)
+    return hip_status(fp8ds::launch_grad_norm_single(tb, grad_scale, max_norm, norm, coef, stream),
+                      who);
+  if (!workspace || workspace_bytes < fp8ds_grad_norm_workspace())
+    return fail(workspace ? FP8DS_ERR_SHAPE : FP8DS_ERR_NULL, "%s: workspace of %lld bytes, %lld "
+                "needed", who, (long long)(workspace ? workspace_bytes : 0),
+                (long long)fp8ds_grad_norm_workspace());
+  if (!aligned16(workspace)) return fail(FP8DS_ERR_ALIGN, "%s: workspace not 16-byte aligned", who);
+  double* parts = static_cast<double*>(workspace);
+  int used = 0;
+  hipError_t e = hipSuccess;
+  while (e == hipSuccess && tb.count > 0) {
+    const uint32_t chunks = tb.start[tb.count];
+    const int blocks = (int)(chunks < (uint32_t)kNormBlocks ? chunks : (uint32_t)kNormBlocks);
+    e = fp8ds::launch_grad_norm_part(tb, blocks, parts + used, stream);
+    used += blocks;
+    fill_table(tb, &i, n_tensors, grads, types, counts, nullptr, nullptr);
+  }
+  if (e == hipSuccess)
+    e = fp8ds::launch_grad_norm_join(parts, used, grad_scale, max_norm, norm, coef, stream);
+  return hip_status(e, who);
+}
+
+int fp8ds_grad_clip(int n_tensors, const void* const* grads, const fp8ds_dtype* types,
+                    const int64_t* counts, void* const* out, const fp8ds_dtype* out_types,
+                    const float* coef, hipStream_t stream) {
+  const char* who = "fp8ds_grad_clip";
+  if (int e = check_grads(who, n_tensors, grads, types, counts, out, out_types)) return e;
+  if (!coef) return fail(FP8DS_ERR_NULL, "%s: coef is required", who);
+  hipError_t e = hipSuccess;
+  for (int i = 0; e == hipSuccess && i < n_tensors;) {
+    fp8ds::TensorTable tb;
+    fill_table(tb, &i, n_tensors, grads, types, counts, out, out_types);
+    e = fp8ds::launch_grad_clip(tb, coef, stream);
+  }
+  return hip_status(e, who);
+}
+
+// ------------------------------------------------------------------ MXFP4
+
+int fp8ds_cast_mxfp4(const void* x, fp8ds_dtype xt, int64_t rows, int64_t cols, uint8_t* q,
+                     uint8_t* scales, uint8_t* q_t, uint8_t* scales_t, hipStream_t stream) {
+  const char* who = "fp8ds_cast_mxfp4";
+  if (!valid_dtype(xt)) return fail(FP8DS_ERR_ENUM, "%s: bad dtype %d", who, (int)xt);
+  if (rows < 0 || cols < 0 || (cols > 0 && rows > kMaxElems / cols))
+    return fail(FP8DS_ERR_SHAPE, "%s: bad shape %lld x %lld", who, (long long)rows,
+                (long long)cols);
+  if (cols % 32 != 0)
+    return fail(FP8DS_ERR_SHAPE, "%s: the row length %lld is not a multiple of the block (32)",
+                who, (long long)cols);
+  const int64_t n = rows * cols;
+  if (n == 0) return ok();
+  if (!x || !q || !scales) return fail(FP8DS_ERR_NULL, "%s: x, q and scales are required", who);
+  if (!q_t != !scales_t) return fail(FP8DS_ERR_NULL, "%s: q_t and scales_t go together", who);
+  if (!aligned16(x) || !aligned16(q) || (q_t && !aligned16(q_t)))
+    return fail(FP8DS_ERR_ALIGN, "%s: x, q and q_t must be 16-byte aligned", who);
+  if (!q_t)
+    return hip_status(fp8ds::launch_mxfp4_cast(x, xt == FP8DS_BF16, n, q, scales, stream), who);
+  if (rows % 32 != 0)
+    return fail(FP8DS_ERR_SHAPE, "%s: a transposed copy needs rows in multiples of 32 (got %lld)",
+                who, (long long)rows);
+  if ((rows + 127) / 128 > 65535 || (cols + 127) / 128 > (int64_t(1) << 31) - 1)
+    return fail(FP8DS_ERR_SHAPE, "%s: too many tiles for a transposed copy", who);
+  return hip_status(fp8ds::launch_mxfp4_cast_transpose(x, xt == FP8DS_BF16, rows, cols, q, scales,
+                                                       q_t, scales_t, stream),
+                    who);
+}
+
+int fp8ds_dequant_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t cols,
+                        void* y, fp8ds_dtype yt, hipStream_t stream) {
+  const char* who = "fp8ds_dequant_mxfp4";
+  if (!valid_dtype(yt)) return fail(FP8DS_ERR_ENUM, "%s: bad dtype %d", who, (int)yt);
+  if (rows < 0 || cols < 0 || (cols > 0 && rows > kMaxElems / cols))
+    return fail(FP8DS_ERR_SHAPE, "%s: bad shape %lld x %lld", who, (long long)rows,
+                (long long)cols);
+  if (cols % 32 != 0)
+    return fail(FP8DS_ERR_SHAPE, "%s: the row length %lld is not a multiple of the block (32)",
+                who, (long long)cols);
+  if (rows * cols == 0) return ok();
+  if (!q || !scales || !y) return fail(FP8DS_ERR_NULL, "%s: q, scales and y are required", who);
+  if (!aligned16(q) || !aligned16(y))
+    return fail(FP8DS_ERR_ALIGN, "%s: q and y must be 16-byte aligned", who);
+  return hip_status(fp8ds::launch_mxfp4_dequant(q, scales, rows * cols, y, yt == FP8DS_BF16, stream),
+                    who);
+}
+
+int fp8ds_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t* A, fp8ds_format fa,
+                     int64_t lda, const uint8_t* scales_a, int64_t ld_scales_a, const uint8_t* B,
+                     int64_t ldb, const uint8_t* scales_b, int64_t ld_scales_b, void* C,
+                     fp8ds_dtype ct, int64_t ldc, float* amax_c, hipStream_t stream) {
+  const char* who = "fp8ds_gemm_mxfp4";
+  if (!valid_mx_fmt(fa)) return fail(FP8DS_ERR_ENUM, "%s: bad format %d", who, (int)fa);
+  if (!valid_dtype(ct)) return fail(FP8DS_ERR_ENUM, "%s: bad output dtype", who);
+  const int64_t lim = int64_t(1) << 31;
+  if (M < 0 || N < 0 || K < 0 || M >= lim || N >= lim || K >= lim)
+    return fail(FP8DS_ERR_SHAPE, "%s: bad M/N/K %lld/%lld/%lld", who, (long long)M, (long long)N,
+                (long long)K);
+  if (K % 32 != 0)
+    return fail(FP8DS_ERR_SHAPE, "%s: K = %lld is not a multiple of the block (32)", who,
+                (long long)K);
+  if (M > 65535 * int64_t(64))
+    return fail(FP8DS_ERR_SHAPE, "%s: M = %lld is too large", who, (long long)M);
+  if (amax_c && reinterpret_cast<uintptr_t>(amax_c) % 4)
+    return fail(FP8DS_ERR_ALIGN, "%s: amax_c is fp32", who);
+  if (M == 0 || N == 0) {
+    if (amax_c)
+      return hip_status(fp8ds::launch_prologue(1, nullptr, nullptr, amax_c, nullptr, stream), who);
+    return ok();
+  }
+  if (lda < K || ldb < K || ldc < N || ld_scales_a < K / 32 || ld_scales_b < K / 32 ||
+      lda > kMaxElems / M || ldb > kMaxElems / N || ldc > kMaxElems / M ||
+      ld_scales_a > kMaxElems / M || ld_scales_b > kMaxElems / N)
+    return fail(FP8DS_ERR_SHAPE, "%s: bad leading dimension", who);
+  if (!C || (K > 0 && (!A || !B || !scales_a || !scales_b)))
+    return fail(FP8DS_ERR_NULL, "%s: A, B, their scales and C are required", who);
+  const int esz = ct == FP8DS_BF16 ? 2 : 4;
+  if (K > 0 && (!aligned16(A) || !aligned16(B) || (M > 1 && lda % (fa == FP8DS_E2M1 ? 32 : 16)) ||
+                (N > 1 && ldb % 32)))
+    return fail(FP8DS_ERR_ALIGN, "%s: the rows of A and B must be 16-byte aligned", who);
+  if (reinterpret_cast<uintptr_t>(C) % esz)
+    return fail(FP8DS_ERR_ALIGN, "%s: C is not aligned to its elements", who);
+  hipError_t e = hipSuccess;
+  if (amax_c) e = fp8ds::launch_prologue(1, nullptr, nullptr, amax_c, nullptr, stream);
+  if (e == hipSuccess) {
+    fp8ds::Mxfp4Gemm p;
+    p.M = M; p.N = N; p.K = K;
+    p.A = A; p.lda = lda; p.sc_a = scales_a; p.ldsa = ld_scales_a;
+    p.B = B; p.ldb = ldb; p.sc_b = scales_b; p.ldsb = ld_scales_b;
+    p.C = C; p.out_bf16 = ct == FP8DS_BF16; p.ldc = ldc; p.amax_c = amax_c;
+    e = fp8ds::launch_gemm_mxfp4(p, (int)fa, num_cus(), stream);
   }
   return hip_status(e, who);
 }

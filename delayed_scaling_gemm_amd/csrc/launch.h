@@ -62,6 +62,7 @@ struct AdamWLaunch {
   uint8_t* qt;             // or null: no transposed copy (requires q)
   float* amax;             // or null; reset by launch_prologue
   uint64_t* sat;           // or null; reset by launch_prologue
+  const float* grad_coef = nullptr;  // or null: device factor that multiplies c.grad_scale
 };
 hipError_t launch_adamw(const AdamWLaunch& a, hipStream_t stream);
 
@@ -159,5 +160,111 @@ hipError_t launch_mx_cast(const void* x, bool bf16, int64_t n, int fmt, uint8_t*
 hipError_t launch_mx_cast_transpose(const void* x, bool bf16, int64_t rows, int64_t cols, int fmt,
                                     uint8_t* q, uint8_t* scales, uint8_t* qt, uint8_t* scales_t,
                                     hipStream_t stream);
+
+// RMSNorm of rows (with the residual's addition) and its quantised output.
+struct NormArgs {
+  const void* x;         // [rows][ldx]
+  bool x_bf16;
+  const void* res;       // or null: [rows][ldr], of h's type
+  bool h_bf16;           // type of res and h (x's type where neither is given)
+  const void* gamma;     // [cols]
+  bool gamma_bf16;
+  int64_t rows, cols, ldx, ldr;
+  float eps;
+  void* h;               // or null: [rows][ldh]
+  int64_t ldh;
+  void* y;               // or null: [rows][ldy]
+  bool y_bf16;
+  int64_t ldy;
+  float* rstd;           // or null: [rows]
+  int mode;              // 0 none, 1 per-tensor scale, 2 per row, 3 blocks of 32
+  int fmt;
+  uint8_t* q;            // [rows][ldq bytes]
+  int64_t ldq;
+  const float* scale_in; // mode 1
+  float* scale_used;     // mode 1, or null
+  float* amax;           // mode 1: combined into; mode 2: [rows]; or null
+  uint64_t* sat;         // mode 1: added to; or null
+  float* scale_out;      // mode 2: [rows]
+  float* scale_inv;      // mode 2: [rows] or null
+  int margin;            // mode 2
+  uint8_t* mx_scales;    // mode 3: [rows][ldms]
+  int64_t ldms;
+  bool vec;              // every row 16-byte aligned and cols % 8 == 0
+};
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t stream);
+
+struct NormBwdArgs {
+  const void* dy;        // [rows][lddy]
+  bool x_bf16;           // dy's type
+  const void* h;         // [rows][ldh]
+  bool h_bf16;           // type of h, dres and dx
+  const void* dres;      // or null
+  const float* rstd;     // [rows]
+  const void* gamma;
+  bool gamma_bf16;
+  int64_t rows, cols, lddy, ldh, lddr, lddx, ldq;
+  void* dx;              // [rows][lddx]
+  float* dgamma;         // [cols]
+  float* work;           // [norm_bwd_parts][cols]
+  int fmt;
+  const float* scale_in; // with q
+  uint8_t* q;            // or null: [rows][ldq]
+  float* scale_used;     // or null
+  float* amax;           // or null: combined into
+  uint64_t* sat;         // or null: added to
+  bool vec;
+};
+int norm_bwd_parts(int64_t rows, int64_t cols);
+hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream);
+
+// Tensors of one launch of the gradient norm or the clip (kernel arguments: at most
+// 4 KB).  start[i]: the launch's first chunk of tensor i, start[count] their number.
+constexpr int kTensors = 128;
+struct TensorTable {
+  const void* src[kTensors];
+  void* dst[kTensors];
+  int64_t n[kTensors];
+  uint32_t start[kTensors + 1];
+  uint32_t src_bf16[kTensors / 32], dst_bf16[kTensors / 32];
+  int count;
+};
+int64_t table_chunks(int64_t n);  // chunks of a tensor of n elements
+// parts[b] for b < blocks: partial sums of squares.
+hipError_t launch_grad_norm_part(const TensorTable& tb, int blocks, double* parts,
+                                 hipStream_t stream);
+// The whole norm in one workgroup.
+hipError_t launch_grad_norm_single(const TensorTable& tb, float grad_scale, float max_norm,
+                                   float* norm, float* coef, hipStream_t stream);
+hipError_t launch_grad_norm_join(const double* parts, int n, float grad_scale, float max_norm,
+                                 float* norm, float* coef, hipStream_t stream);
+hipError_t launch_grad_clip(const TensorTable& tb, const float* coef, hipStream_t stream);
+
+// MXFP4 casts (n a multiple of 32; rows and cols multiples of 32) and back.
+hipError_t launch_mxfp4_cast(const void* x, bool bf16, int64_t n, uint8_t* q, uint8_t* scales,
+                             hipStream_t stream);
+hipError_t launch_mxfp4_cast_transpose(const void* x, bool bf16, int64_t rows, int64_t cols,
+                                       uint8_t* q, uint8_t* scales, uint8_t* qt, uint8_t* scales_t,
+                                       hipStream_t stream);
+hipError_t launch_mxfp4_dequant(const uint8_t* q, const uint8_t* scales, int64_t n, void* y,
+                                bool bf16, hipStream_t stream);
+
+// C = A B^T, B in MXFP4, A of format fa (E4M3, E5M2 or E2M1 = 2) with block scales.
+struct Mxfp4Gemm {
+  int64_t M, N, K;       // K a multiple of 32
+  const uint8_t* A;
+  int64_t lda;           // elements
+  const uint8_t* sc_a;
+  int64_t ldsa;
+  const uint8_t* B;
+  int64_t ldb;           // elements
+  const uint8_t* sc_b;
+  int64_t ldsb;
+  void* C;
+  bool out_bf16;
+  int64_t ldc;
+  float* amax_c;         // or null: combined into
+};
+hipError_t launch_gemm_mxfp4(const Mxfp4Gemm& p, int fa, int num_cus, hipStream_t stream);
 
 }  // namespace fp8ds

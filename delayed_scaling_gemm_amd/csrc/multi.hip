@@ -1,0 +1,259 @@
+// Global gradient norm over many tensors, and clipping.
+//
+// What is computed over the tensors g_t (BF16 or FP32, any sizes):
+//   norm = grad_scale * sqrt( sum_t sum_i g_t[i]^2 )
+//   coef = min(1, max_norm / (norm + 1e-6))
+//   out_t[i] = g_t[i] * coef                  (fp32 product, rounded to out_t's type)
+// (gradient clipping by the global norm, Pascanu, Mikolov & Bengio; the 1e-6 keeps
+// a zero norm from dividing by zero).
+//
+// The squares are added in 64 bits: an fp32 square is exact there, and neither 1e38
+// overflows nor 1e-38 underflows; conversion and fused multiply-add together run at
+// several times the rate at which HBM delivers elements, so it costs nothing.
+// Partial sums go to the workspace, one per workgroup, and are joined in a fixed
+// order by one more launch (or by the same one, where a single workgroup takes it
+// all): no atomics, the same gradients give the same bits.
+//
+// Design for gfx950: HBM-bound, each gradient read once by the norm and once by the
+// clip.  The tensors' addresses travel in the kernel arguments, kTensors of them per
+// launch, so a call reads no table from memory and keeps nothing between calls.
+// A launch's elements are cut into chunks of kChunk that never straddle tensors;
+// a workgroup takes consecutive chunks and finds its tensor by bisection.
+
+#include <math.h>
+
+#include "cast_common.h"
+#include "fp4_common.h"
+#include "launch.h"
+
+namespace fp8ds {
+
+constexpr int kChunk = 8192;  // elements
+
+// The table entry (tensor) of chunk c.
+__device__ __forceinline__ int find_tensor(const TensorTable& tb, uint32_t c) {
+  int lo = 0, hi = tb.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tb.start[mid] <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ bool table_bf16(const uint32_t* bits, int i) {
+  return (bits[i >> 5] >> (i & 31)) & 1u;
+}
+
+__device__ __forceinline__ void add_square(double& s, float v) {
+  const double d = (double)v;
+  s = fma(d, d, s);
+}
+
+// Squares of elements [b, e) of one tensor, spread over NT threads.
+template <int NT>
+__device__ __forceinline__ double sum_squares(const void* g, bool bf, int64_t b, int64_t e) {
+  double s0 = 0.0, s1 = 0.0;
+  const int esz = bf ? 2 : 4, per = 16 / esz;
+  if (((reinterpret_cast<uintptr_t>(g) + b * esz) & 15u) == 0) {
+    const u32x4* v = reinterpret_cast<const u32x4*>(static_cast<const char*>(g) + b * esz);
+    const int n = (int)((e - b) / per);  // whole 16-byte pieces
+    for (int i = threadIdx.x; i < n; i += 4 * NT) {
+      u32x4 d[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        d[k] = i + k * NT < n ? __builtin_nontemporal_load(v + i + k * NT) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          if (bf) {
+            add_square(s0, bf16_lo(d[k][w]));
+            add_square(s1, bf16_hi(d[k][w]));
+          } else {
+            add_square(w & 1 ? s1 : s0, __uint_as_float(d[k][w]));
+          }
+        }
+    }
+    b += (int64_t)n * per;
+  }
+  for (int64_t i = b + threadIdx.x; i < e; i += NT)
+    add_square(s0, bf ? __uint_as_float((uint32_t) static_cast<const uint16_t*>(g)[i] << 16)
+                      : static_cast<const float*>(g)[i]);
+  return s0 + s1;
+}
+
+// Sum over the workgroup (result in thread 0).
+template <int NT>
+__device__ __forceinline__ double block_sum(double v, double* red) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double t = 0.0;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < NT / 64; ++w) t += red[w];
+  return t;
+}
+
+__device__ __forceinline__ void write_norm(double sum, float grad_scale, float max_norm,
+                                           float* norm, float* coef) {
+  const double n = (double)grad_scale * sqrt(sum);
+  *norm = (float)n;
+  if (coef) {
+    const double c = (double)max_norm / (n + 1e-6);
+    *coef = (float)(c > 1.0 ? 1.0 : c);  // NaN stays NaN, an infinite norm gives 0
+  }
+}
+
+// parts != null: one partial sum per workgroup; else this workgroup is the only one
+// and finishes the norm.
+template <int NT>
+__global__ __launch_bounds__(NT) void grad_norm_kernel(TensorTable tb, double* parts,
+                                                       float grad_scale, float max_norm,
+                                                       float* norm, float* coef) {
+  __shared__ double red[NT / 64];
+  const uint32_t chunks = tb.start[tb.count];
+  const uint32_t per = (chunks + gridDim.x - 1) / gridDim.x;
+  uint32_t c = blockIdx.x * per;
+  const uint32_t ce = min(chunks, c + per);
+  double s = 0.0;
+  if (c < ce) {
+    int t = find_tensor(tb, c);
+    while (c < ce) {
+      while (tb.start[t + 1] <= c) ++t;  // tensors without elements have no chunk
+      const int64_t b = (int64_t)(c - tb.start[t]) * kChunk;
+      const int64_t last = (int64_t)(min(ce, tb.start[t + 1]) - tb.start[t]) * kChunk;
+      const int64_t e = last < tb.n[t] ? last : tb.n[t];
+      s += sum_squares<NT>(tb.src[t], table_bf16(tb.src_bf16, t), b, e);
+      c = min(ce, tb.start[t + 1]);
+    }
+  }
+  s = block_sum<NT>(s, red);
+  if (threadIdx.x == 0) {
+    if (parts) parts[blockIdx.x] = s;
+    else write_norm(s, grad_scale, max_norm, norm, coef);
+  }
+}
+
+__global__ __launch_bounds__(1024) void grad_norm_join_kernel(const double* parts, int n,
+                                                              float grad_scale, float max_norm,
+                                                              float* norm, float* coef) {
+  __shared__ double red[16];
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += 1024) s += parts[i];
+  s = block_sum<1024>(s, red);
+  if (threadIdx.x == 0) write_norm(s, grad_scale, max_norm, norm, coef);
+}
+
+// ------------------------------------------------------------------ clip
+
+__device__ __forceinline__ float elem(const void* g, bool bf, int64_t i) {
+  return bf ? __uint_as_float((uint32_t) static_cast<const uint16_t*>(g)[i] << 16)
+            : static_cast<const float*>(g)[i];
+}
+__device__ __forceinline__ void put(void* o, bool bf, int64_t i, float v) {
+  if (bf) static_cast<uint16_t*>(o)[i] = bf16_bits_rne(v);
+  else static_cast<float*>(o)[i] = v;
+}
+
+// One chunk; 4 elements per lane and step, so every instruction of a wave covers one
+// run whatever the two types.
+template <bool SBF, bool DBF>
+__device__ __forceinline__ void clip_quads(const void* g, void* o, int64_t b, int n, float c) {
+  const int q = n / 4;
+  for (int i = threadIdx.x; i < q; i += 4 * 256) {
+    float v[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i + 256 * k >= q) continue;
+      const int64_t at = b + 4 * (int64_t)(i + 256 * k);
+      if constexpr (SBF) {
+        const u32x2 d = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(g) + at));
+        v[k][0] = bf16_lo(d.x);
+        v[k][1] = bf16_hi(d.x);
+        v[k][2] = bf16_lo(d.y);
+        v[k][3] = bf16_hi(d.y);
+      } else {
+        const u32x4 d = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4*>(static_cast<const float*>(g) + at));
+#pragma unroll
+        for (int w = 0; w < 4; ++w) v[k][w] = __uint_as_float(d[w]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i + 256 * k >= q) continue;
+      const int64_t at = b + 4 * (int64_t)(i + 256 * k);
+      if constexpr (DBF) {
+        const u32x2 d = {bf16_pair_rne(v[k][0] * c, v[k][1] * c),
+                         bf16_pair_rne(v[k][2] * c, v[k][3] * c)};
+        __builtin_nontemporal_store(d, reinterpret_cast<u32x2*>(static_cast<uint16_t*>(o) + at));
+      } else {
+        u32x4 d;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) d[w] = __float_as_uint(v[k][w] * c);
+        __builtin_nontemporal_store(d, reinterpret_cast<u32x4*>(static_cast<float*>(o) + at));
+      }
+    }
+  }
+  for (int64_t i = b + 4 * q + threadIdx.x; i < b + n; i += 256)
+    put(o, DBF, i, elem(g, SBF, i) * c);
+}
+
+__global__ __launch_bounds__(256) void grad_clip_kernel(TensorTable tb, const float* coef) {
+  const float c = *coef;
+  const uint32_t chunk = blockIdx.x;
+  const int t = find_tensor(tb, chunk);
+  const void* g = tb.src[t];
+  void* o = tb.dst[t];
+  const bool sbf = table_bf16(tb.src_bf16, t), dbf = table_bf16(tb.dst_bf16, t);
+  if (c == 1.0f && g == o) return;  // in place, nothing to clip
+  const int64_t b = (int64_t)(chunk - tb.start[t]) * kChunk;
+  const int64_t left = tb.n[t] - b;
+  const int n = (int)(left < kChunk ? left : kChunk);
+  if (((reinterpret_cast<uintptr_t>(g) & (sbf ? 7u : 15u)) |
+       (reinterpret_cast<uintptr_t>(o) & (dbf ? 7u : 15u))) == 0) {
+    if (sbf && dbf) clip_quads<true, true>(g, o, b, n, c);
+    else if (sbf) clip_quads<true, false>(g, o, b, n, c);
+    else if (dbf) clip_quads<false, true>(g, o, b, n, c);
+    else clip_quads<false, false>(g, o, b, n, c);
+  } else {
+    for (int64_t i = b + threadIdx.x; i < b + n; i += 256) put(o, dbf, i, elem(g, sbf, i) * c);
+  }
+}
+
+// ------------------------------------------------------------------ host launchers
+
+int64_t table_chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
+
+hipError_t launch_grad_norm_part(const TensorTable& tb, int blocks, double* parts,
+                                 hipStream_t stream) {
+  hipLaunchKernelGGL((grad_norm_kernel<256>), dim3((unsigned)blocks), dim3(256), 0, stream, tb,
+                     parts, 1.0f, 0.0f, nullptr, nullptr);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_norm_single(const TensorTable& tb, float grad_scale, float max_norm,
+                                   float* norm, float* coef, hipStream_t stream) {
+  hipLaunchKernelGGL((grad_norm_kernel<1024>), dim3(1), dim3(1024), 0, stream, tb, nullptr,
+                     grad_scale, max_norm, norm, coef);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_norm_join(const double* parts, int n, float grad_scale, float max_norm,
+                                 float* norm, float* coef, hipStream_t stream) {
+  hipLaunchKernelGGL(grad_norm_join_kernel, dim3(1), dim3(1024), 0, stream, parts, n, grad_scale,
+                     max_norm, norm, coef);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_clip(const TensorTable& tb, const float* coef, hipStream_t stream) {
+  const uint32_t chunks = tb.start[tb.count];
+  if (chunks == 0) return hipSuccess;
+  hipLaunchKernelGGL(grad_clip_kernel, dim3(chunks), dim3(256), 0, stream, tb, coef);
+  return hipGetLastError();
+}
+
+}  // namespace fp8ds

@@ -1,0 +1,774 @@
+// RMSNorm with the residual's addition and an output in 8 (or 4) bits, forward
+// and backward.
+//
+// What is computed, per row of C elements:
+//   h = x + res            rounded to the residual's type when it is BF16: that is
+//                          the value the residual stream carries, and everything
+//                          below uses it, so the codes, rstd and the backward pass
+//                          are functions of what is stored
+//   r = 1 / sqrt(sum h^2 / C + eps)
+//   y = (h r) gamma
+// and from the fp32 y, without a rounding to 16 bits in between, the operand of the
+// next product: FP8 with a given (delayed) per-tensor scale, FP8 with a scale per
+// row, or blocks of 32 with E8M0 scales (FP8 or FP4 elements).  Sums are fp32: each
+// lane adds at most 64 squares in order, lanes are joined as a tree.
+// Backward, with xhat = h r and g = dy gamma:
+//   dx = r (g - xhat sum(g xhat) / C) + dres,   dgamma = sum over rows of dy xhat
+// (d r / d h_j = -r^3 h_j / C gives the middle term; dres is the gradient that
+// reaches h from above, and dx the gradient of both x and res).
+//
+// Design for gfx950: both directions are HBM-bound, so a row is read once and held
+// in registers between its reduction and its output.  TPR threads share a row (16,
+// 64, 256 or 1024, so that a thread holds 1 to 4 groups of 8 elements), and a
+// workgroup takes 256 / TPR rows.  A group of 8 consecutive elements per lane makes
+// 16-byte BF16 accesses; rows that are not 16-byte aligned, or are no multiple of 8
+// long, take the same kernel with consecutive lanes on consecutive elements.
+
+#include "cast_common.h"
+#include "fp4_common.h"
+#include "launch.h"
+
+namespace fp8ds {
+
+enum { kQNone = 0, kQTensor = 1, kQRow = 2, kQMx = 3 };
+
+template <bool BF>
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+  if constexpr (BF)
+    return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
+  else
+    return static_cast<const float*>(p)[i];
+}
+
+template <bool BF>
+__device__ __forceinline__ void store1(void* p, int64_t i, float v) {
+  if constexpr (BF)
+    static_cast<uint16_t*>(p)[i] = bf16_bits_rne(v);
+  else
+    static_cast<float*>(p)[i] = v;
+}
+
+template <bool BF>
+__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
+  if constexpr (BF) {
+    const u32x4 d = __builtin_nontemporal_load(
+        reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = bf16_lo(d[k]);
+      v[2 * k + 1] = bf16_hi(d[k]);
+    }
+  } else {
+    const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + i);
+    const u32x4 a = __builtin_nontemporal_load(s), b = __builtin_nontemporal_load(s + 1);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = __uint_as_float(a[k]);
+      v[4 + k] = __uint_as_float(b[k]);
+    }
+  }
+}
+
+template <bool BF>
+__device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
+  if constexpr (BF) {
+    u32x4 d;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) d[k] = bf16_pair_rne(v[2 * k], v[2 * k + 1]);
+    __builtin_nontemporal_store(d, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i));
+  } else {
+    u32x4 a, b;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a[k] = __float_as_uint(v[k]);
+      b[k] = __float_as_uint(v[4 + k]);
+    }
+    u32x4* s = reinterpret_cast<u32x4*>(static_cast<float*>(p) + i);
+    __builtin_nontemporal_store(a, s);
+    __builtin_nontemporal_store(b, s + 1);
+  }
+}
+
+// gamma is read by every row: an ordinary (cached) load.
+__device__ __forceinline__ void gamma8(const void* g, bool bf, int64_t i, float (&v)[8]) {
+  if (bf) {
+    const u32x4 d = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(g) + i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = bf16_lo(d[k]);
+      v[2 * k + 1] = bf16_hi(d[k]);
+    }
+  } else {
+    const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const float*>(g) + i);
+    const u32x4 a = s[0], b = s[1];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = __uint_as_float(a[k]);
+      v[4 + k] = __uint_as_float(b[k]);
+    }
+  }
+}
+__device__ __forceinline__ float gamma1(const void* g, bool bf, int64_t i) {
+  return bf ? load1<true>(g, i) : load1<false>(g, i);
+}
+
+// Sum over the TPR threads of a row; every thread gets it.  TPR > 64: through LDS
+// (`red`: one word per wave; two barriers keep successive calls apart).
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+#pragma unroll
+  for (int o = (TPR < 64 ? TPR : 64) / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  if constexpr (TPR > 64) {
+    constexpr int NW = TPR / 64;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) t += red[w];
+    __syncthreads();
+    v = t;
+  }
+  return v;
+}
+
+template <int TPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
+#pragma unroll
+  for (int o = (TPR < 64 ? TPR : 64) / 2; o > 0; o >>= 1)
+    v = max(v, (uint32_t)__shfl_xor((int)v, o, 64));
+  if constexpr (TPR > 64) {
+    constexpr int NW = TPR / 64;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    uint32_t t = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) t = max(t, red[w]);
+    __syncthreads();
+    v = t;
+  }
+  return v;
+}
+
+// 1 / sqrt(ss / C + eps), each operation correctly rounded.
+__device__ __forceinline__ float norm_rstd(float ss, int64_t C, float eps) {
+  return __fdiv_rn(1.0f, __builtin_sqrtf(__fdiv_rn(ss, (float)C) + eps));
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// Eight FP8 codes of v s (bytes in order), and what they add to the saturation count.
+__device__ __forceinline__ u32x2 codes8(const float (&v)[8], float s, bool e5m2, uint32_t& sat,
+                                        bool want_sat) {
+  float t[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) t[k] = v[k] * s;
+  if (e5m2) {
+    if (want_sat) sat += sat4<kE5M2>(t[0], t[1], t[2], t[3]) + sat4<kE5M2>(t[4], t[5], t[6], t[7]);
+    return u32x2{encode4<kE5M2>(t[0], t[1], t[2], t[3]), encode4<kE5M2>(t[4], t[5], t[6], t[7])};
+  }
+  if (want_sat) sat += sat4<kE4M3>(t[0], t[1], t[2], t[3]) + sat4<kE4M3>(t[4], t[5], t[6], t[7]);
+  return u32x2{encode4<kE4M3>(t[0], t[1], t[2], t[3]), encode4<kE4M3>(t[4], t[5], t[6], t[7])};
+}
+__device__ __forceinline__ uint32_t code1(float t, bool e5m2) {
+  return e5m2 ? encode_fp8<kE5M2>(t) : encode_fp8<kE4M3>(t);
+}
+__device__ __forceinline__ uint32_t sat1(float t, bool e5m2) {
+  return (uint32_t)(fabsf(t) > (e5m2 ? FmtTraits<kE5M2>::kMax : FmtTraits<kE4M3>::kMax));
+}
+
+// Commit of a workgroup's amax bits and saturation count for any thread count.
+__device__ __forceinline__ void commit(uint32_t amax, uint32_t sat, float* g_amax, uint64_t* g_sat,
+                                       uint32_t* smem) {
+  Health h;
+  block_commit<false>(amax, sat, h, reinterpret_cast<uint32_t*>(g_amax),
+                      reinterpret_cast<unsigned long long*>(g_sat), nullptr, smem);
+}
+
+// ------------------------------------------------------------------ forward
+
+template <bool XBF, bool HBF, int TPR, int VPT, int MODE, bool VEC>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArgs p) {
+  constexpr int NT = TPR > 256 ? TPR : 256;
+  constexpr int RPB = NT / TPR;
+  __shared__ uint32_t red[2 * (NT / 64)];
+  const int t = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  const bool live = row < p.rows;
+  const int64_t C = p.cols;
+  // element k of group j of this thread
+  auto col = [&](int j, int k) -> int64_t {
+    return VEC ? ((int64_t)t + TPR * j) * 8 + k : (int64_t)(j * 8 + k) * TPR + t;
+  };
+  const int64_t ox = row * p.ldx, orr = row * p.ldr, oh = row * p.ldh;
+  float h[VPT][8];
+  if constexpr (VEC) {
+    float r[VPT][8];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const bool in = live && col(j, 0) < C;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[j][k] = r[j][k] = 0.0f;
+      if (in) load8<XBF>(p.x, ox + col(j, 0), h[j]);
+      if (in && p.res) load8<HBF>(p.res, orr + col(j, 0), r[j]);
+    }
+    if (p.res) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          h[j][k] += r[j][k];
+          if constexpr (HBF) h[j][k] = bf16_round(h[j][k]);
+        }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        h[j][k] = 0.0f;
+        if (live && col(j, k) < C) {
+          h[j][k] = load1<XBF>(p.x, ox + col(j, k));
+          if (p.res) {
+            h[j][k] += load1<HBF>(p.res, orr + col(j, k));
+            if constexpr (HBF) h[j][k] = bf16_round(h[j][k]);
+          }
+        }
+      }
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss += h[j][k] * h[j][k];
+  if (p.h) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if constexpr (VEC) {
+        if (live && col(j, 0) < C) store8<HBF>(p.h, oh + col(j, 0), h[j]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (live && col(j, k) < C) store1<HBF>(p.h, oh + col(j, k), h[j][k]);
+      }
+    }
+  }
+  ss = row_sum<TPR>(ss, reinterpret_cast<float*>(red));
+  const float rstd = norm_rstd(ss, C, p.eps);
+  if (p.rstd && live && t == 0) p.rstd[row] = rstd;
+  // y in place of h
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    if constexpr (VEC) {
+      if (live && col(j, 0) < C) {
+        float g[8];
+        gamma8(p.gamma, p.gamma_bf16, col(j, 0), g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[j][k] = (h[j][k] * rstd) * g[k];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (live && col(j, k) < C)
+          h[j][k] = (h[j][k] * rstd) * gamma1(p.gamma, p.gamma_bf16, col(j, k));
+    }
+  }
+  if (p.y) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if constexpr (VEC) {
+        if (live && col(j, 0) < C) {
+          if (p.y_bf16)
+            store8<true>(p.y, row * p.ldy + col(j, 0), h[j]);
+          else
+            store8<false>(p.y, row * p.ldy + col(j, 0), h[j]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (live && col(j, k) < C) {
+            if (p.y_bf16)
+              store1<true>(p.y, row * p.ldy + col(j, k), h[j][k]);
+            else
+              store1<false>(p.y, row * p.ldy + col(j, k), h[j][k]);
+          }
+      }
+    }
+  }
+  if constexpr (MODE == kQNone) return;
+  const bool e5m2 = p.fmt == kE5M2;
+  if constexpr (MODE == kQTensor || MODE == kQRow) {
+    uint32_t amax = 0, sat = 0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) amax = max(amax, abs_bits(h[j][k]));
+    float s;
+    if constexpr (MODE == kQTensor) {
+      s = *p.scale_in;
+      if (p.scale_used && blockIdx.x == 0 && threadIdx.x == 0) *p.scale_used = s;
+    } else {
+      amax = canonical_amax_bits(row_max<TPR>(amax, red));
+      s = scale_from_amax(__uint_as_float(amax), e5m2 ? FmtTraits<kE5M2>::kMax : FmtTraits<kE4M3>::kMax,
+                          p.margin);
+      if (live && t == 0) {
+        p.scale_out[row] = s;
+        if (p.scale_inv) p.scale_inv[row] = __fdiv_rn(1.0f, s);
+        if (p.amax) p.amax[row] = __uint_as_float(amax);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      if constexpr (VEC) {
+        if (live && col(j, 0) < C) {
+          const u32x2 c = codes8(h[j], s, e5m2, sat, MODE == kQTensor && p.sat);
+          __builtin_nontemporal_store(c, reinterpret_cast<u32x2*>(p.q + row * p.ldq + col(j, 0)));
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (live && col(j, k) < C) {
+            const float v = h[j][k] * s;
+            p.q[row * p.ldq + col(j, k)] = (uint8_t)code1(v, e5m2);
+            if (MODE == kQTensor && p.sat) sat += sat1(v, e5m2);
+          }
+      }
+    }
+    if constexpr (MODE == kQTensor) commit(amax, sat, p.amax, p.sat, red);
+  } else if constexpr (MODE == kQMx) {
+    // a block of 32 is 4 consecutive lanes (VEC only; C is a multiple of 32)
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) a = max(a, abs_bits(h[j][k]));
+      a = max(a, (uint32_t)__shfl_xor((int)a, 1));
+      a = max(a, (uint32_t)__shfl_xor((int)a, 2));
+      const int64_t c0 = col(j, 0);
+      if (!live || c0 >= C) continue;
+      const uint32_t code = mx_code(a, p.fmt == kE2M1 ? 2u : e5m2 ? 15u : 8u);
+      if ((t & 3) == 0) p.mx_scales[row * p.ldms + c0 / 32] = (uint8_t)code;
+      if (p.fmt == kE2M1) {
+        const uint32_t c = code == 255u ? kFp4NanBlock : fp4_codes8(h[j], code);
+        *reinterpret_cast<uint32_t*>(p.q + row * p.ldq + c0 / 2) = c;
+      } else {
+        u32x2 c = {0x7F7F7F7Fu, 0x7F7F7F7Fu};
+        uint32_t unused = 0;
+        if (code != 255u) c = codes8(h[j], __uint_as_float((254u - code) << 23), e5m2, unused, false);
+        __builtin_nontemporal_store(c, reinterpret_cast<u32x2*>(p.q + row * p.ldq + c0));
+      }
+    }
+  }
+}
+
+// Rows longer than a workgroup's registers hold: one workgroup per row passes over
+// it two or three times (sum of squares; row amax; output).  h is taken back from
+// p.h where it is stored, since p.h may be the residual's own buffer.
+template <bool XBF, bool HBF, int MODE>
+__global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormArgs p) {
+  __shared__ uint32_t red[2 * 16];
+  const int t = threadIdx.x;
+  const int64_t row = blockIdx.x, C = p.cols;
+  const int64_t ox = row * p.ldx, orr = row * p.ldr, oh = row * p.ldh;
+  auto fresh = [&](int64_t c) {
+    float v = load1<XBF>(p.x, ox + c);
+    if (p.res) {
+      v += load1<HBF>(p.res, orr + c);
+      if constexpr (HBF) v = bf16_round(v);
+    }
+    return v;
+  };
+  float ss = 0.0f;
+  for (int64_t c = t; c < C; c += 1024) {
+    const float v = fresh(c);
+    ss += v * v;
+    if (p.h) store1<HBF>(p.h, oh + c, v);
+  }
+  ss = row_sum<1024>(ss, reinterpret_cast<float*>(red));
+  const float rstd = norm_rstd(ss, C, p.eps);
+  if (p.rstd && t == 0) p.rstd[row] = rstd;
+  auto value = [&](int64_t c) {
+    const float v = p.h ? load1<HBF>(p.h, oh + c) : fresh(c);
+    return (v * rstd) * gamma1(p.gamma, p.gamma_bf16, c);
+  };
+  const bool e5m2 = p.fmt == kE5M2;
+  uint32_t amax = 0, sat = 0;
+  float s = 1.0f;
+  if constexpr (MODE == kQTensor) {
+    s = *p.scale_in;
+    if (p.scale_used && row == 0 && t == 0) *p.scale_used = s;
+  }
+  if constexpr (MODE == kQRow) {
+    for (int64_t c = t; c < C; c += 1024) amax = max(amax, abs_bits(value(c)));
+    amax = canonical_amax_bits(row_max<1024>(amax, red));
+    s = scale_from_amax(__uint_as_float(amax),
+                        e5m2 ? FmtTraits<kE5M2>::kMax : FmtTraits<kE4M3>::kMax, p.margin);
+    if (t == 0) {
+      p.scale_out[row] = s;
+      if (p.scale_inv) p.scale_inv[row] = __fdiv_rn(1.0f, s);
+      if (p.amax) p.amax[row] = __uint_as_float(amax);
+    }
+  }
+  // the lanes of a block of 32 stay together: C is a multiple of 32 with kQMx, and a
+  // wave's 64 lanes hold two whole blocks
+  for (int64_t c = t; c < C; c += 1024) {
+    const float v = value(c);
+    if (p.y) {
+      if (p.y_bf16)
+        store1<true>(p.y, row * p.ldy + c, v);
+      else
+        store1<false>(p.y, row * p.ldy + c, v);
+    }
+    if constexpr (MODE == kQTensor) amax = max(amax, abs_bits(v));
+    if constexpr (MODE == kQTensor || MODE == kQRow) {
+      p.q[row * p.ldq + c] = (uint8_t)code1(v * s, e5m2);
+      if (MODE == kQTensor && p.sat) sat += sat1(v * s, e5m2);
+    }
+    if constexpr (MODE == kQMx) {
+      uint32_t a = abs_bits(v);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) a = max(a, (uint32_t)__shfl_xor((int)a, o));
+      const uint32_t code = mx_code(a, p.fmt == kE2M1 ? 2u : e5m2 ? 15u : 8u);
+      if ((t & 31) == 0) p.mx_scales[row * p.ldms + c / 32] = (uint8_t)code;
+      const float m = __uint_as_float(code == 255u ? 0x3F800000u : (254u - code) << 23);
+      if (p.fmt == kE2M1) {
+        const uint32_t c4 = code == 255u ? (kFp4NanBlock & 15u) : fp4_code1(v * m);
+        const uint32_t up = (uint32_t)__shfl_xor((int)c4, 1);
+        if ((t & 1) == 0) p.q[row * p.ldq + c / 2] = (uint8_t)(c4 | (up << 4));
+      } else {
+        p.q[row * p.ldq + c] = code == 255u ? 0x7Fu : (uint8_t)code1(v * m, e5m2);
+      }
+    }
+  }
+  if constexpr (MODE == kQTensor) commit(amax, sat, p.amax, p.sat, red);
+}
+
+// ------------------------------------------------------------------ backward
+
+// A workgroup takes rows blockIdx.x * RPB + slot, then gridDim.x * RPB further, and
+// keeps its share of dgamma in registers: partial [gridDim.x][C] in `work`, summed by
+// norm_dgamma_kernel in a fixed order (no atomics: the same inputs give the same
+// bits).
+template <bool XBF, bool HBF, int TPR, int VPT, bool VEC>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwdArgs p) {
+  constexpr int NT = TPR > 256 ? TPR : 256;
+  constexpr int RPB = NT / TPR;
+  __shared__ uint32_t red[2 * (NT / 64)];
+  __shared__ float dg_lds[RPB > 1 ? TPR * VPT * 8 : 1];
+  const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+  const int64_t C = p.cols;
+  auto col = [&](int j, int k) -> int64_t {
+    return VEC ? ((int64_t)t + TPR * j) * 8 + k : (int64_t)(j * 8 + k) * TPR + t;
+  };
+  const bool e5m2 = p.fmt == kE5M2;
+  float s = 1.0f;
+  if (p.q) {
+    s = *p.scale_in;
+    if (p.scale_used && blockIdx.x == 0 && threadIdx.x == 0) *p.scale_used = s;
+  }
+  float acc[VPT][8];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[j][k] = 0.0f;
+  uint32_t amax = 0, sat = 0;
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.rows; r0 += step) {
+    const int64_t row = r0 + slot;
+    const bool live = row < p.rows;
+    float xh[VPT][8], g[VPT][8], dr[VPT][8];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) xh[j][k] = g[j][k] = dr[j][k] = 0.0f;
+      if constexpr (VEC) {
+        if (live && col(j, 0) < C) {
+          load8<HBF>(p.h, row * p.ldh + col(j, 0), xh[j]);
+          load8<XBF>(p.dy, row * p.lddy + col(j, 0), g[j]);
+          if (p.dres) load8<HBF>(p.dres, row * p.lddr + col(j, 0), dr[j]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (live && col(j, k) < C) {
+            xh[j][k] = load1<HBF>(p.h, row * p.ldh + col(j, k));
+            g[j][k] = load1<XBF>(p.dy, row * p.lddy + col(j, k));
+            if (p.dres) dr[j][k] = load1<HBF>(p.dres, row * p.lddr + col(j, k));
+          }
+      }
+    }
+    const float rstd = live ? p.rstd[row] : 0.0f;
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      float gm[8];
+      if constexpr (VEC) {
+        if (col(j, 0) < C) {
+          gamma8(p.gamma, p.gamma_bf16, col(j, 0), gm);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) gm[k] = 0.0f;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          gm[k] = col(j, k) < C ? gamma1(p.gamma, p.gamma_bf16, col(j, k)) : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        xh[j][k] *= rstd;
+        acc[j][k] += g[j][k] * xh[j][k];
+        g[j][k] *= gm[k];
+        dot += g[j][k] * xh[j][k];
+      }
+    }
+    const float mean = row_sum<TPR>(dot, reinterpret_cast<float*>(red)) / (float)C;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) g[j][k] = rstd * (g[j][k] - xh[j][k] * mean) + dr[j][k];
+      if constexpr (VEC) {
+        if (live && col(j, 0) < C) {
+          store8<HBF>(p.dx, row * p.lddx + col(j, 0), g[j]);
+          if (p.q) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) amax = max(amax, abs_bits(g[j][k]));
+            const u32x2 c = codes8(g[j], s, e5m2, sat, p.sat != nullptr);
+            __builtin_nontemporal_store(c, reinterpret_cast<u32x2*>(p.q + row * p.ldq + col(j, 0)));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (live && col(j, k) < C) {
+            store1<HBF>(p.dx, row * p.lddx + col(j, k), g[j][k]);
+            if (p.q) {
+              amax = max(amax, abs_bits(g[j][k]));
+              p.q[row * p.ldq + col(j, k)] = (uint8_t)code1(g[j][k] * s, e5m2);
+              if (p.sat) sat += sat1(g[j][k] * s, e5m2);
+            }
+          }
+      }
+    }
+  }
+  // dgamma: the slots of a workgroup one after the other, then one partial row
+  float* out = p.work + (int64_t)blockIdx.x * C;
+  if constexpr (RPB > 1) {
+    for (int w = 0; w < RPB; ++w) {
+      if (slot == w) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float* d = &dg_lds[(j * 8 + k) * TPR + t];
+            *d = w == 0 ? acc[j][k] : *d + acc[j][k];
+          }
+      }
+      __syncthreads();
+    }
+    if (slot == 0) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (col(j, k) < C) out[col(j, k)] = dg_lds[(j * 8 + k) * TPR + t];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (col(j, k) < C) out[col(j, k)] = acc[j][k];
+  }
+  if (p.q) commit(amax, sat, p.amax, p.sat, red);
+}
+
+// Rows longer than the registers: one workgroup walks its rows, each read twice; its
+// dgamma partial is kept in `work` (each element by one thread).
+template <bool XBF, bool HBF>
+__global__ __launch_bounds__(1024) void norm_bwd_long_kernel(NormBwdArgs p) {
+  __shared__ uint32_t red[2 * 16];
+  const int t = threadIdx.x;
+  const int64_t C = p.cols;
+  const bool e5m2 = p.fmt == kE5M2;
+  float s = 1.0f;
+  if (p.q) {
+    s = *p.scale_in;
+    if (p.scale_used && blockIdx.x == 0 && t == 0) *p.scale_used = s;
+  }
+  float* out = p.work + (int64_t)blockIdx.x * C;
+  uint32_t amax = 0, sat = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const float rstd = p.rstd[row];
+    float dot = 0.0f;
+    for (int64_t c = t; c < C; c += 1024) {
+      const float xh = load1<HBF>(p.h, row * p.ldh + c) * rstd;
+      const float dy = load1<XBF>(p.dy, row * p.lddy + c);
+      dot += dy * gamma1(p.gamma, p.gamma_bf16, c) * xh;
+      out[c] = dy * xh + (row == (int64_t)blockIdx.x ? 0.0f : out[c]);
+    }
+    const float mean = row_sum<1024>(dot, reinterpret_cast<float*>(red)) / (float)C;
+    for (int64_t c = t; c < C; c += 1024) {
+      const float xh = load1<HBF>(p.h, row * p.ldh + c) * rstd;
+      const float g = load1<XBF>(p.dy, row * p.lddy + c) * gamma1(p.gamma, p.gamma_bf16, c);
+      float d = rstd * (g - xh * mean);
+      if (p.dres) d += load1<HBF>(p.dres, row * p.lddr + c);
+      store1<HBF>(p.dx, row * p.lddx + c, d);
+      if (p.q) {
+        amax = max(amax, abs_bits(d));
+        p.q[row * p.ldq + c] = (uint8_t)code1(d * s, e5m2);
+        if (p.sat) sat += sat1(d * s, e5m2);
+      }
+    }
+  }
+  if (p.q) commit(amax, sat, p.amax, p.sat, red);
+}
+
+// dgamma[c] = sum of `parts` partial rows: 32 columns x 16 shares of the rows per
+// workgroup, joined in LDS in a fixed order.
+__global__ __launch_bounds__(512) void norm_dgamma_kernel(const float* __restrict__ work, int parts,
+                                                          int64_t C, float* __restrict__ dgamma) {
+  __shared__ float part[16][33];
+  const int cl = threadIdx.x & 31, sh = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + cl;
+  float v = 0.0f;
+  if (c < C) {
+#pragma unroll 4
+    for (int i = sh; i < parts; i += 16) v += work[(int64_t)i * C + c];
+  }
+  part[sh][cl] = v;
+  __syncthreads();
+  if (sh == 0 && c < C) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += part[i][cl];
+    dgamma[c] = t;
+  }
+}
+
+// ------------------------------------------------------------------ host launchers
+
+// Threads per row and groups of 8 per thread.  Few threads per row keep small rows
+// from leaving lanes idle; with few rows, 1024 threads share a long row so that its
+// loads are all in flight at once.
+struct RowShape {
+  int tpr, vpt;  // vpt 0: the long-row kernel
+};
+static RowShape row_shape(int64_t rows, int64_t cols) {
+  const int64_t g = (cols + 7) / 8;
+  if (g <= 16) return {16, 1};
+  if (g <= 64) return {64, 1};
+  if (g <= 128) return {64, 2};
+  if (g <= 256) return {256, 1};
+  if (g <= 512) return {256, 2};
+  if (g <= 1024) return rows >= 512 ? RowShape{256, 4} : RowShape{1024, 1};
+  if (g <= 2048) return {1024, 2};
+  if (g <= 4096) return {1024, 4};
+  return {1024, 0};
+}
+
+template <bool XBF, bool HBF, int MODE, bool VEC>
+static hipError_t launch_fwd(const NormArgs& a, RowShape sh, hipStream_t stream) {
+#define FP8DS_NORM_CASE(T, V)                                                                    \
+  if (sh.tpr == T && sh.vpt == V) {                                                              \
+    const int rpb = T > 256 ? 1 : 256 / T;                                                       \
+    hipLaunchKernelGGL((norm_fwd_kernel<XBF, HBF, T, V, MODE, VEC>),                              \
+                       dim3((unsigned)((a.rows + rpb - 1) / rpb)), dim3(T > 256 ? T : 256), 0,   \
+                       stream, a);                                                               \
+    return hipGetLastError();                                                                    \
+  }
+  FP8DS_NORM_CASE(16, 1)
+  FP8DS_NORM_CASE(64, 1)
+  FP8DS_NORM_CASE(64, 2)
+  FP8DS_NORM_CASE(256, 1)
+  FP8DS_NORM_CASE(256, 2)
+  FP8DS_NORM_CASE(256, 4)
+  FP8DS_NORM_CASE(1024, 1)
+  FP8DS_NORM_CASE(1024, 2)
+  FP8DS_NORM_CASE(1024, 4)
+#undef FP8DS_NORM_CASE
+  hipLaunchKernelGGL((norm_fwd_long_kernel<XBF, HBF, MODE>), dim3((unsigned)a.rows), dim3(1024), 0,
+                     stream, a);
+  return hipGetLastError();
+}
+
+template <bool XBF, bool HBF>
+static hipError_t launch_fwd_t(const NormArgs& a, RowShape sh, hipStream_t s) {
+  switch (a.mode) {
+    case kQNone: return a.vec ? launch_fwd<XBF, HBF, kQNone, true>(a, sh, s)
+                              : launch_fwd<XBF, HBF, kQNone, false>(a, sh, s);
+    case kQTensor: return a.vec ? launch_fwd<XBF, HBF, kQTensor, true>(a, sh, s)
+                                : launch_fwd<XBF, HBF, kQTensor, false>(a, sh, s);
+    case kQRow: return a.vec ? launch_fwd<XBF, HBF, kQRow, true>(a, sh, s)
+                             : launch_fwd<XBF, HBF, kQRow, false>(a, sh, s);
+    default: return launch_fwd<XBF, HBF, kQMx, true>(a, sh, s);
+  }
+}
+
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t stream) {
+  const RowShape sh = row_shape(a.rows, a.cols);
+  if (a.x_bf16 && a.h_bf16) return launch_fwd_t<true, true>(a, sh, stream);
+  if (a.x_bf16) return launch_fwd_t<true, false>(a, sh, stream);
+  return launch_fwd_t<false, false>(a, sh, stream);
+}
+
+// The backward pass holds four values per element: 512 threads, whose waves may have
+// 256 registers, take up to 16384 columns; 1024 threads (128 registers) would spill.
+static RowShape bwd_shape(int64_t cols) {
+  const int64_t g = (cols + 7) / 8;
+  if (g <= 1024) return row_shape(1 << 20, cols);
+  if (g <= 2048) return {512, 4};
+  return {1024, 0};
+}
+
+// Workgroups of the backward pass: at most 1024, so that the dgamma partials stay a
+// small part of the traffic.
+int norm_bwd_parts(int64_t rows, int64_t cols) {
+  const RowShape sh = bwd_shape(cols);
+  const int64_t rpb = sh.tpr > 256 ? 1 : 256 / sh.tpr;
+  const int64_t blocks = (rows + rpb - 1) / rpb;
+  return (int)(blocks < 1024 ? blocks : 1024);
+}
+
+template <bool XBF, bool HBF, bool VEC>
+static hipError_t launch_bwd(const NormBwdArgs& a, RowShape sh, int parts, hipStream_t stream) {
+#define FP8DS_NORM_CASE(T, V)                                                                     \
+  if (sh.tpr == T && sh.vpt == V) {                                                               \
+    hipLaunchKernelGGL((norm_bwd_kernel<XBF, HBF, T, V, VEC>), dim3((unsigned)parts),             \
+                       dim3(T > 256 ? T : 256), 0, stream, a);                                    \
+    return hipGetLastError();                                                                     \
+  }
+  FP8DS_NORM_CASE(16, 1)
+  FP8DS_NORM_CASE(64, 1)
+  FP8DS_NORM_CASE(64, 2)
+  FP8DS_NORM_CASE(256, 1)
+  FP8DS_NORM_CASE(256, 2)
+  FP8DS_NORM_CASE(256, 4)
+  FP8DS_NORM_CASE(512, 4)
+#undef FP8DS_NORM_CASE
+  hipLaunchKernelGGL((norm_bwd_long_kernel<XBF, HBF>), dim3((unsigned)parts), dim3(1024), 0, stream,
+                     a);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
+  const RowShape sh = bwd_shape(a.cols);
+  const int parts = norm_bwd_parts(a.rows, a.cols);
+  hipError_t e = hipSuccess;
+  if (parts > 0) {
+    if (a.x_bf16 && a.h_bf16)
+      e = a.vec ? launch_bwd<true, true, true>(a, sh, parts, stream)
+                : launch_bwd<true, true, false>(a, sh, parts, stream);
+    else if (a.x_bf16)
+      e = a.vec ? launch_bwd<true, false, true>(a, sh, parts, stream)
+                : launch_bwd<true, false, false>(a, sh, parts, stream);
+    else
+      e = a.vec ? launch_bwd<false, false, true>(a, sh, parts, stream)
+                : launch_bwd<false, false, false>(a, sh, parts, stream);
+  }
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((a.cols + 31) / 32)), dim3(512), 0, stream,
+                     a.work, parts, a.cols, a.dgamma);
+  return hipGetLastError();
+}
+
+}  // namespace fp8ds

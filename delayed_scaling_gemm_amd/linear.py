@@ -32,9 +32,10 @@ from __future__ import annotations
 
 import torch
 
-from . import (ALGO_MAX, E4M3, E5M2, HEALTH_COUNTS, HEALTH_NAMES, MMA_EXACT, MMA_FP8, OP_N, OP_T,
-               fp8ds_adamw, fp8ds_cast_acc, fp8ds_cast_health, fp8ds_cast_mx, fp8ds_gemm,
-               fp8ds_gemm_acc, fp8ds_gemm_mx, fp8ds_scale_update, fp8ds_scale_update_clear)
+from . import (ALGO_MAX, E2M1, E4M3, E5M2, HEALTH_COUNTS, HEALTH_NAMES, MMA_EXACT, MMA_FP8, OP_N,
+               OP_T, fp8ds_adamw, fp8ds_cast_acc, fp8ds_cast_health, fp8ds_cast_mx,
+               fp8ds_cast_mxfp4, fp8ds_gemm, fp8ds_gemm_acc, fp8ds_gemm_mx, fp8ds_gemm_mxfp4,
+               fp8ds_scale_update, fp8ds_scale_update_clear)
 
 X, W, DY = 0, 1, 2
 # shortest forward reduction that runs on the FP8 matrix instructions by default
@@ -252,7 +253,7 @@ class DelayedScalingLinear:
         return out
 
     def adamw_step(self, w, m, v, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0,
-                   grad_scale=1.0, stream=None):
+                   grad_scale=1.0, stream=None, grad_coef=None, grad_norm=None):
         """Fused AdamW on the fp32 master weights ``w`` [in, out] and moments ``m``,
         ``v`` with the dW of the last :meth:`step` (step count ``step`` >= 1).
 
@@ -262,7 +263,11 @@ class DelayedScalingLinear:
         FP8 训练与优化器 Kernel" §FP8 训练主路径图: fused optimizer -> master weight ->
         cast to FP8).  The result is bit-identical to updating ``w`` and casting it
         at the start of the next step.  A non-finite dW amax skips the update
-        (weights and moments stay; their FP8 copy is still made)."""
+        (weights and moments stay; their FP8 copy is still made).
+
+        ``grad_coef`` (device scalar of :func:`fp8ds_grad_norm`) clips the gradient;
+        with ``grad_norm``, the norm of the same call, it is that norm's finiteness and
+        not this dW's that decides, so that one bad tensor skips every layer's step."""
         dw = self._bufs.get("dw")
         if dw is None or tuple(dw.shape) != tuple(w.shape):
             raise RuntimeError("adamw_step needs the dW of a preceding fwd+bwd step of this shape")
@@ -275,9 +280,9 @@ class DelayedScalingLinear:
         s, su = self.scale, self.scale_used
         am, sat = self._amax_of(self._slot), self._sat_of(self._slot)
         fp8ds_adamw(w, dw, m, v, lr, beta1, beta2, eps, weight_decay, step, grad_scale=grad_scale,
-                    grad_amax=self.amax_dw, fmt=self.fmts[W], scale=s[W:W + 1], q=wq, q_t=wqt,
-                    scale_used=su[W:W + 1], amax=am[W:W + 1], sat_count=sat[W:W + 1],
-                    stream=stream)
+                    grad_amax=self.amax_dw if grad_norm is None else grad_norm, fmt=self.fmts[W],
+                    scale=s[W:W + 1], q=wq, q_t=wqt, scale_used=su[W:W + 1], amax=am[W:W + 1],
+                    sat_count=sat[W:W + 1], stream=stream, grad_coef=grad_coef)
         self._w_prepared = w
 
 
@@ -416,5 +421,86 @@ class MXLinear:
             dx, dw = self._buf("dx", (M, K), bf), self._buf("dw", (K, N), bf)
             self._gemm(M, K, N, dyq, dys, self.fmts[DY], wq, ws, self.fmts[W], dx, stream)
             self._gemm(K, N, M, xqt, xst, self.fmts[X], dyqt, dyst, self.fmts[DY], dw, stream)
+            out.update(dx=dx, dw=dw, dyq=dyq, dys=dys, dyqt=dyqt, dyst=dyst)
+        return out
+
+
+class MXFP4Linear:
+    """The Linear in MXFP4: every operand in blocks of 32 E2M1 elements along the
+    contraction, each with its E8M0 scale.
+
+    Training, :meth:`step`: X, W and dY are each cast once with their transposed copy
+    (fp8ds_cast_mxfp4), which gives each product both operands blocked along its own K:
+
+      Y  = X W        q of X,    q_t of W     K = in
+      dX = dY W^T     q of dY,   q of W       K = out
+      dW = X^T dY     q_t of X,  q_t of dY    K = tokens
+
+    tokens, in and out multiples of 32.  Serving: :meth:`quantize` keeps W's codes, then
+    :meth:`forward` takes any number of tokens, its activations in MXFP4 or, with
+    ``fmt`` E4M3 or E5M2, in MXFP8."""
+
+    def __init__(self, device="cuda"):
+        self.device = torch.device(device)
+        self._bufs = {}
+
+    def _buf(self, name, shape, dtype):
+        b = self._bufs.get(name)
+        if b is None or b.shape != shape or b.dtype != dtype:
+            b = torch.empty(shape, dtype=dtype, device=self.device)
+            self._bufs[name] = b
+        return b
+
+    def _cast(self, name, x, stream):
+        r, c = x.shape
+        u8 = torch.uint8
+        q, s = self._buf(name + "q", (r, c // 2), u8), self._buf(name + "s", (r, c // 32), u8)
+        qt, st = self._buf(name + "qt", (c, r // 2), u8), self._buf(name + "st", (c, r // 32), u8)
+        fp8ds_cast_mxfp4(x, q, s, qt, st, stream)
+        return q, s, qt, st
+
+    @staticmethod
+    def _gemm(m, n, k, a, sa, fa, b, sb, out, stream):
+        fp8ds_gemm_mxfp4(m, n, k, a, fa, k, sa, k // 32, b, k, sb, k // 32, out, n, None, stream)
+        return out
+
+    def quantize(self, w, stream=None):
+        """Keep the MXFP4 codes of ``w`` [in, out] for :meth:`forward`."""
+        self._cast("w", w, stream)
+        self.shape = tuple(w.shape)
+
+    def forward(self, x, fmt=E2M1, stream=None):
+        """y [tokens, out] BF16 of ``x`` [tokens, in] with the weights of :meth:`quantize`
+        (of the last :meth:`step` where that came later)."""
+        if "wqt" not in self._bufs:
+            raise RuntimeError("forward() needs the weights of a preceding quantize()")
+        K, N = self.shape
+        M = x.shape[0]
+        if x.shape[1] != K:
+            raise ValueError(f"x has {x.shape[1]} features, the weights {K}")
+        xq = self._buf("fq", (M, K // 2 if fmt == E2M1 else K), torch.uint8)
+        xs = self._buf("fs", (M, K // 32), torch.uint8)
+        if fmt == E2M1:
+            fp8ds_cast_mxfp4(x, xq, xs, stream=stream)
+        else:
+            fp8ds_cast_mx(x, fmt, xq, xs, stream=stream)
+        return self._gemm(M, N, K, xq, xs, fmt, self._bufs["wqt"], self._bufs["wst"],
+                          self._buf("fy", (M, N), torch.bfloat16), stream)
+
+    def step(self, x, w, dy=None, stream=None):
+        """x [M, K], w [K, N] (and dy [M, N]), BF16 or FP32 on the device.  Returns the BF16
+        outputs y (and dx, dw) and the MXFP4 copies of the inputs."""
+        (M, K), N = x.shape, w.shape[1]
+        bf = torch.bfloat16
+        xq, xs, xqt, xst = self._cast("x", x, stream)
+        wq, ws, wqt, wst = self._cast("w", w, stream)
+        self.shape = (K, N)
+        y = self._gemm(M, N, K, xq, xs, E2M1, wqt, wst, self._buf("y", (M, N), bf), stream)
+        out = {"y": y, "xq": xq, "xs": xs, "xqt": xqt, "xst": xst, "wq": wq, "ws": ws,
+               "wqt": wqt, "wst": wst}
+        if dy is not None:
+            dyq, dys, dyqt, dyst = self._cast("dy", dy, stream)
+            dx = self._gemm(M, K, N, dyq, dys, E2M1, wq, ws, self._buf("dx", (M, K), bf), stream)
+            dw = self._gemm(K, N, M, xqt, xst, E2M1, dyqt, dyst, self._buf("dw", (K, N), bf), stream)
             out.update(dx=dx, dw=dw, dyq=dyq, dys=dys, dyqt=dyqt, dyst=dyst)
         return out

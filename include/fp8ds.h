@@ -64,8 +64,10 @@ typedef enum {
 
 /* FP8 formats ([P2] §一 "FP8 格式设计"; [P3] §核心原理 "E4M3 与 E5M2 承担不同职责"):
  * E4M3: bias 7, largest finite 448, no infinity (OCP "fn" variant, [OCP]).
- * E5M2: bias 15, largest finite 57344, with +-inf ([OCP]). */
-typedef enum { FP8DS_E4M3 = 0, FP8DS_E5M2 = 1 } fp8ds_format;
+ * E5M2: bias 15, largest finite 57344, with +-inf ([OCP]).
+ * E2M1: the 4-bit element of MXFP4 (OCP Microscaling Formats): 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * and their negatives; accepted only where a call says so. */
+typedef enum { FP8DS_E4M3 = 0, FP8DS_E5M2 = 1, FP8DS_E2M1 = 2 } fp8ds_format;
 
 /* High-precision element types of inputs and GEMM outputs. */
 typedef enum { FP8DS_F32 = 0, FP8DS_BF16 = 1 } fp8ds_dtype;
@@ -530,6 +532,177 @@ int fp8ds_gemm_mx(int64_t M, int64_t N, int64_t K, const uint8_t* A, fp8ds_forma
                   const uint8_t* scales_a, int64_t ld_scales_a, const uint8_t* B, fp8ds_format fb,
                   int64_t ldb, const uint8_t* scales_b, int64_t ld_scales_b, void* C,
                   fp8ds_dtype ct, int64_t ldc, float* amax_c, fp8ds_mma mma, hipStream_t stream);
+
+/*
+ * RMSNorm with the residual's addition and a quantised output.  Per row:
+ *   h = x + residual   rounded to ht (the residual stream's type); h = x without residual
+ *   r = 1 / sqrt(sum_c h[c]^2 / cols + eps)          fp32 sums
+ *   y[c] = (h[c] * r) * gamma[c]                     fp32, from the rounded h
+ * and y, in fp32, is cast as the call says: the operand of the next product, with no
+ * 16-bit copy of y in between.  (Squares are fp32: |h| above 1e18 overflows them.)
+ *
+ * Arguments of the three calls:
+ *   x          device [rows x cols] of xt, rows ldx elements apart.
+ *   residual   device or NULL: [rows x cols] of ht, ldr apart.
+ *   gamma      device [cols] of gt.
+ *   eps        finite, >= 0.
+ *   h          device or NULL: [rows x cols] of ht, ldh apart: the new residual stream.
+ *              May be residual or x itself (same type, same leading dimension).
+ *   y          device or NULL: [rows x cols] of yt, ldy apart.
+ *   rstd       device or NULL: [rows], r (for the backward pass).
+ *   rows, cols >= 0 and < 2^31; any cols (fp8ds_rmsnorm_mx: a multiple of 32).  Leading
+ *              dimensions at least cols.  Matrices aligned to their elements; fastest
+ *              with 16-byte aligned rows (8 bytes for q) and cols a multiple of 8.
+ *   (xt, ht)   (BF16, BF16), (BF16, F32) or (F32, F32); (F32, BF16) is
+ *              FP8DS_ERR_UNSUPPORTED.
+ * No rows or no columns: nothing but *scale_used is written.
+ */
+
+/*
+ * fp8ds_rmsnorm -- y and / or its FP8 copy with a given per-tensor scale, as
+ * fp8ds_cast_acc casts: q = encode(y * (*scale)), amax and sat_count are COMBINED INTO
+ * (max / add; zero them first, fp8ds_scale_update_clear does), scale_used is written.
+ * scale NULL: no FP8 copy, then q, scale_used, amax and sat_count must be NULL.
+ *   q          device [rows x cols] bytes, rows ldq apart.
+ */
+int fp8ds_rmsnorm(const void* x, fp8ds_dtype xt, int64_t ldx, const void* residual, int64_t ldr,
+                  fp8ds_dtype ht, const void* gamma, fp8ds_dtype gt, int64_t rows, int64_t cols,
+                  float eps, void* h, int64_t ldh, void* y, fp8ds_dtype yt, int64_t ldy,
+                  float* rstd, fp8ds_format fmt, const float* scale, uint8_t* q, int64_t ldq,
+                  float* scale_used, float* amax, uint64_t* sat_count, hipStream_t stream);
+
+/*
+ * fp8ds_rmsnorm_rowwise -- the FP8 copy with a scale per row, as fp8ds_cast_rowwise
+ * casts: scale, scale_inv (or NULL) and amax (or NULL) are [rows], overwritten.
+ */
+int fp8ds_rmsnorm_rowwise(const void* x, fp8ds_dtype xt, int64_t ldx, const void* residual,
+                          int64_t ldr, fp8ds_dtype ht, const void* gamma, fp8ds_dtype gt,
+                          int64_t rows, int64_t cols, float eps, void* h, int64_t ldh, void* y,
+                          fp8ds_dtype yt, int64_t ldy, float* rstd, fp8ds_format fmt, int margin,
+                          uint8_t* q, int64_t ldq, float* scale, float* scale_inv, float* amax,
+                          hipStream_t stream);
+
+/*
+ * fp8ds_rmsnorm_mx -- the copy in blocks of 32 with E8M0 scales, as fp8ds_cast_mx (E4M3,
+ * E5M2) or fp8ds_cast_mxfp4 (E2M1: two elements per byte) casts.
+ *   q          device [rows], ldq bytes apart (at least cols, E2M1: cols / 2).
+ *   scales     device [rows x cols / 32], rows ld_scales apart.
+ * Every row of x, residual, h, y 16-byte aligned, gamma too, rows of q 8-byte aligned
+ * (FP8DS_ERR_ALIGN otherwise).
+ */
+int fp8ds_rmsnorm_mx(const void* x, fp8ds_dtype xt, int64_t ldx, const void* residual, int64_t ldr,
+                     fp8ds_dtype ht, const void* gamma, fp8ds_dtype gt, int64_t rows, int64_t cols,
+                     float eps, void* h, int64_t ldh, void* y, fp8ds_dtype yt, int64_t ldy,
+                     float* rstd, fp8ds_format fmt, uint8_t* q, int64_t ldq, uint8_t* scales,
+                     int64_t ld_scales, hipStream_t stream);
+
+/*
+ * fp8ds_rmsnorm_bwd -- backward of the norm.  With xhat = h r and g = dy gamma, per row
+ *   dx     = r (g - xhat * (sum_c g xhat) / cols) + dres
+ *   dgamma = sum over rows of dy xhat
+ * dx is the gradient of x and of residual; dres is the gradient that reaches h from above.
+ *   dy         device [rows x cols] of dt, lddy apart.
+ *   h          device [rows x cols] of ht, ldh apart: what the forward stored (or its x).
+ *   rstd       device [rows]: what the forward stored.
+ *   gamma      device [cols] of gt.
+ *   dres       device or NULL: [rows x cols] of ht, lddr apart.
+ *   dx         device [rows x cols] of ht, lddx apart.  May be dres, or dy (same type and
+ *              leading dimension).
+ *   dgamma     device [cols] fp32, overwritten (zeros for rows == 0).
+ *   workspace  device, at least fp8ds_rmsnorm_bwd_workspace(rows, cols) bytes, 16-byte
+ *              aligned; its contents need no preparation and do not matter afterwards.
+ *   scale      device or NULL: with it dx, in fp32, is also cast to FP8 as fp8ds_rmsnorm
+ *              casts y (fmt, q, ldq, scale_used, amax, sat_count): the dY operand of the
+ *              products below.
+ * (dt, ht) as (xt, ht) above.  Sums are fp32, in an order fixed by the shape.
+ */
+int64_t fp8ds_rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
+int fp8ds_rmsnorm_bwd(const void* dy, fp8ds_dtype dt, int64_t lddy, const void* h, fp8ds_dtype ht,
+                      int64_t ldh, const float* rstd, const void* gamma, fp8ds_dtype gt,
+                      const void* dres, int64_t lddr, int64_t rows, int64_t cols, void* dx,
+                      int64_t lddx, float* dgamma, void* workspace, int64_t workspace_bytes,
+                      fp8ds_format fmt, const float* scale, uint8_t* q, int64_t ldq,
+                      float* scale_used, float* amax, uint64_t* sat_count, hipStream_t stream);
+
+/*
+ * fp8ds_grad_norm -- global norm of n_tensors gradients and the clipping coefficient:
+ *   norm = grad_scale * sqrt(sum over all elements of g^2)     sums in 64 bits
+ *   coef = min(1, max_norm / (norm + 1e-6))
+ * An infinite norm gives coef 0, NaN gives NaN: hand `norm` to fp8ds_adamw_clip as
+ * grad_amax and such a step is skipped.
+ *   grads      HOST array of device addresses (each aligned to its elements), types and
+ *              counts HOST arrays; read during the call only.  0 to 4096 tensors, of any
+ *              size (0 included; its address may be NULL), 2^40 elements at most.
+ *   grad_scale finite, > 0: the un-scaling that the optimizer applies (its grad_scale).
+ *   max_norm   > 0 (may be infinite); unused if coef is NULL.
+ *   norm, coef device, 1 float each (coef or NULL).
+ *   workspace  device, fp8ds_grad_norm_workspace() bytes, 16-byte aligned, needing no
+ *              preparation; may be NULL for up to 65536 elements in up to 128 tensors.
+ */
+int64_t fp8ds_grad_norm_workspace(void);
+int fp8ds_grad_norm(int n_tensors, const void* const* grads, const fp8ds_dtype* types,
+                    const int64_t* counts, float grad_scale, float max_norm, float* norm,
+                    float* coef, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * fp8ds_grad_clip -- out_t[i] = grads_t[i] * (*coef), an fp32 product rounded to out's
+ * type.  out NULL: in place (nothing is touched if *coef is 1).  out_t may be grads_t
+ * (same type) and must not overlap it otherwise.  Arrays as fp8ds_grad_norm.
+ */
+int fp8ds_grad_clip(int n_tensors, const void* const* grads, const fp8ds_dtype* types,
+                    const int64_t* counts, void* const* out, const fp8ds_dtype* out_types,
+                    const float* coef, hipStream_t stream);
+
+/*
+ * fp8ds_adamw_clip -- fp8ds_adamw whose gradient is also multiplied by a device factor
+ * (fp8ds_grad_norm's coef): g' = g * fl32(grad_scale * (*grad_coef)); otherwise identical.
+ * Clipping then costs no pass over the gradients and no synchronisation.
+ */
+int fp8ds_adamw_clip(float* w, const void* g, fp8ds_dtype gt, float* m, float* v, int64_t rows,
+                     int64_t cols, float lr, float beta1, float beta2, float eps,
+                     float weight_decay, float grad_scale, const float* grad_coef, int64_t step,
+                     const float* grad_amax, fp8ds_format fmt, const float* scale, uint8_t* q,
+                     uint8_t* q_t, float* scale_used, float* amax, uint64_t* sat_count,
+                     hipStream_t stream);
+
+/*
+ * fp8ds_cast_mxfp4 -- MXFP4 cast of a [rows x cols] matrix along its rows: blocks of 32
+ * consecutive elements, E8M0 code floor(log2 amax) - 2 + 127 clamped to [0, 254] (0 for a
+ * zero block, 255 for one that holds a NaN or infinity, whose elements are stored as 6),
+ * elements round to nearest (ties to the even code), saturating at 6, sign kept.
+ *   x          device [rows x cols] of xt, contiguous, 16-byte aligned; cols a multiple of 32.
+ *   q          device [rows x cols / 2] bytes, 16-byte aligned: element 2 i in the low half.
+ *   scales     device [rows x cols / 32].
+ *   q_t, scales_t  device or both NULL: the transpose [cols x rows / 2], [cols x rows / 32],
+ *              blocked along its own rows, from the same read; rows a multiple of 32.
+ */
+int fp8ds_cast_mxfp4(const void* x, fp8ds_dtype xt, int64_t rows, int64_t cols, uint8_t* q,
+                     uint8_t* scales, uint8_t* q_t, uint8_t* scales_t, hipStream_t stream);
+
+/*
+ * fp8ds_dequant_mxfp4 -- the values y [rows x cols] of yt that MXFP4 codes stand for
+ * (exact; NaN for a block with code 255).  q and y contiguous, 16-byte aligned.
+ */
+int fp8ds_dequant_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t cols,
+                        void* y, fp8ds_dtype yt, hipStream_t stream);
+
+/*
+ * fp8ds_gemm_mxfp4 -- C = A B^T with B [N x K] in MXFP4 and A [M x K] in MXFP4 or MXFP8:
+ *   C[i][j] = convert_ct( sum_k X_a(i, k/32) a(i,k) X_b(j, k/32) b(j,k) )
+ * on gfx950's block-scaled matrix instruction, with FP32 accumulation (across a group of
+ * products of an FP8 A the summation precision of FP8DS_MMA_FP8).  A NaN block makes
+ * every output that it touches NaN.
+ *   A, fa      E2M1 (two per byte), E4M3 or E5M2; rows lda ELEMENTS apart.
+ *   scales_a   [M x ld_scales_a] E8M0 codes; scales_b [N x ld_scales_b].
+ *   B          E2M1; rows ldb ELEMENTS apart.
+ *   C          [M x ldc] of ct, aligned to its elements.   amax_c  device or NULL: max |C|.
+ *   M, N       >= 0, any size (M <= 65535 * 64).   K  >= 0, a multiple of 32.
+ *   Rows of A and B 16-byte aligned (lda a multiple of 32, of 16 for FP8; ldb of 32).
+ */
+int fp8ds_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t* A, fp8ds_format fa,
+                     int64_t lda, const uint8_t* scales_a, int64_t ld_scales_a, const uint8_t* B,
+                     int64_t ldb, const uint8_t* scales_b, int64_t ld_scales_b, void* C,
+                     fp8ds_dtype ct, int64_t ldc, float* amax_c, hipStream_t stream);
 
 #ifdef __cplusplus
 }
