@@ -11,6 +11,7 @@
 
 #include "cast_common.h"
 #include "fp4_common.h"
+#include "gemm_kernel.h"
 #include "launch.h"
 
 namespace fp8ds {
@@ -20,12 +21,12 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // matrix-instruction code of an element format
 template <int F>
-constexpr int mfma_format() { return F == kE4M3 ? 0 : F == kE5M2 ? 1 : 4; }
+constexpr int kMfmaFormat = F == kE4M3 ? 0 : F == kE5M2 ? 1 : 4;
 
 template <int FA>
 __device__ __forceinline__ f32x4 mfma_a_fp4(const i32x8& a, const i32x8& b, const f32x4& c, int sa,
                                             int sb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, mfma_format<FA>(), 4, 0, sa, 0,
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, kMfmaFormat<FA>, 4, 0, sa, 0,
                                                           sb);
 }
 
@@ -121,6 +122,328 @@ __global__ __launch_bounds__(64 * KW) void gemm_mxfp4_direct_kernel(Mxfp4Gemm p)
   }
 }
 
+// ------------------------------------------------------------------ tiles through LDS
+
+// A workgroup of four waves (2 x 2) makes a BM x BN tile of C; a wave owns
+// (BM / 2) x (BN / 2) of it as 32 x 32 blocks of v_mfma_scale_f32_32x32x64_f8f6f4.  The
+// operands reach LDS by loads straight into it, two stages of KST elements of K deep,
+// in rows of 128 bytes (64 for the FP4 operand beside an FP8 one) whose 16-byte
+// chunks are permuted by the row, so that consecutive lanes of a fragment read fall in
+// different banks.  K may be walked in any order as long as both operands agree: MFMA
+// step s of a stage takes, in lane half h, block (KST / 64) h + s, so that the E8M0 codes
+// of all of a half's steps lie next to each other, and one 4-byte load per 32 rows and
+// stage serves them; the instruction picks byte s.
+template <int FA>
+struct TileShape {
+  static constexpr int KST = FA == kE2M1 ? 256 : 128;  // elements of K per stage
+  static constexpr int NS = KST / 64;                  // MFMA steps per stage
+  static constexpr int RA = 128;                       // bytes per LDS row of A
+  static constexpr int RB = KST / 2;                   // bytes per LDS row of B
+};
+
+// LDS byte offset of 16-byte chunk c of row r, for rows of RB bytes.  The permutation
+// depends on the row modulo 8 only: rows 32 apart are a constant apart, and the loads'
+// rows (8 or 16 per instruction) all have the same lane pattern.
+template <int RB>
+__device__ __forceinline__ int chunk_off(int r, int c) {
+  if constexpr (RB == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+  else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// This wave's share of the loads of one operand tile (ROWS rows of RB bytes).
+template <int ROWS, int RB>
+struct TileLoader {
+  static constexpr int kRowsPer = 1024 / RB;  // rows per load instruction of a wave
+  static constexpr int kPerWave = ROWS / kRowsPer / 4;
+  __amdgpu_buffer_rsrc_t rsrc;
+  int ld, w, col, voff;
+
+  __device__ __forceinline__ TileLoader(const uint8_t* src, int64_t ld_, int64_t row0, int64_t rows,
+                                        int64_t row_bytes, int tid) {
+    const int lane = tid & 63;
+    ld = (int)ld_;
+    w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // the lane's place in the 1 KB that an instruction fills, and the chunk that belongs there
+    const int row = lane / (RB / 16), place = lane % (RB / 16);
+    col = (RB == 128 ? place ^ (row & 7) : place ^ ((row >> 1) & 3)) * 16;
+    voff = row * ld + col;
+    const int64_t left = rows - row0 < ROWS ? rows - row0 : ROWS;
+    rsrc = byte_rsrc(src + row0 * ld_, (left - 1) * ld_ + row_bytes);
+  }
+
+  // Bytes [k0, k0 + RB) of every row; what lies at or past row_bytes reads as zeros.
+  __device__ __forceinline__ void issue(int k0, int row_bytes, uint8_t* lds) const {
+    const int v = k0 + col < row_bytes ? voff : 0x40000000;
+#pragma unroll
+    for (int i = 0; i < kPerWave; ++i) {
+      const int seg = w * kPerWave + i;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (void __attribute__((address_space(3)))*)(lds + seg * 1024), 16, v,
+          seg * kRowsPer * ld + k0, 0, 0);
+    }
+  }
+};
+
+template <int FA, int OP>
+__device__ __forceinline__ v16f mfma_tile(const v8i& b, const v8i& a, const v16f& c, int sb, int sa) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 4, kMfmaFormat<FA>, OP, sb, OP, sa);
+}
+
+// Where a lane half's E8M0 codes of a stage are in its rows of codes: one load of NS bytes
+// at `at`, shifted down by `shift` bits, gives byte s for step s.  In the stage that K ends
+// in the load stays inside the row (nblk >= NS) and the blocks past its end get code 0:
+// their elements are zeros, and a zero times any power of two is zero.
+template <int FA>
+struct ScalePlace {
+  static constexpr int NS = TileShape<FA>::NS;
+  int at;
+  uint32_t shift;
+  __device__ __forceinline__ ScalePlace(int stage, int nblk, int h) {
+    const int b = stage * (2 * NS) + NS * h;
+    at = min(b, nblk - NS);
+    shift = 8u * (uint32_t)min(b - at, NS);
+  }
+  // rows of codes may start at any byte
+  __device__ __forceinline__ int load(__amdgpu_buffer_rsrc_t rsrc, int row) const {
+    if constexpr (NS == 4) {
+      const uint32_t v = __builtin_amdgcn_raw_buffer_load_b32(rsrc, row + at, 0, 0);
+      return (int)(((uint64_t)v) >> shift);
+    } else {
+      const uint32_t v = __builtin_amdgcn_raw_buffer_load_b16(rsrc, row + at, 0, 0);
+      return (int)(v >> shift);
+    }
+  }
+};
+
+// The codes of a tile's rows: reads outside them give 0.
+template <int ROWS>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_rsrc(const uint8_t* sc, int64_t ld,
+                                                             int64_t row0, int64_t rows, int nblk) {
+  const int64_t left = rows - row0 < ROWS ? rows - row0 : ROWS;
+  return byte_rsrc(sc + row0 * ld, (left - 1) * ld + nblk);
+}
+
+template <int FA, int BM, int BN>
+__global__ __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) void gemm_mxfp4_tile_kernel(
+    Mxfp4Gemm p, int tiles_m, int tiles_n) {
+  using S = TileShape<FA>;
+  constexpr int NS = S::NS, WM = BM / 2, WN = BN / 2, MI = WM / 32, NI = WN / 32;
+  constexpr int kA = BM * S::RA, kB = BN * S::RB, kStage = kA + kB;
+  constexpr int kOut = BM * BN * 2;  // the BF16 tile on its way out
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage > kOut ? 2 * kStage : kOut];
+  __shared__ uint32_t red[8];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int r = lane & 31, h = lane >> 5;
+  const int wm = (w >> 1) * WM, wn = (w & 1) * WN;
+  int tm, tn;
+  tile_coords(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int row_a = (int)(FA == kE2M1 ? p.K / 2 : p.K), row_b = (int)(p.K / 2);
+  const TileLoader<BM, S::RA> la(p.A, FA == kE2M1 ? p.lda / 2 : p.lda, m0, p.M, row_a, tid);
+  const TileLoader<BN, S::RB> lb(p.B, p.ldb / 2, n0, p.N, row_b, tid);
+  const int nblk = (int)(p.K / 32);
+  const __amdgpu_buffer_rsrc_t ca = scale_rsrc<BM>(p.sc_a, p.ldsa, m0, p.M, nblk);
+  const __amdgpu_buffer_rsrc_t cb = scale_rsrc<BN>(p.sc_b, p.ldsb, n0, p.N, nblk);
+  // rows past the edge read as code 0: their elements are zeros
+  int ra[MI], rb[NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) ra[i] = (wm + 32 * i + r) * (int)p.ldsa;
+#pragma unroll
+  for (int j = 0; j < NI; ++j) rb[j] = (wn + 32 * j + r) * (int)p.ldsb;
+  // this lane's fragment chunks in a row of LDS, one per load of a stage
+  int oa[S::RA == 128 && FA != kE2M1 ? 2 * NS : NS], ob[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    if constexpr (FA == kE2M1) {
+      oa[s] = chunk_off<S::RA>(r, NS * h + s);
+    } else {  // a lane holds half h of the blocks of both lane halves: s and NS + s
+      oa[s] = chunk_off<S::RA>(r, 2 * s + h);
+      oa[NS + s] = chunk_off<S::RA>(r, 2 * (NS + s) + h);
+    }
+    ob[s] = chunk_off<S::RB>(r, NS * h + s);
+  }
+  v16f acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+  const int nst = (int)((p.K + S::KST - 1) / S::KST);
+  auto issue = [&](int k) {
+    uint8_t* dst = lds + (k & 1) * kStage;
+    la.issue(k * S::RA, row_a, dst);
+    lb.issue(k * S::RB, row_b, dst + kA);
+  };
+  int sa[MI], sb[NI], na[MI], nb[NI];
+  auto scales = [&](int k) {
+    const ScalePlace<FA> at(k, nblk, h);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) na[i] = at.load(ca, ra[i]);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) nb[j] = at.load(cb, rb[j]);
+  };
+  v8i fa[2][MI], fb[2][NI];
+  // fragments of step s of the stage in buffer `buf`, into register set s & 1
+  auto frags = [&](int buf, auto step) {
+    constexpr int s = decltype(step)::value;
+    const uint8_t *pa = lds + buf * kStage + wm * S::RA, *pb = lds + buf * kStage + kA + wn * S::RB;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const u32x4 d = *reinterpret_cast<const u32x4*>(pa + oa[s] + 32 * i * S::RA);
+      fa[s & 1][i] = v8i{(int)d[0], (int)d[1], (int)d[2], (int)d[3], 0, 0, 0, 0};
+      if constexpr (FA != kE2M1) {
+        const u32x4 e = *reinterpret_cast<const u32x4*>(pa + oa[NS + s] + 32 * i * S::RA);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) fa[s & 1][i][4 + x] = (int)e[x];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const u32x4 d = *reinterpret_cast<const u32x4*>(pb + ob[s] + 32 * j * S::RB);
+      fb[s & 1][j] = v8i{(int)d[0], (int)d[1], (int)d[2], (int)d[3], 0, 0, 0, 0};
+    }
+  };
+  auto mfmas = [&](auto step) {
+    constexpr int s = decltype(step)::value;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+        acc[i][j] = mfma_tile<FA, s>(fb[s & 1][j], fa[s & 1][i], acc[i][j], sb[j], sa[i]);
+  };
+  using std::integral_constant;
+  // One stage.  LOAD: the loads two stages ahead; NEXT: there is a next stage.  The only
+  // barrier sits before the last step's MFMAs: every wave then has all of the stage's
+  // fragments in registers, so its buffer may be refilled, and the next stage is in LDS.
+  auto stage = [&](int k, auto load, auto next) {
+    const int buf = k & 1;
+    if constexpr (decltype(next)::value) scales(k + 1);
+    frags(buf, integral_constant<int, 1>{});
+    mfmas(integral_constant<int, 0>{});
+    if constexpr (NS == 4) {
+      frags(buf, integral_constant<int, 2>{});
+      mfmas(integral_constant<int, 1>{});
+      frags(buf, integral_constant<int, 3>{});
+      mfmas(integral_constant<int, 2>{});
+    }
+    if constexpr (decltype(next)::value) {
+      vmem_wait_all();
+      __syncthreads();
+      if constexpr (decltype(load)::value) issue(k + 2);
+      frags(buf ^ 1, integral_constant<int, 0>{});
+    }
+    mfmas(integral_constant<int, NS - 1>{});
+    if constexpr (decltype(next)::value) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) sa[i] = na[i];
+#pragma unroll
+      for (int j = 0; j < NI; ++j) sb[j] = nb[j];
+    }
+  };
+  if (nst > 0) {
+    issue(0);
+    scales(0);
+    if (nst > 1) issue(1);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) sa[i] = na[i];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) sb[j] = nb[j];
+    vmem_wait_all();
+    __syncthreads();
+    frags(0, integral_constant<int, 0>{});
+    int k = 0;
+    for (; k < nst - 2; ++k)
+      stage(k, integral_constant<bool, true>{}, integral_constant<bool, true>{});
+    if (nst > 1) {
+      stage(k, integral_constant<bool, false>{}, integral_constant<bool, true>{});
+      ++k;
+    }
+    stage(k, integral_constant<bool, false>{}, integral_constant<bool, false>{});
+  }
+
+  // Epilogue.  Lane (r, h) holds, of block (i, j), row r and columns 8 q + 4 h + {0..3} in
+  // elements 4 q .. 4 q + 3.  BF16: each wave parks its rows in LDS (16-byte chunks
+  // permuted by the row) and writes whole row runs; FP32: 16-byte pieces.
+  uint32_t amax = 0;
+  const int64_t cm = m0 + wm, cn = n0 + wn;
+  if (p.out_bf16) {
+    __syncthreads();  // the tiles in LDS are done with
+    uint8_t* out = lds + w * (WM * WN * 2);
+    constexpr int CH = WN / 8;  // 16-byte chunks per row
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const u32x2 d = {bf16_pair_rne(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
+                           bf16_pair_rne(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
+          const int row = 32 * i + r, c = 4 * j + q;
+          *reinterpret_cast<u32x2*>(out + row * (WN * 2) + ((c ^ (row & (CH - 1))) << 4) + 8 * h) = d;
+        }
+    __builtin_amdgcn_wave_barrier();
+    uint16_t* C = static_cast<uint16_t*>(p.C);
+    const bool wide = ((reinterpret_cast<uintptr_t>(C) | (uint64_t)(p.ldc * 2)) & 15u) == 0;
+    constexpr int RPI = 64 / CH;  // rows per wave instruction
+#pragma unroll 4
+    for (int it = 0; it < WM / RPI; ++it) {
+      const int row = it * RPI + lane / CH, c = lane % CH;
+      const u32x4 d = *reinterpret_cast<const u32x4*>(out + row * (WN * 2) + ((c ^ (row & (CH - 1))) << 4));
+      const int64_t m = cm + row, n = cn + 8 * c;
+      if (m >= p.M || n >= p.N) continue;
+      if (wide && n + 8 <= p.N) {
+        __builtin_nontemporal_store(d, reinterpret_cast<u32x4*>(C + m * p.ldc + n));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          amax = max(amax, max((d[e] & 0x7FFFu) << 16, d[e] & 0x7FFF0000u));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (n + e >= p.N) continue;
+          const uint32_t v = (d[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+          C[m * p.ldc + n + e] = (uint16_t)v;
+          amax = max(amax, (v & 0x7FFFu) << 16);
+        }
+      }
+    }
+  } else {
+    float* C = static_cast<float*>(p.C);
+    const bool wide = ((reinterpret_cast<uintptr_t>(C) | (uint64_t)(p.ldc * 4)) & 15u) == 0;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int64_t m = cm + 32 * i + r;
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t n = cn + 32 * j + 8 * q + 4 * h;
+          if (m >= p.M || n >= p.N) continue;
+          u32x4 d;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[e] = __float_as_uint(acc[i][j][4 * q + e]);
+          if (wide && n + 4 <= p.N) {
+            __builtin_nontemporal_store(d, reinterpret_cast<u32x4*>(C + m * p.ldc + n));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) amax = max(amax, d[e] & 0x7FFFFFFFu);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (n + e >= p.N) continue;
+              C[m * p.ldc + n + e] = __uint_as_float(d[e]);
+              amax = max(amax, d[e] & 0x7FFFFFFFu);
+            }
+          }
+        }
+    }
+  }
+  if (p.amax_c) {
+    Health hh;
+    block_commit<false>(amax, 0u, hh, reinterpret_cast<uint32_t*>(p.amax_c), nullptr, nullptr, red);
+  }
+}
+
 // ------------------------------------------------------------------ host launcher
 
 template <int FA, int MT, int NT, int KW>
@@ -131,17 +454,31 @@ static hipError_t launch_direct(const Mxfp4Gemm& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int FA, int BM, int BN>
+static hipError_t launch_tile(const Mxfp4Gemm& p, hipStream_t stream) {
+  const int tm = (int)((p.M + BM - 1) / BM), tn = (int)((p.N + BN - 1) / BN);
+  hipLaunchKernelGGL((gemm_mxfp4_tile_kernel<FA, BM, BN>), dim3((unsigned)(tm * tn)), dim3(256), 0,
+                     stream, p, tm, tn);
+  return hipGetLastError();
+}
+
 template <int FA>
-static hipError_t launch_fa(const Mxfp4Gemm& p, hipStream_t stream) {
+static hipError_t launch_fa(const Mxfp4Gemm& p, int num_cus, hipStream_t stream) {
   if (p.M <= 16) return launch_direct<FA, 1, 1, 8>(p, stream);
-  return launch_direct<FA, 4, 4, 1>(p, stream);
+  // the tile loads address their rows with 30 bits, the codes' loads need four blocks a row
+  const bool fits = p.lda < (1 << 21) && p.ldb < (1 << 21) && p.ldsa < (1 << 21) &&
+                    p.ldsb < (1 << 21) && p.K >= 128;
+  if (!fits) return launch_direct<FA, 4, 4, 1>(p, stream);
+  const int64_t big = ((p.M + 255) / 256) * ((p.N + 255) / 256);
+  if (big >= num_cus) return launch_tile<FA, 256, 256>(p, stream);
+  return launch_tile<FA, 128, 128>(p, stream);
 }
 
 hipError_t launch_gemm_mxfp4(const Mxfp4Gemm& p, int fa, int num_cus, hipStream_t stream) {
   switch (fa) {
-    case kE4M3: return launch_fa<kE4M3>(p, stream);
-    case kE5M2: return launch_fa<kE5M2>(p, stream);
-    default: return launch_fa<kE2M1>(p, stream);
+    case kE4M3: return launch_fa<kE4M3>(p, num_cus, stream);
+    case kE5M2: return launch_fa<kE5M2>(p, num_cus, stream);
+    default: return launch_fa<kE2M1>(p, num_cus, stream);
   }
 }
 
