@@ -124,8 +124,8 @@ __global__ __launch_bounds__(64 * KW) void gemm_mxfp4_direct_kernel(Mxfp4Gemm p)
 
 // ------------------------------------------------------------------ tiles through LDS
 
-// A workgroup of four waves (2 x 2) makes a BM x BN tile of C; a wave owns
-// (BM / 2) x (BN / 2) of it as 32 x 32 blocks of v_mfma_scale_f32_32x32x64_f8f6f4.  The
+// A workgroup of GM x GN waves makes a BM x BN tile of C; a wave owns
+// (BM / GM) x (BN / GN) of it as 32 x 32 blocks of v_mfma_scale_f32_32x32x64_f8f6f4.  The
 // operands reach LDS by loads straight into it, two stages of KST elements of K deep,
 // in rows of 128 bytes (64 for the FP4 operand beside an FP8 one) whose 16-byte
 // chunks are permuted by the row, so that consecutive lanes of a fragment read fall in
@@ -151,10 +151,10 @@ __device__ __forceinline__ int chunk_off(int r, int c) {
 }
 
 // This wave's share of the loads of one operand tile (ROWS rows of RB bytes).
-template <int ROWS, int RB>
+template <int ROWS, int RB, int NW>
 struct TileLoader {
   static constexpr int kRowsPer = 1024 / RB;  // rows per load instruction of a wave
-  static constexpr int kPerWave = ROWS / kRowsPer / 4;
+  static constexpr int kPerWave = ROWS / kRowsPer / NW;
   __amdgpu_buffer_rsrc_t rsrc;
   int ld, w, col, voff;
 
@@ -184,33 +184,54 @@ struct TileLoader {
   }
 };
 
+// The order of a step: DS fragment reads and VM loads spread over its MF MFMAs, the reads
+// over the first three quarters so that the last of them has arrived for the next step.
+template <int MF, int DS, int VM, int I = 0>
+__device__ __forceinline__ void interleave() {
+  if constexpr (I < MF) {
+    constexpr int kSpan = MF * 3 / 4;
+    constexpr int d0 = I < kSpan ? DS * I / kSpan : DS, d1 = I + 1 < kSpan ? DS * (I + 1) / kSpan : DS;
+    constexpr int v0 = VM * I / MF, v1 = VM * (I + 1) / MF;
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                              // MFMA
+    if constexpr (d1 > d0) __builtin_amdgcn_sched_group_barrier(0x100, d1 - d0, 0);  // LDS read
+    if constexpr (v1 > v0) __builtin_amdgcn_sched_group_barrier(0x020, v1 - v0, 0);  // VMEM read
+    interleave<MF, DS, VM, I + 1>();
+  }
+}
+
 template <int FA, int OP>
 __device__ __forceinline__ v16f mfma_tile(const v8i& b, const v8i& a, const v16f& c, int sb, int sa) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 4, kMfmaFormat<FA>, OP, sb, OP, sa);
 }
 
-// Where a lane half's E8M0 codes of a stage are in its rows of codes: one load of NS bytes
-// at `at`, shifted down by `shift` bits, gives byte s for step s.  In the stage that K ends
-// in the load stays inside the row (nblk >= NS) and the blocks past its end get code 0:
-// their elements are zeros, and a zero times any power of two is zero.
-template <int FA>
-struct ScalePlace {
+// E8M0 codes of a tile's rows, 16 blocks of each at a time, by loads straight into LDS
+// (16 bytes per row: row i of A, then of B).  Read from memory by every lane for its own
+// rows and stage, they cost as many cache lines as the elements themselves: half the
+// kernel's time at 4096 x 4096 x 16384.
+template <int FA, int BM, int BN, int NW>
+struct ScaleTiles {
   static constexpr int NS = TileShape<FA>::NS;
-  int at;
-  uint32_t shift;
-  __device__ __forceinline__ ScalePlace(int stage, int nblk, int h) {
-    const int b = stage * (2 * NS) + NS * h;
-    at = min(b, nblk - NS);
-    shift = 8u * (uint32_t)min(b - at, NS);
-  }
-  // rows of codes may start at any byte
-  __device__ __forceinline__ int load(__amdgpu_buffer_rsrc_t rsrc, int row) const {
-    if constexpr (NS == 4) {
-      const uint32_t v = __builtin_amdgcn_raw_buffer_load_b32(rsrc, row + at, 0, 0);
-      return (int)(((uint64_t)v) >> shift);
-    } else {
-      const uint32_t v = __builtin_amdgcn_raw_buffer_load_b16(rsrc, row + at, 0, 0);
-      return (int)(v >> shift);
+  static constexpr int kStages = 16 / (2 * NS);      // stages served by a load
+  static constexpr int kBytes = (BM + BN) * 16;
+  static constexpr int kPerWave = (BM + BN) / (64 * NW);
+
+  // The first block of group g's load: the last group stays inside the row.
+  static __device__ __forceinline__ int first(int g, int nblk) { return min(16 * g, nblk - 16); }
+
+  static __device__ __forceinline__ void issue(__amdgpu_buffer_rsrc_t ca, __amdgpu_buffer_rsrc_t cb,
+                                               int lda, int ldb, int g, int nblk, int w, int lane,
+                                               uint8_t* dst) {
+    const int wv = __builtin_amdgcn_readfirstlane(w), f = first(g, nblk);
+    // 64 rows per instruction, no branch
+#pragma unroll
+    for (int x = 0; x < kPerWave; ++x) {
+      constexpr int kSegA = BM / 64;
+      const int seg = NW * x + wv;
+      const bool of_a = kSegA % NW == 0 ? x < kSegA / NW : seg < kSegA;
+      const int ld = of_a ? lda : ldb, row = (of_a ? seg : seg - kSegA) * 64;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          of_a ? ca : cb, (void __attribute__((address_space(3)))*)(dst + seg * 1024), 16, lane * ld,
+          row * ld + f, 0, 0);
     }
   }
 };
@@ -223,33 +244,32 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_rsrc(const uint8_t* sc, 
   return byte_rsrc(sc + row0 * ld, (left - 1) * ld + nblk);
 }
 
-template <int FA, int BM, int BN>
-__global__ __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) void gemm_mxfp4_tile_kernel(
-    Mxfp4Gemm p, int tiles_m, int tiles_n) {
+template <int FA, int BM, int BN, int GM, int GN>
+__global__ __launch_bounds__(64 * GM * GN, 2) void gemm_mxfp4_tile_kernel(Mxfp4Gemm p, int tiles_m,
+                                                                         int tiles_n) {
   using S = TileShape<FA>;
-  constexpr int NS = S::NS, WM = BM / 2, WN = BN / 2, MI = WM / 32, NI = WN / 32;
-  constexpr int kA = BM * S::RA, kB = BN * S::RB, kStage = kA + kB;
-  constexpr int kOut = BM * BN * 2;  // the BF16 tile on its way out
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage > kOut ? 2 * kStage : kOut];
-  __shared__ uint32_t red[8];
+  constexpr int NS = S::NS, NW = GM * GN, WM = BM / GM, WN = BN / GN, MI = WM / 32, NI = WN / 32;
+  using SC = ScaleTiles<FA, BM, BN, NW>;
+  constexpr int kA = BM * S::RA, kB = BN * S::RB, kStage = kA + kB + SC::kBytes;
+  constexpr int kOut = BM * BN;  // half of the BF16 tile on its way out
+  // The two stages are two variables, and the loop below names them: the compiler then
+  // knows that a fragment read does not touch the buffer being loaded, and does not wait
+  // for the loads in flight before each of them.
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[kStage > kOut ? kStage : kOut];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds1[kStage > kOut ? kStage : kOut];
+  __shared__ uint32_t red[2 * NW];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int r = lane & 31, h = lane >> 5;
-  const int wm = (w >> 1) * WM, wn = (w & 1) * WN;
+  const int wm = (w / GN) * WM, wn = (w % GN) * WN;
   int tm, tn;
   tile_coords(blockIdx.x, tiles_m, tiles_n, tm, tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int row_a = (int)(FA == kE2M1 ? p.K / 2 : p.K), row_b = (int)(p.K / 2);
-  const TileLoader<BM, S::RA> la(p.A, FA == kE2M1 ? p.lda / 2 : p.lda, m0, p.M, row_a, tid);
-  const TileLoader<BN, S::RB> lb(p.B, p.ldb / 2, n0, p.N, row_b, tid);
+  const TileLoader<BM, S::RA, NW> la(p.A, FA == kE2M1 ? p.lda / 2 : p.lda, m0, p.M, row_a, tid);
+  const TileLoader<BN, S::RB, NW> lb(p.B, p.ldb / 2, n0, p.N, row_b, tid);
   const int nblk = (int)(p.K / 32);
   const __amdgpu_buffer_rsrc_t ca = scale_rsrc<BM>(p.sc_a, p.ldsa, m0, p.M, nblk);
   const __amdgpu_buffer_rsrc_t cb = scale_rsrc<BN>(p.sc_b, p.ldsb, n0, p.N, nblk);
-  // rows past the edge read as code 0: their elements are zeros
-  int ra[MI], rb[NI];
-#pragma unroll
-  for (int i = 0; i < MI; ++i) ra[i] = (wm + 32 * i + r) * (int)p.ldsa;
-#pragma unroll
-  for (int j = 0; j < NI; ++j) rb[j] = (wn + 32 * j + r) * (int)p.ldsb;
   // this lane's fragment chunks in a row of LDS, one per load of a stage
   int oa[S::RA == 128 && FA != kE2M1 ? 2 * NS : NS], ob[NS];
 #pragma unroll
@@ -271,24 +291,18 @@ __global__ __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) void gemm_mxfp4_t
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
   const int nst = (int)((p.K + S::KST - 1) / S::KST);
-  auto issue = [&](int k) {
-    uint8_t* dst = lds + (k & 1) * kStage;
+  int sa[MI], sb[NI];
+  v8i fa[2][MI], fb[2][NI];
+  // the loads of stage k: elements of A, of B, codes of both
+  auto issue = [&](int k, uint8_t* dst) {
     la.issue(k * S::RA, row_a, dst);
     lb.issue(k * S::RB, row_b, dst + kA);
+    SC::issue(ca, cb, (int)p.ldsa, (int)p.ldsb, k / SC::kStages, nblk, w, lane, dst + kA + kB);
   };
-  int sa[MI], sb[NI], na[MI], nb[NI];
-  auto scales = [&](int k) {
-    const ScalePlace<FA> at(k, nblk, h);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) na[i] = at.load(ca, ra[i]);
-#pragma unroll
-    for (int j = 0; j < NI; ++j) nb[j] = at.load(cb, rb[j]);
-  };
-  v8i fa[2][MI], fb[2][NI];
-  // fragments of step s of the stage in buffer `buf`, into register set s & 1
-  auto frags = [&](int buf, auto step) {
+  // fragments of step s of the stage in `src`, into register set s & 1
+  auto frags = [&](const uint8_t* src, auto step) {
     constexpr int s = decltype(step)::value;
-    const uint8_t *pa = lds + buf * kStage + wm * S::RA, *pb = lds + buf * kStage + kA + wn * S::RB;
+    const uint8_t *pa = src + wm * S::RA, *pb = src + kA + wn * S::RB;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       const u32x4 d = *reinterpret_cast<const u32x4*>(pa + oa[s] + 32 * i * S::RA);
@@ -314,53 +328,77 @@ __global__ __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) void gemm_mxfp4_t
         acc[i][j] = mfma_tile<FA, s>(fb[s & 1][j], fa[s & 1][i], acc[i][j], sb[j], sa[i]);
   };
   using std::integral_constant;
-  // One stage.  LOAD: the loads two stages ahead; NEXT: there is a next stage.  The only
-  // barrier sits before the last step's MFMAs: every wave then has all of the stage's
-  // fragments in registers, so its buffer may be refilled, and the next stage is in LDS.
-  auto stage = [&](int k, auto load, auto next) {
-    const int buf = k & 1;
-    if constexpr (decltype(next)::value) scales(k + 1);
-    frags(buf, integral_constant<int, 1>{});
+  // One stage, from its barrier on.  The fragments of a step are read while the step
+  // before it is multiplied, so the previous stage's last step comes first here, and the
+  // loads of the next stage start beside it, into the buffer that this barrier freed.
+  auto stage = [&](int k, const uint8_t* rd, uint8_t* wr) {
+    // the codes of this lane's rows and half, byte s for step s; blocks past the end of K
+    // take code 0 (their elements are zeros), and so do rows past the edge
+    const int off = k * (2 * NS) + NS * h - SC::first(k / SC::kStages, nblk);
+    const bool in = off <= 16 - NS;
+    const uint8_t* src = rd + kA + kB + r * 16 + (in ? off : 0);
+    int na[MI], nb[NI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const uint8_t* q = src + (wm + 32 * i) * 16;
+      na[i] = NS == 4 ? *reinterpret_cast<const int*>(q) : *reinterpret_cast<const uint16_t*>(q);
+    }
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const uint8_t* q = src + (BM + wn + 32 * j) * 16;
+      nb[j] = NS == 4 ? *reinterpret_cast<const int*>(q) : *reinterpret_cast<const uint16_t*>(q);
+    }
+    frags(rd, integral_constant<int, 0>{});
+    issue(k + 1, wr);
+    mfmas(integral_constant<int, NS - 1>{});
+#pragma unroll
+    for (int i = 0; i < MI; ++i) sa[i] = in ? na[i] : 0;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) sb[j] = in ? nb[j] : 0;
+    frags(rd, integral_constant<int, 1>{});
     mfmas(integral_constant<int, 0>{});
     if constexpr (NS == 4) {
-      frags(buf, integral_constant<int, 2>{});
+      frags(rd, integral_constant<int, 2>{});
       mfmas(integral_constant<int, 1>{});
-      frags(buf, integral_constant<int, 3>{});
+      frags(rd, integral_constant<int, 3>{});
       mfmas(integral_constant<int, 2>{});
     }
-    if constexpr (decltype(next)::value) {
-      vmem_wait_all();
-      __syncthreads();
-      if constexpr (decltype(load)::value) issue(k + 2);
-      frags(buf ^ 1, integral_constant<int, 0>{});
-    }
-    mfmas(integral_constant<int, NS - 1>{});
-    if constexpr (decltype(next)::value) {
+    // issue order: fragment reads and loads between the MFMAs that hide them
+    constexpr int kReads = MI * (FA == kE2M1 ? 1 : 2) + NI, kMf = MI * NI;
+    interleave<kMf, kReads + MI + NI, la.kPerWave + lb.kPerWave + SC::kPerWave>();
 #pragma unroll
-      for (int i = 0; i < MI; ++i) sa[i] = na[i];
-#pragma unroll
-      for (int j = 0; j < NI; ++j) sb[j] = nb[j];
-    }
+    for (int s = 0; s < NS - 1; ++s) interleave<kMf, kReads, 0>();
   };
-  if (nst > 0) {
-    issue(0);
-    scales(0);
-    if (nst > 1) issue(1);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) sa[i] = na[i];
-#pragma unroll
-    for (int j = 0; j < NI; ++j) sb[j] = nb[j];
+  // this wave's loads have arrived, then everyone's
+  auto arrived = [] {
     vmem_wait_all();
     __syncthreads();
-    frags(0, integral_constant<int, 0>{});
-    int k = 0;
-    for (; k < nst - 2; ++k)
-      stage(k, integral_constant<bool, true>{}, integral_constant<bool, true>{});
-    if (nst > 1) {
-      stage(k, integral_constant<bool, false>{}, integral_constant<bool, true>{});
-      ++k;
+  };
+  if (nst > 0) {
+    // "the last step of the stage before the first": zeros
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      sa[i] = 127;
+      fa[1][i] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
     }
-    stage(k, integral_constant<bool, false>{}, integral_constant<bool, false>{});
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      sb[j] = 127;
+      fb[1][j] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
+    }
+    issue(0, lds0);
+    // Two exits of one loop, and loads in the last stage too (what lies past K reads as
+    // zeros without reaching memory): stages without loads, as code of their own, cost the
+    // registers of both.
+    for (int k = 0;; ++k) {
+      arrived();
+      stage(k, lds0, lds1);
+      if (++k >= nst) break;
+      arrived();
+      stage(k, lds1, lds0);
+      if (k + 1 >= nst) break;
+    }
+    mfmas(integral_constant<int, NS - 1>{});
   }
 
   // Epilogue.  Lane (r, h) holds, of block (i, j), row r and columns 8 q + 4 h + {0..3} in
@@ -369,8 +407,8 @@ __global__ __launch_bounds__(256, BM * BN > 128 * 128 ? 1 : 2) void gemm_mxfp4_t
   uint32_t amax = 0;
   const int64_t cm = m0 + wm, cn = n0 + wn;
   if (p.out_bf16) {
-    __syncthreads();  // the tiles in LDS are done with
-    uint8_t* out = lds + w * (WM * WN * 2);
+    arrived();  // the tiles in LDS are done with
+    uint8_t* out = (w >= NW / 2 ? lds1 : lds0) + w % (NW / 2) * (WM * WN * 2);
     constexpr int CH = WN / 8;  // 16-byte chunks per row
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -454,10 +492,10 @@ static hipError_t launch_direct(const Mxfp4Gemm& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int FA, int BM, int BN>
+template <int FA, int BM, int BN, int GM, int GN>
 static hipError_t launch_tile(const Mxfp4Gemm& p, hipStream_t stream) {
   const int tm = (int)((p.M + BM - 1) / BM), tn = (int)((p.N + BN - 1) / BN);
-  hipLaunchKernelGGL((gemm_mxfp4_tile_kernel<FA, BM, BN>), dim3((unsigned)(tm * tn)), dim3(256), 0,
+  hipLaunchKernelGGL((gemm_mxfp4_tile_kernel<FA, BM, BN, GM, GN>), dim3((unsigned)(tm * tn)), dim3(64 * GM * GN), 0,
                      stream, p, tm, tn);
   return hipGetLastError();
 }
@@ -465,13 +503,17 @@ static hipError_t launch_tile(const Mxfp4Gemm& p, hipStream_t stream) {
 template <int FA>
 static hipError_t launch_fa(const Mxfp4Gemm& p, int num_cus, hipStream_t stream) {
   if (p.M <= 16) return launch_direct<FA, 1, 1, 8>(p, stream);
-  // the tile loads address their rows with 30 bits, the codes' loads need four blocks a row
+  // The tile loads address their rows with 30 bits; the codes' loads take 16 blocks of a
+  // row at a time, at addresses that are a multiple of 4.
+  const bool scales_aligned = ((reinterpret_cast<uintptr_t>(p.sc_a) | (uint64_t)p.ldsa |
+                                reinterpret_cast<uintptr_t>(p.sc_b) | (uint64_t)p.ldsb |
+                                (uint64_t)(p.K / 32)) & 3u) == 0;
   const bool fits = p.lda < (1 << 21) && p.ldb < (1 << 21) && p.ldsa < (1 << 21) &&
-                    p.ldsb < (1 << 21) && p.K >= 128;
+                    p.ldsb < (1 << 21) && p.K >= 512 && scales_aligned;
   if (!fits) return launch_direct<FA, 4, 4, 1>(p, stream);
   const int64_t big = ((p.M + 255) / 256) * ((p.N + 255) / 256);
-  if (big >= num_cus) return launch_tile<FA, 256, 256>(p, stream);
-  return launch_tile<FA, 128, 128>(p, stream);
+  if (big >= num_cus) return launch_tile<FA, 256, 256, 4, 2>(p, stream);
+  return launch_tile<FA, 128, 128, 2, 2>(p, stream);
 }
 
 hipError_t launch_gemm_mxfp4(const Mxfp4Gemm& p, int fa, int num_cus, hipStream_t stream) {
