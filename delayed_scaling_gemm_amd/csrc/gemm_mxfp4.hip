@@ -386,17 +386,24 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void gemm_mxfp4_tile_kernel(Mxfp4G
       sb[j] = 127;
       fb[1][j] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
     }
-    issue(0, lds0);
-    // Two exits of one loop, and loads in the last stage too (what lies past K reads as
-    // zeros without reaching memory): stages without loads, as code of their own, cost the
-    // registers of both.
-    for (int k = 0;; ++k) {
+    // Stages go in pairs, an odd first one by itself.  The last one's loads are issued
+    // too (what lies past K reads as zeros without reaching memory): a loop that leaves
+    // them out, or that can end between the two stages, was compiled to copies of the
+    // accumulators.
+    int k = 0;
+    if (nst & 1) {
+      issue(0, lds1);
+      arrived();
+      stage(0, lds1, lds0);
+      k = 1;
+    } else {
+      issue(0, lds0);
+    }
+    for (; k < nst; k += 2) {
       arrived();
       stage(k, lds0, lds1);
-      if (++k >= nst) break;
       arrived();
-      stage(k, lds1, lds0);
-      if (k + 1 >= nst) break;
+      stage(k + 1, lds1, lds0);
     }
     mfmas(integral_constant<int, NS - 1>{});
   }
