@@ -23,46 +23,70 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 template <int F>
 constexpr int kMfmaFormat = F == kE4M3 ? 0 : F == kE5M2 ? 1 : 4;
 
-template <int FA>
+template <int FA, int OP>
 __device__ __forceinline__ f32x4 mfma_a_fp4(const i32x8& a, const i32x8& b, const f32x4& c, int sa,
                                             int sb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, kMfmaFormat<FA>, 4, 0, sa, 0,
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, kMfmaFormat<FA>, 4, OP, sa, OP,
                                                           sb);
 }
 
-// One lane's operand of rows [0, rows) of a matrix with `ld` bytes per row, at K offset
-// k0 (elements): row r, group g.  Rows and blocks out of range give zeros (with the
-// scale of 1, so that 0 * scale is 0).
+// ------------------------------------------------------------------ few rows
+
+// 512 elements of K of one lane's row of an operand, for four MFMA steps.  Step u takes, in
+// lane group g, block 4 g + u, so that a lane's elements are 64 consecutive bytes (FP4)
+// and its codes one dword, of which the instruction picks byte u.
+struct Span {
+  i32x8 v[4];
+  int s;
+};
+constexpr int kSpan = 512;
+
 template <int F>
-__device__ __forceinline__ void load_frag(const uint8_t* p, int64_t ld, const uint8_t* sc,
-                                          int64_t lds, int64_t r, int64_t rows, int64_t k0,
-                                          int64_t K, int g, i32x8& v, int& s) {
-  v = i32x8{0, 0, 0, 0, 0, 0, 0, 0};
-  s = 127;
-  if (r >= rows) return;
-  if (k0 + 32 * g < K) s = sc[r * lds + k0 / 32 + g];
-  if constexpr (F == kE2M1) {
-    if (k0 + 32 * g < K) {
-      const u32x4 d = *reinterpret_cast<const u32x4*>(p + r * ld + (k0 + 32 * g) / 2);
+struct RowPtr {
+  const uint8_t *p, *sc;
+  __device__ __forceinline__ RowPtr(const uint8_t* base, int64_t ld, const uint8_t* codes,
+                                    int64_t ldc, int64_t row, int64_t rows) {
+    // rows past the end read the last one: what they give is not stored
+    row = row < rows ? row : rows - 1;
+    p = base + row * (F == kE2M1 ? ld / 2 : ld);
+    sc = codes + row * ldc;
+  }
+  // The span at k (a multiple of 512).  Blocks past the end of K: the row's start is read
+  // in their place and the code is 0; zeros for an FP8 operand (a NaN element would
+  // survive the code; the products of two FP4 elements at 2^-254 vanish).
+  __device__ __forceinline__ void load(Span& d, int64_t k, int64_t K, int g) const {
+    const int64_t b = k / 32 + 4 * g, nblk = K / 32;
+    if (b + 4 <= nblk) {
+      __builtin_memcpy(&d.s, sc + b, 4);  // rows of codes may start anywhere
+    } else {
+      d.s = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = (int)d[i];
+      for (int u = 0; u < 4; ++u)
+        if (b + u < nblk) d.s |= (int)sc[b + u] << (8 * u);
     }
-  } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t k = k0 + 64 * h + 16 * g;
-      if (k < K) {
-        const u32x4 d = *reinterpret_cast<const u32x4*>(p + r * ld + k);
+    for (int u = 0; u < 4; ++u) {
+      if constexpr (F == kE2M1) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(p + (b + u < nblk ? (b + u) * 16 : 0));
+        d.v[u] = i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
+      } else {
+        // half g % 2 of the blocks of lane groups g / 2 and 2 + g / 2
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[4 * h + i] = (int)d[i];
+        for (int h = 0; h < 2; ++h) {
+          const int64_t c = k / 32 + 4 * (2 * h + (g >> 1)) + u;
+          const u32x4 x = *reinterpret_cast<const u32x4*>(p + (c < nblk ? c * 32 : 0) + 16 * (g & 1));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d.v[u][4 * h + i] = c < nblk ? (int)x[i] : 0;
+        }
       }
     }
   }
-}
+};
 
-// A workgroup of KW waves makes a tile of 16 MT x 16 NT outputs; wave w takes the K steps
-// w, w + KW, ... of 128, straight from memory to registers, and the waves' sums are
-// joined in LDS in a fixed order.
+// A workgroup of KW waves makes 16 MT x 16 NT outputs; the waves share K, a span each at a
+// time, straight from memory to registers, and their sums are joined in LDS in a fixed
+// order.  A wave has the loads of its next span in flight while it multiplies: with few
+// rows the product is the reading of B, (1/2 + 1/32) byte per weight.
 template <int FA, int MT, int NT, int KW>
 __global__ __launch_bounds__(64 * KW) void gemm_mxfp4_direct_kernel(Mxfp4Gemm p) {
   constexpr int BM = 16 * MT, BN = 16 * NT;
@@ -76,20 +100,41 @@ __global__ __launch_bounds__(64 * KW) void gemm_mxfp4_direct_kernel(Mxfp4Gemm p)
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int64_t lda = FA == kE2M1 ? p.lda / 2 : p.lda, ldb = p.ldb / 2;
-  for (int64_t k = 128 * w; k < p.K; k += 128 * KW) {
-    i32x8 a[MT], b[NT];
-    int sa[MT], sb[NT];
+  int64_t k = (int64_t)kSpan * w;
+  if (k < p.K) {
+    struct Operands {
+      Span a[MT], b[NT];
+    };
+    Operands now;
+    auto load = [&](int64_t at, Operands& x) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-      load_frag<FA>(p.A, lda, p.sc_a, p.ldsa, m0 + 16 * i + r, p.M, k, p.K, g, a[i], sa[i]);
+      for (int j = 0; j < NT; ++j)
+        RowPtr<kE2M1>(p.B, p.ldb, p.sc_b, p.ldsb, n0 + 16 * j + r, p.N).load(x.b[j], at, p.K, g);
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-      load_frag<kE2M1>(p.B, ldb, p.sc_b, p.ldsb, n0 + 16 * j + r, p.N, k, p.K, g, b[j], sb[j]);
+      for (int i = 0; i < MT; ++i)
+        RowPtr<FA>(p.A, p.lda, p.sc_a, p.ldsa, m0 + 16 * i + r, p.M).load(x.a[i], at, p.K, g);
+    };
+    auto mfmas = [&](auto step) {
+      constexpr int u = decltype(step)::value;
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = mfma_a_fp4<FA>(a[i], b[j], acc[i][j], sa[i], sb[j]);
+        for (int j = 0; j < NT; ++j)
+          acc[i][j] = mfma_a_fp4<FA, u>(now.a[i].v[u], now.b[j].v[u], acc[i][j], now.a[i].s, now.b[j].s);
+    };
+    load(k, now);
+    while (true) {
+      k += kSpan * KW;
+      const bool more = k < p.K;
+      Operands next;
+      if (more) load(k, next);
+      mfmas(std::integral_constant<int, 0>{});
+      mfmas(std::integral_constant<int, 1>{});
+      mfmas(std::integral_constant<int, 2>{});
+      mfmas(std::integral_constant<int, 3>{});
+      if (!more) break;
+      now = next;
+    }
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -99,6 +144,7 @@ __global__ __launch_bounds__(64 * KW) void gemm_mxfp4_direct_kernel(Mxfp4Gemm p)
       for (int e = 0; e < 4; ++e) part[w][16 * i + 4 * g + e][16 * j + r] = acc[i][j][e];
   __syncthreads();
   uint32_t amax = 0;
+#pragma unroll 1
   for (int u = threadIdx.x; u < BM * BN; u += 64 * KW) {
     const int m = u / BN, n = u % BN;
     float v = 0.0f;
@@ -107,9 +153,9 @@ __global__ __launch_bounds__(64 * KW) void gemm_mxfp4_direct_kernel(Mxfp4Gemm p)
     if (m0 + m < p.M && n0 + n < p.N) {
       const int64_t at = (m0 + m) * p.ldc + n0 + n;
       if (p.out_bf16) {
-        const uint16_t b = bf16_bits_rne(v);
-        static_cast<uint16_t*>(p.C)[at] = b;
-        amax = max(amax, (uint32_t)(b & 0x7FFFu) << 16);
+        const uint16_t c = bf16_bits_rne(v);
+        static_cast<uint16_t*>(p.C)[at] = c;
+        amax = max(amax, (uint32_t)(c & 0x7FFFu) << 16);
       } else {
         static_cast<float*>(p.C)[at] = v;
         amax = max(amax, __float_as_uint(v) & 0x7FFFFFFFu);
@@ -126,37 +172,58 @@ __global__ __launch_bounds__(64 * KW) void gemm_mxfp4_direct_kernel(Mxfp4Gemm p)
 
 // A workgroup of GM x GN waves makes a BM x BN tile of C; a wave owns
 // (BM / GM) x (BN / GN) of it as 32 x 32 blocks of v_mfma_scale_f32_32x32x64_f8f6f4.  The
-// operands reach LDS by loads straight into it, two stages of KST elements of K deep,
-// in rows of 128 bytes (64 for the FP4 operand beside an FP8 one) whose 16-byte
-// chunks are permuted by the row, so that consecutive lanes of a fragment read fall in
-// different banks.  K may be walked in any order as long as both operands agree: MFMA
-// step s of a stage takes, in lane half h, block (KST / 64) h + s, so that the E8M0 codes
-// of all of a half's steps lie next to each other, and one 4-byte load per 32 rows and
-// stage serves them; the instruction picks byte s.
+// operands reach LDS by loads straight into it, a stage of K at a time: rows of 128 bytes
+// (64 for the FP4 operand beside an FP8 one) whose 16-byte chunks are permuted by the row
+// against bank conflicts, and each row's E8M0 codes.  K may be walked in any order as long
+// as both operands agree: MFMA step s of a stage takes, in lane half h, block steps h + s,
+// so that a half's codes lie next to each other and the instruction picks byte s.
+//
+// Stages: 256 elements of K and two buffers for FP4 x FP4, 128 elements and three for
+// FP8 x FP4, which is what 160 KB of LDS hold of a 256 x 256 tile in rows of 128 bytes.
+// Four buffers of 128 elements (rows of 64 bytes) for FP4 x FP4 have longer to arrive, but
+// L2 serves rows of 64 bytes at half the rate of 128: 132 us became 164 at
+// 4096 x 4096 x 16384.  Two buffers for FP8 x FP4: 416 us instead of 395 at
+// 8192 x 14336 x 4096.
 template <int FA>
-struct TileShape {
-  static constexpr int KST = FA == kE2M1 ? 256 : 128;  // elements of K per stage
-  static constexpr int NS = KST / 64;                  // MFMA steps per stage
-  static constexpr int RA = 128;                       // bytes per LDS row of A
-  static constexpr int RB = KST / 2;                   // bytes per LDS row of B
+struct Stage {
+  static constexpr int K = FA == kE2M1 ? 256 : 128;
+  static constexpr int kSteps = K / 64;
+  static constexpr int kBuffers = FA == kE2M1 ? 2 : 3;
+  static constexpr int kRowA = 128;  // bytes of a row of A
+  static constexpr int kRowB = K / 2;
 };
 
-// LDS byte offset of 16-byte chunk c of row r, for rows of RB bytes.  The permutation
-// depends on the row modulo 8 only: rows 32 apart are a constant apart, and the loads'
-// rows (8 or 16 per instruction) all have the same lane pattern.
+// LDS byte offset of 16-byte chunk c of row r, for rows of RB bytes.  A fragment read
+// serves 16 consecutive rows at a time from the 16 16-byte columns of LDS; the chunks are
+// permuted by the row so that those 16 pieces lie in 16 columns (two rows of 128 bytes, or
+// four of 64, share the columns).
 template <int RB>
 __device__ __forceinline__ int chunk_off(int r, int c) {
-  if constexpr (RB == 128) return r * 128 + ((c ^ (r & 7)) << 4);
-  else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  if constexpr (RB == 128) return r * 128 + ((c ^ ((r >> 1) & 7)) << 4);
+  else return r * 64 + ((c ^ ((r >> 2) & 3)) << 4);
 }
 
-// This wave's share of the loads of one operand tile (ROWS rows of RB bytes).
+__device__ __forceinline__ void load_to_lds16(__amdgpu_buffer_rsrc_t rsrc, uint8_t* lds, int voff,
+                                              int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      rsrc, (void __attribute__((address_space(3)))*)lds, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void load_to_lds4(__amdgpu_buffer_rsrc_t rsrc, uint8_t* lds, int voff,
+                                             int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      rsrc, (void __attribute__((address_space(3)))*)lds, 4, voff, soff, 0, 0);
+}
+// An offset past every buffer: such a load gives zeros and does not reach memory.
+constexpr int kNowhere = 0x40000000;
+
+// This wave's share of the loads of one operand tile (ROWS rows of RB bytes a stage).
 template <int ROWS, int RB, int NW>
 struct TileLoader {
   static constexpr int kRowsPer = 1024 / RB;  // rows per load instruction of a wave
   static constexpr int kPerWave = ROWS / kRowsPer / NW;
+  static_assert(RB != 128 || kPerWave % 2 == 0, "a wave's first rows start a group of 16");
   __amdgpu_buffer_rsrc_t rsrc;
-  int ld, w, col, voff;
+  int ld, w, row_off, col;
 
   __device__ __forceinline__ TileLoader(const uint8_t* src, int64_t ld_, int64_t row0, int64_t rows,
                                         int64_t row_bytes, int tid) {
@@ -165,24 +232,117 @@ struct TileLoader {
     w = __builtin_amdgcn_readfirstlane(tid >> 6);
     // the lane's place in the 1 KB that an instruction fills, and the chunk that belongs there
     const int row = lane / (RB / 16), place = lane % (RB / 16);
-    col = (RB == 128 ? place ^ (row & 7) : place ^ ((row >> 1) & 3)) * 16;
-    voff = row * ld + col;
+    col = (RB == 128 ? place ^ (row >> 1) : place ^ (row >> 2)) * 16;
+    row_off = row * ld;
     const int64_t left = rows - row0 < ROWS ? rows - row0 : ROWS;
     rsrc = byte_rsrc(src + row0 * ld_, (left - 1) * ld_ + row_bytes);
   }
 
-  // Bytes [k0, k0 + RB) of every row; what lies at or past row_bytes reads as zeros.
+  // Bytes [k0, k0 + RB) of every row; what lies at or past row_bytes reads as zeros, and
+  // so do rows past the matrix.
   __device__ __forceinline__ void issue(int k0, int row_bytes, uint8_t* lds) const {
-    const int v = k0 + col < row_bytes ? voff : 0x40000000;
+    // rows 8 .. 15 of every 16 rows of 128 bytes have the other half of the permutations
+    const int even = k0 + col < row_bytes ? row_off + col : kNowhere;
+    const int odd = k0 + (col ^ 64) < row_bytes ? row_off + (col ^ 64) : kNowhere;
 #pragma unroll
     for (int i = 0; i < kPerWave; ++i) {
       const int seg = w * kPerWave + i;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsrc, (void __attribute__((address_space(3)))*)(lds + seg * 1024), 16, v,
-          seg * kRowsPer * ld + k0, 0, 0);
+      load_to_lds16(rsrc, lds + seg * 1024, RB == 128 && (i & 1) ? odd : even,
+                    seg * kRowsPer * ld + k0);
     }
   }
 };
+
+// The E8M0 codes of a tile's rows (A's, then B's) by loads straight into LDS.  L2 answers
+// a load of 4 bytes per row with as many requests as one of 64, and the tile kernels come
+// near its request rate: read by every lane for its own rows and stage, the codes took 20%
+// of the kernel at 4096 x 4096 x 16384, loaded as dwords for every stage 4%.
+//
+// !WIDE: rows of codes that start at dwords and K a multiple of 128 of at least 512.  A load takes 16
+// codes of a row, which serve the kBuffers stages of one turn of the loop.
+// WIDE: rows of codes that start anywhere, any K.  The dwords that hold a row's codes of a
+// stage, one load each: plane d has dword d of every row, and a shift brings the codes
+// down.  The outer bytes of those dwords may belong to the neighbouring rows, or to
+// nothing: they share a dword with a code of this row, so they can be read, and they are
+// not used.
+template <int BM, int BN, int NW, int STEPS, bool WIDE>
+struct CodeLoader {
+  static constexpr int kPlane = (BM + BN) * 4;
+  static constexpr int kDwords = STEPS / 2 + 1;           // WIDE: per stage
+  static constexpr int kBytes = WIDE ? kDwords * kPlane : (BM + BN) * 16;
+  static constexpr int kPerWave = (BM + BN) / (64 * NW);  // groups of 64 rows per wave
+  static constexpr int kLoads = kPerWave * (WIDE ? kDwords : 1);
+  __amdgpu_buffer_rsrc_t ra, rb;
+  int lda, ldb, w, lane, mis_a, mis_b, nblk;
+
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* sc, int64_t ld,
+                                                                int64_t row0, int64_t rows,
+                                                                int64_t most, int nblk, int& mis) {
+    const uint8_t* p = sc + row0 * ld;
+    mis = WIDE ? (int)(reinterpret_cast<uintptr_t>(p) & 3u) : 0;
+    const int64_t left = rows - row0 < most ? rows - row0 : most;
+    return byte_rsrc(p - mis, ((left - 1) * ld + nblk + mis + 3) & ~int64_t(3));
+  }
+  __device__ __forceinline__ CodeLoader(const Mxfp4Gemm& p, int64_t m0, int64_t n0, int tid) {
+    lda = (int)p.ldsa;
+    ldb = (int)p.ldsb;
+    lane = tid & 63;
+    w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    nblk = (int)(p.K / 32);
+    ra = rsrc(p.sc_a, p.ldsa, m0, p.M, BM, nblk, mis_a);
+    rb = rsrc(p.sc_b, p.ldsb, n0, p.N, BN, nblk, mis_b);
+  }
+  // !WIDE: the first block of the load that serves the stages from k on (in the row still)
+  __device__ __forceinline__ int first(int k) const { return min(2 * STEPS * k, nblk - 16); }
+
+  // the codes of stage k (WIDE) or of the stages from k on
+  __device__ __forceinline__ void issue(int k, uint8_t* lds) const {
+#pragma unroll
+    for (int x = 0; x < kPerWave; ++x) {
+      constexpr int kSegA = BM / 64;
+      const int seg = NW * x + w;
+      const bool of_a = kSegA % NW == 0 ? x < kSegA / NW : seg < kSegA;
+      const int ld = of_a ? lda : ldb, row = (of_a ? seg : seg - kSegA) * 64;
+      if constexpr (!WIDE) {
+        load_to_lds16(of_a ? ra : rb, lds + seg * 1024, lane * ld, row * ld + first(k));
+      } else {
+        const int at = ((row + lane) * ld + (of_a ? mis_a : mis_b)) & ~3;
+        const int to = 2 * STEPS * k < nblk ? at : kNowhere;
+#pragma unroll
+        for (int d = 0; d < kDwords; ++d)
+          load_to_lds4(of_a ? ra : rb, lds + d * kPlane + seg * 256, to, 2 * STEPS * k + 4 * d);
+      }
+    }
+  }
+  // Codes of half h of row i of the tile (A's rows, then B's), byte s for step s.  `off`
+  // (!WIDE): the half's first block of the stage less first(); `shift` (WIDE): 8 times the
+  // place of the row's first code in its dword.
+  static __device__ __forceinline__ uint32_t read(const uint8_t* lds, int i, int h, int off,
+                                                  uint32_t shift) {
+    if constexpr (WIDE) {
+      const uint8_t* q = lds + i * 4 + (STEPS == 4 ? h * kPlane : 0);
+      const uint32_t lo = *reinterpret_cast<const uint32_t*>(q);
+      const uint32_t hi = *reinterpret_cast<const uint32_t*>(q + kPlane);
+      return (uint32_t)((((uint64_t)hi << 32) | lo) >> (shift + (STEPS == 4 ? 0 : 16 * h)));
+    } else if constexpr (STEPS == 4) {
+      return *reinterpret_cast<const uint32_t*>(lds + i * 16 + off);
+    } else {
+      return *reinterpret_cast<const uint16_t*>(lds + i * 16 + off);
+    }
+  }
+};
+
+// Barrier of a stage: every wave's reads of LDS are done, and all but its last N loads.
+// (__syncthreads would wait for all loads.)  The fences order this thread's accesses for
+// the compiler and wait for nothing.
+template <int N>
+__device__ __forceinline__ void stage_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  // vmcnt N, lgkmcnt 0, expcnt unconstrained
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // The order of a step: DS fragment reads and VM loads spread over its MF MFMAs, the reads
 // over the first three quarters so that the last of them has arrived for the next step.
@@ -204,59 +364,24 @@ __device__ __forceinline__ v16f mfma_tile(const v8i& b, const v8i& a, const v16f
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 4, kMfmaFormat<FA>, OP, sb, OP, sa);
 }
 
-// E8M0 codes of a tile's rows, 16 blocks of each at a time, by loads straight into LDS
-// (16 bytes per row: row i of A, then of B).  Read from memory by every lane for its own
-// rows and stage, they cost as many cache lines as the elements themselves: half the
-// kernel's time at 4096 x 4096 x 16384.
-template <int FA, int BM, int BN, int NW>
-struct ScaleTiles {
-  static constexpr int NS = TileShape<FA>::NS;
-  static constexpr int kStages = 16 / (2 * NS);      // stages served by a load
-  static constexpr int kBytes = (BM + BN) * 16;
-  static constexpr int kPerWave = (BM + BN) / (64 * NW);
-
-  // The first block of group g's load: the last group stays inside the row.
-  static __device__ __forceinline__ int first(int g, int nblk) { return min(16 * g, nblk - 16); }
-
-  static __device__ __forceinline__ void issue(__amdgpu_buffer_rsrc_t ca, __amdgpu_buffer_rsrc_t cb,
-                                               int lda, int ldb, int g, int nblk, int w, int lane,
-                                               uint8_t* dst) {
-    const int wv = __builtin_amdgcn_readfirstlane(w), f = first(g, nblk);
-    // 64 rows per instruction, no branch
-#pragma unroll
-    for (int x = 0; x < kPerWave; ++x) {
-      constexpr int kSegA = BM / 64;
-      const int seg = NW * x + wv;
-      const bool of_a = kSegA % NW == 0 ? x < kSegA / NW : seg < kSegA;
-      const int ld = of_a ? lda : ldb, row = (of_a ? seg : seg - kSegA) * 64;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          of_a ? ca : cb, (void __attribute__((address_space(3)))*)(dst + seg * 1024), 16, lane * ld,
-          row * ld + f, 0, 0);
-    }
-  }
-};
-
-// The codes of a tile's rows: reads outside them give 0.
-template <int ROWS>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_rsrc(const uint8_t* sc, int64_t ld,
-                                                             int64_t row0, int64_t rows, int nblk) {
-  const int64_t left = rows - row0 < ROWS ? rows - row0 : ROWS;
-  return byte_rsrc(sc + row0 * ld, (left - 1) * ld + nblk);
-}
-
-template <int FA, int BM, int BN, int GM, int GN>
+// The stages are variables of their own, and the loop names them: the compiler then knows
+// that a fragment read does not touch a buffer being loaded, and does not wait for the
+// loads in flight before each of them.
+template <int FA, int BM, int BN, int GM, int GN, bool WIDE>
 __global__ __launch_bounds__(64 * GM * GN, 2) void gemm_mxfp4_tile_kernel(Mxfp4Gemm p, int tiles_m,
                                                                          int tiles_n) {
-  using S = TileShape<FA>;
-  constexpr int NS = S::NS, NW = GM * GN, WM = BM / GM, WN = BN / GN, MI = WM / 32, NI = WN / 32;
-  using SC = ScaleTiles<FA, BM, BN, NW>;
-  constexpr int kA = BM * S::RA, kB = BN * S::RB, kStage = kA + kB + SC::kBytes;
-  constexpr int kOut = BM * BN;  // half of the BF16 tile on its way out
-  // The two stages are two variables, and the loop below names them: the compiler then
-  // knows that a fragment read does not touch the buffer being loaded, and does not wait
-  // for the loads in flight before each of them.
-  __shared__ __attribute__((aligned(1024))) uint8_t lds0[kStage > kOut ? kStage : kOut];
-  __shared__ __attribute__((aligned(1024))) uint8_t lds1[kStage > kOut ? kStage : kOut];
+  using S = Stage<FA>;
+  constexpr int NW = GM * GN, WM = BM / GM, WN = BN / GN, MI = WM / 32, NI = WN / 32;
+  constexpr int NS = S::kSteps, NBUF = S::kBuffers, RA = S::kRowA, RB = S::kRowB;
+  using Codes = CodeLoader<BM, BN, NW, NS, WIDE>;
+  constexpr int kA = BM * RA, kB = BN * RB, kStage = kA + kB + (WIDE ? Codes::kBytes : 0);
+  // the BF16 tile on its way out takes the stages' place, kOutWaves waves to each
+  constexpr int kOutWaves = (NW + NBUF - 1) / NBUF, kOut = kOutWaves * WM * WN * 2;
+  constexpr int kBuf = kStage > kOut ? kStage : kOut;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[kBuf];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds1[kBuf];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds2[NBUF == 3 ? kBuf : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t codes[WIDE ? 16 : Codes::kBytes];
   __shared__ uint32_t red[2 * NW];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int r = lane & 31, h = lane >> 5;
@@ -265,23 +390,29 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void gemm_mxfp4_tile_kernel(Mxfp4G
   tile_coords(blockIdx.x, tiles_m, tiles_n, tm, tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int row_a = (int)(FA == kE2M1 ? p.K / 2 : p.K), row_b = (int)(p.K / 2);
-  const TileLoader<BM, S::RA, NW> la(p.A, FA == kE2M1 ? p.lda / 2 : p.lda, m0, p.M, row_a, tid);
-  const TileLoader<BN, S::RB, NW> lb(p.B, p.ldb / 2, n0, p.N, row_b, tid);
   const int nblk = (int)(p.K / 32);
-  const __amdgpu_buffer_rsrc_t ca = scale_rsrc<BM>(p.sc_a, p.ldsa, m0, p.M, nblk);
-  const __amdgpu_buffer_rsrc_t cb = scale_rsrc<BN>(p.sc_b, p.ldsb, n0, p.N, nblk);
-  // this lane's fragment chunks in a row of LDS, one per load of a stage
-  int oa[S::RA == 128 && FA != kE2M1 ? 2 * NS : NS], ob[NS];
+  const TileLoader<BM, RA, NW> la(p.A, FA == kE2M1 ? p.lda / 2 : p.lda, m0, p.M, row_a, tid);
+  const TileLoader<BN, RB, NW> lb(p.B, p.ldb / 2, n0, p.N, row_b, tid);
+  const Codes lc(p, m0, n0, tid);
+  // this lane's fragment chunks in a row of LDS
+  int oa[FA == kE2M1 ? NS : 2 * NS], ob[NS];
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
     if constexpr (FA == kE2M1) {
-      oa[s] = chunk_off<S::RA>(r, NS * h + s);
+      oa[s] = chunk_off<RA>(r, NS * h + s);
     } else {  // a lane holds half h of the blocks of both lane halves: s and NS + s
-      oa[s] = chunk_off<S::RA>(r, 2 * s + h);
-      oa[NS + s] = chunk_off<S::RA>(r, 2 * (NS + s) + h);
+      oa[s] = chunk_off<RA>(r, 2 * s + h);
+      oa[NS + s] = chunk_off<RA>(r, 2 * (NS + s) + h);
     }
-    ob[s] = chunk_off<S::RB>(r, NS * h + s);
+    ob[s] = chunk_off<RB>(r, NS * h + s);
   }
+  uint32_t sha[MI], shb[NI];  // WIDE: the shift of each row's codes
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+    sha[i] = WIDE ? 8u * (((wm + 32 * i + r) * lc.lda + lc.mis_a) & 3) : 0u;
+#pragma unroll
+  for (int j = 0; j < NI; ++j)
+    shb[j] = WIDE ? 8u * (((wn + 32 * j + r) * lc.ldb + lc.mis_b) & 3) : 0u;
   v16f acc[MI][NI];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
@@ -290,32 +421,46 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void gemm_mxfp4_tile_kernel(Mxfp4G
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  const int nst = (int)((p.K + S::KST - 1) / S::KST);
+  const int nst = (int)((p.K + S::K - 1) / S::K);
   int sa[MI], sb[NI];
+  uint32_t pa_next[MI], pb_next[NI];  // codes read a stage ahead
   v8i fa[2][MI], fb[2][NI];
-  // the loads of stage k: elements of A, of B, codes of both
+  // the loads of stage k (zeros for k >= nst)
   auto issue = [&](int k, uint8_t* dst) {
-    la.issue(k * S::RA, row_a, dst);
-    lb.issue(k * S::RB, row_b, dst + kA);
-    SC::issue(ca, cb, (int)p.ldsa, (int)p.ldsb, k / SC::kStages, nblk, w, lane, dst + kA + kB);
+    la.issue(k * RA, row_a, dst);
+    lb.issue(k * RB, row_b, dst + kA);
+    if constexpr (WIDE) lc.issue(k, dst + kA + kB);
+  };
+  constexpr int kLoads = la.kPerWave + lb.kPerWave + (WIDE ? lc.kLoads : 0);
+  // Codes of stage k for this lane's rows and half, out of the load for the stages from k0
+  // on.  Blocks past the end of K take code 0: their elements are zeros, and a zero times
+  // any power of two is zero, while the byte there may be the code of NaN.
+  auto read_codes = [&](int k, int k0, const uint8_t* src, uint32_t (&ca)[MI], uint32_t (&cb)[NI]) {
+    const int block = 2 * NS * k + NS * h, left = nblk - block;
+    const uint32_t mask = left >= NS ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+    const int off = WIDE ? 0 : min(block - lc.first(k0), 16 - NS);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) ca[i] = Codes::read(src, wm + 32 * i + r, h, off, sha[i]) & mask;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) cb[j] = Codes::read(src, BM + wn + 32 * j + r, h, off, shb[j]) & mask;
   };
   // fragments of step s of the stage in `src`, into register set s & 1
   auto frags = [&](const uint8_t* src, auto step) {
     constexpr int s = decltype(step)::value;
-    const uint8_t *pa = src + wm * S::RA, *pb = src + kA + wn * S::RB;
+    const uint8_t *pa = src + wm * RA, *pb = src + kA + wn * RB;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const u32x4 d = *reinterpret_cast<const u32x4*>(pa + oa[s] + 32 * i * S::RA);
+      const u32x4 d = *reinterpret_cast<const u32x4*>(pa + oa[s] + 32 * i * RA);
       fa[s & 1][i] = v8i{(int)d[0], (int)d[1], (int)d[2], (int)d[3], 0, 0, 0, 0};
       if constexpr (FA != kE2M1) {
-        const u32x4 e = *reinterpret_cast<const u32x4*>(pa + oa[NS + s] + 32 * i * S::RA);
+        const u32x4 e = *reinterpret_cast<const u32x4*>(pa + oa[NS + s] + 32 * i * RA);
 #pragma unroll
         for (int x = 0; x < 4; ++x) fa[s & 1][i][4 + x] = (int)e[x];
       }
     }
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      const u32x4 d = *reinterpret_cast<const u32x4*>(pb + ob[s] + 32 * j * S::RB);
+      const u32x4 d = *reinterpret_cast<const u32x4*>(pb + ob[s] + 32 * j * RB);
       fb[s & 1][j] = v8i{(int)d[0], (int)d[1], (int)d[2], (int)d[3], 0, 0, 0, 0};
     }
   };
@@ -328,33 +473,35 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void gemm_mxfp4_tile_kernel(Mxfp4G
         acc[i][j] = mfma_tile<FA, s>(fb[s & 1][j], fa[s & 1][i], acc[i][j], sb[j], sa[i]);
   };
   using std::integral_constant;
-  // One stage, from its barrier on.  The fragments of a step are read while the step
-  // before it is multiplied, so the previous stage's last step comes first here, and the
-  // loads of the next stage start beside it, into the buffer that this barrier freed.
-  auto stage = [&](int k, const uint8_t* rd, uint8_t* wr) {
-    // the codes of this lane's rows and half, byte s for step s; blocks past the end of K
-    // take code 0 (their elements are zeros), and so do rows past the edge
-    const int off = k * (2 * NS) + NS * h - SC::first(k / SC::kStages, nblk);
-    const bool in = off <= 16 - NS;
-    const uint8_t* src = rd + kA + kB + r * 16 + (in ? off : 0);
-    int na[MI], nb[NI];
+  // Stage k, from its barrier on, as number G of a turn of the loop.  The fragments of a
+  // step are read while the step before it is multiplied, so the previous stage's last step
+  // comes first here; and the loads of stage k + NBUF - 1 start beside it, into the buffer
+  // that this barrier freed.  !WIDE: the turn's last stage has had its codes read by the
+  // one before it, and loads the next turn's into their place.
+  auto stage = [&](int k, const uint8_t* rd, uint8_t* wr, auto number) {
+    constexpr int G = decltype(number)::value;
+    constexpr bool kLast = !WIDE && G == NBUF - 1, kAhead = !WIDE && G == NBUF - 2;
+    stage_barrier<(NBUF - 2) * kLoads>();  // all but the loads of later stages have arrived
+    uint32_t ca[MI], cb[NI];
+    if constexpr (kLast) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const uint8_t* q = src + (wm + 32 * i) * 16;
-      na[i] = NS == 4 ? *reinterpret_cast<const int*>(q) : *reinterpret_cast<const uint16_t*>(q);
-    }
+      for (int i = 0; i < MI; ++i) ca[i] = pa_next[i];
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const uint8_t* q = src + (BM + wn + 32 * j) * 16;
-      nb[j] = NS == 4 ? *reinterpret_cast<const int*>(q) : *reinterpret_cast<const uint16_t*>(q);
+      for (int j = 0; j < NI; ++j) cb[j] = pb_next[j];
+      lc.issue(k + 1, codes);
+      // no load may pass them: the next barrier counts on the codes being the older ones
+      __builtin_amdgcn_sched_barrier(0x78F);
+    } else {
+      read_codes(k, k - G, WIDE ? rd + kA + kB : codes, ca, cb);
+      if constexpr (kAhead) read_codes(k + 1, k - G, codes, pa_next, pb_next);
     }
     frags(rd, integral_constant<int, 0>{});
-    issue(k + 1, wr);
+    issue(k + NBUF - 1, wr);
     mfmas(integral_constant<int, NS - 1>{});
 #pragma unroll
-    for (int i = 0; i < MI; ++i) sa[i] = in ? na[i] : 0;
+    for (int i = 0; i < MI; ++i) sa[i] = (int)ca[i];
 #pragma unroll
-    for (int j = 0; j < NI; ++j) sb[j] = in ? nb[j] : 0;
+    for (int j = 0; j < NI; ++j) sb[j] = (int)cb[j];
     frags(rd, integral_constant<int, 1>{});
     mfmas(integral_constant<int, 0>{});
     if constexpr (NS == 4) {
@@ -365,14 +512,10 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void gemm_mxfp4_tile_kernel(Mxfp4G
     }
     // issue order: fragment reads and loads between the MFMAs that hide them
     constexpr int kReads = MI * (FA == kE2M1 ? 1 : 2) + NI, kMf = MI * NI;
-    interleave<kMf, kReads + MI + NI, la.kPerWave + lb.kPerWave + SC::kPerWave>();
+    constexpr int kCodeReads = (MI + NI) * (WIDE ? 2 : kLast ? 0 : kAhead ? 2 : 1);
+    interleave<kMf, kReads + kCodeReads, kLoads>();
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s) interleave<kMf, kReads, 0>();
-  };
-  // this wave's loads have arrived, then everyone's
-  auto arrived = [] {
-    vmem_wait_all();
-    __syncthreads();
   };
   if (nst > 0) {
     // "the last step of the stage before the first": zeros
@@ -386,24 +529,38 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void gemm_mxfp4_tile_kernel(Mxfp4G
       sb[j] = 127;
       fb[1][j] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
     }
-    // Stages go in pairs, an odd first one by itself.  The last one's loads are issued
-    // too (what lies past K reads as zeros without reaching memory): a loop that leaves
-    // them out, or that can end between the two stages, was compiled to copies of the
-    // accumulators.
+    // Stages go NBUF at a time.  Of two, an odd one comes first and by itself (a loop that
+    // can end between them was compiled to copies of the accumulators); of three, the last
+    // turn is filled up with stages of zeros.  The loads past the last stage are issued too:
+    // they give zeros and do not reach memory.
+    constexpr integral_constant<int, 0> k0th{};
+    constexpr integral_constant<int, 1> k1st{};
     int k = 0;
-    if (nst & 1) {
-      issue(0, lds1);
-      arrived();
-      stage(0, lds1, lds0);
-      k = 1;
+    if constexpr (!WIDE) lc.issue(0, codes);
+    if constexpr (NBUF == 2) {
+      if (nst & 1) {
+        issue(0, lds1);
+        if constexpr (!WIDE) {
+          stage_barrier<0>();
+          read_codes(0, 0, codes, pa_next, pb_next);
+        }
+        stage(0, lds1, lds0, k1st);
+        k = 1;
+      } else {
+        issue(0, lds0);
+      }
+      for (; k < nst; k += 2) {
+        stage(k, lds0, lds1, k0th);
+        stage(k + 1, lds1, lds0, k1st);
+      }
     } else {
       issue(0, lds0);
-    }
-    for (; k < nst; k += 2) {
-      arrived();
-      stage(k, lds0, lds1);
-      arrived();
-      stage(k + 1, lds1, lds0);
+      issue(1, lds1);
+      for (; k < nst; k += 3) {
+        stage(k, lds0, lds2, k0th);
+        stage(k + 1, lds1, lds0, k1st);
+        stage(k + 2, lds2, lds1, integral_constant<int, 2>{});
+      }
     }
     mfmas(integral_constant<int, NS - 1>{});
   }
@@ -414,8 +571,10 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void gemm_mxfp4_tile_kernel(Mxfp4G
   uint32_t amax = 0;
   const int64_t cm = m0 + wm, cn = n0 + wn;
   if (p.out_bf16) {
-    arrived();  // the tiles in LDS are done with
-    uint8_t* out = (w >= NW / 2 ? lds1 : lds0) + w % (NW / 2) * (WM * WN * 2);
+    vmem_wait_all();
+    __syncthreads();  // the stages in LDS are done with
+    const int part = w / kOutWaves;
+    uint8_t* out = (part == 0 ? lds0 : part == 1 ? lds1 : lds2) + w % kOutWaves * (WM * WN * 2);
     constexpr int CH = WN / 8;  // 16-byte chunks per row
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -499,28 +658,49 @@ static hipError_t launch_direct(const Mxfp4Gemm& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int FA, int BM, int BN, int GM, int GN>
+template <int FA, int BM, int BN, int GM, int GN, bool WIDE>
 static hipError_t launch_tile(const Mxfp4Gemm& p, hipStream_t stream) {
   const int tm = (int)((p.M + BM - 1) / BM), tn = (int)((p.N + BN - 1) / BN);
-  hipLaunchKernelGGL((gemm_mxfp4_tile_kernel<FA, BM, BN, GM, GN>), dim3((unsigned)(tm * tn)), dim3(64 * GM * GN), 0,
-                     stream, p, tm, tn);
+  hipLaunchKernelGGL((gemm_mxfp4_tile_kernel<FA, BM, BN, GM, GN, WIDE>), dim3((unsigned)(tm * tn)),
+                     dim3(64 * GM * GN), 0, stream, p, tm, tn);
   return hipGetLastError();
 }
 
+// Which kernel (times in us, one MI355X, FP4 x FP4 unless stated):
+//  - up to 16 rows, direct: 16 x 16 outputs and 8 waves, or 16 x 32 and 4 waves where those
+//    still give every CU a workgroup: 1 x 14336 x 4096 8.7 and 8.4 (FP8 A 11.6 and 9.3),
+//    13 x 4096 x 14336 9.9 and 14.8;
+//  - few outputs, direct with 32 x 32: up to one workgroup per CU (64 x 4096 x 4096: 6.9, on
+//    128 x 128 tiles 13.2), with 8 waves, or 4 for an FP8 A, whose operands would spill; up
+//    to two per CU for an FP4 A, with 4 waves (32 x 14336 x 4096: 12.6, tiles 14.2; with an
+//    FP8 A 18.5, tiles 16);
+//  - 256 x 256 tiles where they give every CU one, else 128 x 128 (8192 x 1024 x 4096: 24,
+//    on 256 x 256 tiles 33; 4096 x 4096 x 4128 with an FP8 A: 90, on 128 x 128 tiles 129).
 template <int FA>
 static hipError_t launch_fa(const Mxfp4Gemm& p, int num_cus, hipStream_t stream) {
-  if (p.M <= 16) return launch_direct<FA, 1, 1, 8>(p, stream);
-  // The tile loads address their rows with 30 bits; the codes' loads take 16 blocks of a
-  // row at a time, at addresses that are a multiple of 4.
-  const bool scales_aligned = ((reinterpret_cast<uintptr_t>(p.sc_a) | (uint64_t)p.ldsa |
-                                reinterpret_cast<uintptr_t>(p.sc_b) | (uint64_t)p.ldsb |
-                                (uint64_t)(p.K / 32)) & 3u) == 0;
-  const bool fits = p.lda < (1 << 21) && p.ldb < (1 << 21) && p.ldsa < (1 << 21) &&
-                    p.ldsb < (1 << 21) && p.K >= 512 && scales_aligned;
-  if (!fits) return launch_direct<FA, 4, 4, 1>(p, stream);
+  if (p.M <= 16) {
+    if ((p.N + 31) / 32 >= num_cus) return launch_direct<FA, 1, 2, 4>(p, stream);
+    return launch_direct<FA, 1, 1, 8>(p, stream);
+  }
+  const int64_t small = ((p.M + 31) / 32) * ((p.N + 31) / 32);
+  if constexpr (FA == kE2M1) {
+    if (small <= num_cus) return launch_direct<FA, 2, 2, 8>(p, stream);
+  }
+  // the tile loads address their rows with 30 bits
+  const int64_t most = 1 << 21;
+  if (p.lda >= most || p.ldb >= most || p.ldsa >= most || p.ldsb >= most ||
+      small <= (FA == kE2M1 ? 2 : 1) * num_cus)
+    return launch_direct<FA, 2, 2, 4>(p, stream);
+  // where a load may take 16 codes of a row at a dword address (CodeLoader)
+  const bool wide = p.K < 512 || ((reinterpret_cast<uintptr_t>(p.sc_a) | (uint64_t)p.ldsa |
+                                   reinterpret_cast<uintptr_t>(p.sc_b) | (uint64_t)p.ldsb |
+                                   (uint64_t)(p.K / 32)) & 3u) != 0;
   const int64_t big = ((p.M + 255) / 256) * ((p.N + 255) / 256);
-  if (big >= num_cus) return launch_tile<FA, 256, 256, 4, 2>(p, stream);
-  return launch_tile<FA, 128, 128, 2, 2>(p, stream);
+  if (big >= num_cus)
+    return wide ? launch_tile<FA, 256, 256, 4, 2, true>(p, stream)
+                : launch_tile<FA, 256, 256, 4, 2, false>(p, stream);
+  return wide ? launch_tile<FA, 128, 128, 2, 2, true>(p, stream)
+              : launch_tile<FA, 128, 128, 2, 2, false>(p, stream);
 }
 
 hipError_t launch_gemm_mxfp4(const Mxfp4Gemm& p, int fa, int num_cus, hipStream_t stream) {
