@@ -15,6 +15,7 @@ Functions keep the C names: ``fp8ds_amax``, ``fp8ds_cast``, ``fp8ds_cast_health`
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -145,12 +146,20 @@ def lib():
 _recording = threading.local()
 
 
+_fns = {}
+
+
 def _call(name: str, *args):
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
     rec = getattr(_recording, "calls", None)
     if rec is not None:
-        rec.append((getattr(lib(), name), args))
+        rec.append((fn, args))
         return
-    _check(getattr(lib(), name)(*args))
+    status = fn(*args)
+    if status:
+        _check(status)
 
 
 def prepare(fn):
@@ -184,18 +193,34 @@ def _check(status: int):
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
 
-def _stream(stream):
-    if stream is None:
+_raw_stream = None
+
+
+def _current_stream():
+    """The current stream's handle: ``torch.cuda.current_stream().cuda_stream`` without the
+    Stream object, which costs as much as a kernel launch."""
+    global _raw_stream
+    if _raw_stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        get, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream",
+                                                         "_cuda_getDevice"))
+        if get is None or dev is None:  # not in this torch
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            torch.cuda.init()
+            _raw_stream = lambda: get(dev())  # noqa: E731
+    return _raw_stream()
+
+
+def _stream(stream):
+    if stream is None:
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -751,19 +776,38 @@ def fp8ds_rmsnorm_bwd(dy, h, rstd, gamma, dx, dgamma, workspace, dres=None, fmt=
           _vec(sat_count, "sat_count", (torch.int64,), 1), _stream(stream))
 
 
+class _Address(int):
+    """The address of an array that lives as long as this number does."""
+
+    keep = None
+
+
+def _host_array(kind, values):
+    a = array.array(kind, values)
+    p = _Address(a.buffer_info()[0])
+    p.keep = a
+    return p
+
+
 def _tensor_list(ts, name):
-    """(addresses, dtype codes, counts) of dense high-precision tensors, as C arrays."""
-    high, n = _high(), len(ts)
-    for i, t in enumerate(ts):
-        if not t.is_cuda:
-            raise ValueError(f"{name}[{i}]: expected a CUDA tensor")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}[{i}]: expected a contiguous tensor")
-        if t.dtype not in high:
-            raise TypeError(f"{name}[{i}]: dtype {t.dtype} not in {tuple(high)}")
-    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in ts]),
-            (ctypes.c_int * n)(*[high[t.dtype] for t in ts]),
-            (ctypes.c_int64 * n)(*[t.numel() for t in ts]))
+    """(addresses, dtype codes, counts) of dense high-precision tensors as host arrays, and the
+    counts as a list."""
+    import torch
+
+    high, T = _high(), torch.Tensor
+    types = [t.dtype for t in ts]
+    if not (all(map(T.is_contiguous, ts)) and all([t.is_cuda for t in ts])
+            and high.keys() >= set(types)):
+        for i, t in enumerate(ts):
+            if not t.is_cuda:
+                raise ValueError(f"{name}[{i}]: expected a CUDA tensor")
+            if not t.is_contiguous():
+                raise ValueError(f"{name}[{i}]: expected a contiguous tensor")
+            if t.dtype not in high:
+                raise TypeError(f"{name}[{i}]: dtype {t.dtype} not in {tuple(high)}")
+    n = list(map(T.numel, ts))
+    return (_host_array("Q", list(map(T.data_ptr, ts))),
+            _host_array("i", [high[d] for d in types]), _host_array("q", n), n)
 
 
 def fp8ds_grad_norm_workspace() -> int:
@@ -777,7 +821,7 @@ def fp8ds_grad_norm(grads, max_norm, norm, coef=None, workspace=None, grad_scale
     :func:`fp8ds_grad_norm_workspace` bytes (needed above 65536 elements or 128 tensors)."""
     import torch
 
-    p, ty, n = _tensor_list(grads, "grads")
+    p, ty, n, _ = _tensor_list(grads, "grads")
     f32 = (torch.float32,)
     _call("fp8ds_grad_norm", len(grads), p, ty, n, float(grad_scale), float(max_norm),
           _vec(norm, "norm", f32, 1), _vec(coef, "coef", f32, 1),
@@ -790,15 +834,12 @@ def fp8ds_grad_clip(grads, coef, out=None, stream=None):
     tensors ``out`` (of the same sizes; bf16 or fp32)."""
     import torch
 
-    p, ty, n = _tensor_list(grads, "grads")
+    p, ty, n, counts = _tensor_list(grads, "grads")
     op = oty = None
     if out is not None:
-        if len(out) != len(grads):
-            raise ValueError(f"out: {len(out)} tensors for {len(grads)} gradients")
-        op, oty, on = _tensor_list(out, "out")
-        for i in range(len(grads)):
-            if on[i] != n[i]:
-                raise ValueError(f"out[{i}]: {on[i]} elements for {n[i]}")
+        op, oty, _, out_counts = _tensor_list(out, "out")
+        if out_counts != counts:
+            raise ValueError(f"out: sizes {out_counts} for gradients of {counts}")
     _call("fp8ds_grad_clip", len(grads), p, ty, n, op, oty, _vec(coef, "coef", (torch.float32,), 1),
           _stream(stream))
 
@@ -840,7 +881,7 @@ def fp8ds_gemm_mxfp4(M, N, K, a, fa, lda, scales_a, ld_scales_a, b, ldb, scales_
 
     u8, high = (torch.uint8,), _high()
     if K > 0:
-        pa, pb = (2 if fa == E2M1 else 1), 2
+        pa, pb = (2 if fa == E2M1 else 1), 2  # elements per byte
         _need(a, "a", u8, _span(M, K // pa, lda // pa), contiguous=False)
         _need(b, "b", u8, _span(N, K // pb, ldb // pb), contiguous=False)
         _need(scales_a, "scales_a", u8, _span(M, K // 32, ld_scales_a), contiguous=False)
