@@ -997,7 +997,7 @@ int fp8ds_cast_mxfp4(const void* x, fp8ds_dtype xt, int64_t rows, int64_t cols, 
   if (!aligned16(x) || !aligned16(q) || (q_t && !aligned16(q_t)))
     return fail(FP8DS_ERR_ALIGN, "%s: x, q and q_t must be 16-byte aligned", who);
   if (!q_t)
-    return hip_status(fp8ds::launch_mxfp4_cast(x, xt == FP8DS_BF16, n, q, scales, stream), who);
+    return hip_status(fp8ds::launch_mxfp4_cast(x, xt == FP8DS_BF16, n, q, scales, num_cus(), stream), who);
   if (rows % 32 != 0)
     return fail(FP8DS_ERR_SHAPE, "%s: a transposed copy needs rows in multiples of 32 (got %lld)",
                 who, (long long)rows);

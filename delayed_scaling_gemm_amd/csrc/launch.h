@@ -242,7 +242,7 @@ hipError_t launch_grad_clip(const TensorTable& tb, const float* coef, hipStream_
 
 // MXFP4 casts (n a multiple of 32; rows and cols multiples of 32) and back.
 hipError_t launch_mxfp4_cast(const void* x, bool bf16, int64_t n, uint8_t* q, uint8_t* scales,
-                             hipStream_t stream);
+                             int num_cus, hipStream_t stream);
 hipError_t launch_mxfp4_cast_transpose(const void* x, bool bf16, int64_t rows, int64_t cols,
                                        uint8_t* q, uint8_t* scales, uint8_t* qt, uint8_t* scales_t,
                                        hipStream_t stream);

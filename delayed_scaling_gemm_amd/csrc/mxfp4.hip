@@ -20,8 +20,6 @@
 
 namespace fp8ds {
 
-constexpr int kFp4Pieces = 8;  // 16-byte pieces per thread
-
 template <bool BF16>
 __device__ __forceinline__ void piece_values(const u32x4& d, float (&v)[8]) {
 #pragma unroll
@@ -58,21 +56,23 @@ __device__ __forceinline__ void store_piece(uint8_t* q, int64_t piece, const u32
     __builtin_nontemporal_store((uint16_t)c, reinterpret_cast<uint16_t*>(q) + piece);
 }
 
-template <bool BF16>
+// P 16-byte pieces per thread: 8, or 1 where 8 would leave CUs without a workgroup
+// (13 x 14336 BF16: 4.1 us with 8).
+template <bool BF16, int P>
 __global__ __launch_bounds__(256) void mxfp4_cast_kernel(const void* __restrict__ x,
                                                          int64_t npieces, uint8_t* __restrict__ q,
                                                          uint8_t* __restrict__ scales) {
   constexpr int PPB = BF16 ? 4 : 8;  // pieces (lanes) per block
-  const int64_t base = (int64_t)blockIdx.x * 256 * kFp4Pieces + threadIdx.x;
+  const int64_t base = (int64_t)blockIdx.x * 256 * P + threadIdx.x;
   const u32x4* xv = static_cast<const u32x4*>(x);
-  u32x4 v[kFp4Pieces];
+  u32x4 v[P];
 #pragma unroll
-  for (int j = 0; j < kFp4Pieces; ++j) {
+  for (int j = 0; j < P; ++j) {
     const int64_t pc = base + 256 * j;
     v[j] = pc < npieces ? __builtin_nontemporal_load(xv + pc) : u32x4{0u, 0u, 0u, 0u};
   }
 #pragma unroll
-  for (int j = 0; j < kFp4Pieces; ++j) {
+  for (int j = 0; j < P; ++j) {
     const int64_t pc = base + 256 * j;  // a block's lanes are all in range or all out
     const uint32_t code = mx_code(row_block_amax<BF16>(v[j]), 2u);
     if (pc < npieces) {
@@ -203,15 +203,23 @@ __global__ __launch_bounds__(256) void mxfp4_dequant_kernel(const uint8_t* __res
 
 // ------------------------------------------------------------------ host launchers
 
-hipError_t launch_mxfp4_cast(const void* x, bool bf16, int64_t n, uint8_t* q, uint8_t* scales,
-                             hipStream_t stream) {
-  const int64_t npieces = n / (bf16 ? 8 : 4), per = 256 * kFp4Pieces;
-  const dim3 grid((unsigned)((npieces + per - 1) / per));
-  if (bf16)
-    hipLaunchKernelGGL((mxfp4_cast_kernel<true>), grid, dim3(256), 0, stream, x, npieces, q, scales);
+template <bool BF16>
+static hipError_t launch_cast4(const void* x, int64_t n, uint8_t* q, uint8_t* scales, int num_cus,
+                               hipStream_t stream) {
+  const int64_t npieces = n / (BF16 ? 8 : 4);
+  if (npieces < 256 * 8 * (int64_t)num_cus)
+    hipLaunchKernelGGL((mxfp4_cast_kernel<BF16, 1>), dim3((unsigned)((npieces + 255) / 256)), dim3(256),
+                       0, stream, x, npieces, q, scales);
   else
-    hipLaunchKernelGGL((mxfp4_cast_kernel<false>), grid, dim3(256), 0, stream, x, npieces, q, scales);
+    hipLaunchKernelGGL((mxfp4_cast_kernel<BF16, 8>), dim3((unsigned)((npieces + 2047) / 2048)),
+                       dim3(256), 0, stream, x, npieces, q, scales);
   return hipGetLastError();
+}
+
+hipError_t launch_mxfp4_cast(const void* x, bool bf16, int64_t n, uint8_t* q, uint8_t* scales,
+                             int num_cus, hipStream_t stream) {
+  return bf16 ? launch_cast4<true>(x, n, q, scales, num_cus, stream)
+              : launch_cast4<false>(x, n, q, scales, num_cus, stream);
 }
 
 hipError_t launch_mxfp4_cast_transpose(const void* x, bool bf16, int64_t rows, int64_t cols,

@@ -21,8 +21,10 @@
 // in registers between its reduction and its output.  TPR threads share a row (16,
 // 64, 256 or 1024, so that a thread holds 1 to 4 groups of 8 elements), and a
 // workgroup takes 256 / TPR rows.  A group of 8 consecutive elements per lane makes
-// 16-byte BF16 accesses; rows that are not 16-byte aligned, or are no multiple of 8
-// long, take the same kernel with consecutive lanes on consecutive elements.
+// 16-byte BF16 accesses, at the elements' alignment where rows have no better; a row that
+// is no multiple of 8 long has its last elements taken one by one.
+
+#include <type_traits>
 
 #include "cast_common.h"
 #include "fp4_common.h"
@@ -48,19 +50,31 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
     static_cast<float*>(p)[i] = v;
 }
 
-template <bool BF>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
-  if constexpr (BF) {
-    const u32x4 d = __builtin_nontemporal_load(
-        reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i));
+// Vectors at the alignment of the elements: gfx950 takes 8- and 16-byte accesses at any
+// address, an unaligned one costs the extra cache line that it touches.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
+
+// n (1 .. 8; 8 = a whole group) elements at i.  AL: 16-byte aligned, whole groups only.
+template <bool BF, bool AL>
+__device__ __forceinline__ void load8(const void* p, int64_t i, int n, float (&v)[8],
+                                      bool keep = false) {
+  using V = std::conditional_t<AL, u32x4, u32x4_any>;
+  if (!AL && n < 8) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = k < n ? load1<BF>(p, i + k) : 0.0f;
+  } else if constexpr (BF) {
+    const V* s = reinterpret_cast<const V*>(static_cast<const uint16_t*>(p) + i);
+    const u32x4 d = AL && !keep ? (u32x4)__builtin_nontemporal_load(s) : (u32x4)*s;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       v[2 * k] = bf16_lo(d[k]);
       v[2 * k + 1] = bf16_hi(d[k]);
     }
   } else {
-    const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + i);
-    const u32x4 a = __builtin_nontemporal_load(s), b = __builtin_nontemporal_load(s + 1);
+    const V* s = reinterpret_cast<const V*>(static_cast<const float*>(p) + i);
+    const u32x4 a = AL && !keep ? (u32x4)__builtin_nontemporal_load(s) : (u32x4)s[0];
+    const u32x4 b = AL && !keep ? (u32x4)__builtin_nontemporal_load(s + 1) : (u32x4)s[1];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       v[k] = __uint_as_float(a[k]);
@@ -69,13 +83,20 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
   }
 }
 
-template <bool BF>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
-  if constexpr (BF) {
+template <bool BF, bool AL>
+__device__ __forceinline__ void store8(void* p, int64_t i, int n, const float (&v)[8]) {
+  using V = std::conditional_t<AL, u32x4, u32x4_any>;
+  if (!AL && n < 8) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) store1<BF>(p, i + k, v[k]);
+  } else if constexpr (BF) {
     u32x4 d;
 #pragma unroll
     for (int k = 0; k < 4; ++k) d[k] = bf16_pair_rne(v[2 * k], v[2 * k + 1]);
-    __builtin_nontemporal_store(d, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i));
+    V* s = reinterpret_cast<V*>(static_cast<uint16_t*>(p) + i);
+    if constexpr (AL) __builtin_nontemporal_store(d, s);
+    else *s = d;
   } else {
     u32x4 a, b;
 #pragma unroll
@@ -83,30 +104,36 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
       a[k] = __float_as_uint(v[k]);
       b[k] = __float_as_uint(v[4 + k]);
     }
-    u32x4* s = reinterpret_cast<u32x4*>(static_cast<float*>(p) + i);
-    __builtin_nontemporal_store(a, s);
-    __builtin_nontemporal_store(b, s + 1);
+    V* s = reinterpret_cast<V*>(static_cast<float*>(p) + i);
+    if constexpr (AL) {
+      __builtin_nontemporal_store(a, s);
+      __builtin_nontemporal_store(b, s + 1);
+    } else {
+      s[0] = a;
+      s[1] = b;
+    }
+  }
+}
+
+// Eight codes, or the first n of them.
+template <bool AL>
+__device__ __forceinline__ void store_codes(uint8_t* q, int n, const u32x2& c) {
+  if (!AL && n < 8) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) q[k] = (uint8_t)(c[k >> 2] >> (8 * (k & 3)));
+  } else if constexpr (AL) {
+    __builtin_nontemporal_store(c, reinterpret_cast<u32x2*>(q));
+  } else {
+    *reinterpret_cast<u32x2_any*>(q) = c;
   }
 }
 
 // gamma is read by every row: an ordinary (cached) load.
-__device__ __forceinline__ void gamma8(const void* g, bool bf, int64_t i, float (&v)[8]) {
-  if (bf) {
-    const u32x4 d = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(g) + i);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = bf16_lo(d[k]);
-      v[2 * k + 1] = bf16_hi(d[k]);
-    }
-  } else {
-    const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const float*>(g) + i);
-    const u32x4 a = s[0], b = s[1];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = __uint_as_float(a[k]);
-      v[4 + k] = __uint_as_float(b[k]);
-    }
-  }
+template <bool AL>
+__device__ __forceinline__ void gamma8(const void* g, bool bf, int64_t i, int n, float (&v)[8]) {
+  if (bf) load8<true, AL>(g, i, n, v, true);
+  else load8<false, AL>(g, i, n, v, true);
 }
 __device__ __forceinline__ float gamma1(const void* g, bool bf, int64_t i) {
   return bf ? load1<true>(g, i) : load1<false>(g, i);
@@ -186,7 +213,7 @@ __device__ __forceinline__ void commit(uint32_t amax, uint32_t sat, float* g_ama
 
 // ------------------------------------------------------------------ forward
 
-template <bool XBF, bool HBF, int TPR, int VPT, int MODE, bool VEC>
+template <bool XBF, bool HBF, int TPR, int VPT, int MODE, bool AL>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArgs p) {
   constexpr int NT = TPR > 256 ? TPR : 256;
   constexpr int RPB = NT / TPR;
@@ -195,62 +222,37 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
   const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
   const bool live = row < p.rows;
   const int64_t C = p.cols;
-  // element k of group j of this thread
-  auto col = [&](int j, int k) -> int64_t {
-    return VEC ? ((int64_t)t + TPR * j) * 8 + k : (int64_t)(j * 8 + k) * TPR + t;
+  // group j of this thread: its first column, and how many elements it has
+  auto col = [&](int j) -> int64_t { return ((int64_t)t + TPR * j) * 8; };
+  auto count = [&](int j) -> int {
+    const int64_t left = C - col(j);
+    return !live || left <= 0 ? 0 : AL || left >= 8 ? 8 : (int)left;
   };
   const int64_t ox = row * p.ldx, orr = row * p.ldr, oh = row * p.ldh;
-  float h[VPT][8];
-  if constexpr (VEC) {
-    float r[VPT][8];
+  float h[VPT][8], r[VPT][8];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const bool in = live && col(j, 0) < C;
+  for (int j = 0; j < VPT; ++j) {
+    const int n = count(j);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) h[j][k] = r[j][k] = 0.0f;
-      if (in) load8<XBF>(p.x, ox + col(j, 0), h[j]);
-      if (in && p.res) load8<HBF>(p.res, orr + col(j, 0), r[j]);
-    }
-    if (p.res) {
-#pragma unroll
-      for (int j = 0; j < VPT; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          h[j][k] += r[j][k];
-          if constexpr (HBF) h[j][k] = bf16_round(h[j][k]);
-        }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        h[j][k] = 0.0f;
-        if (live && col(j, k) < C) {
-          h[j][k] = load1<XBF>(p.x, ox + col(j, k));
-          if (p.res) {
-            h[j][k] += load1<HBF>(p.res, orr + col(j, k));
-            if constexpr (HBF) h[j][k] = bf16_round(h[j][k]);
-          }
-        }
-      }
+    for (int k = 0; k < 8; ++k) h[j][k] = r[j][k] = 0.0f;
+    if (n > 0) load8<XBF, AL>(p.x, ox + col(j), n, h[j]);
+    if (n > 0 && p.res) load8<HBF, AL>(p.res, orr + col(j), n, r[j]);
   }
   float ss = 0.0f;
 #pragma unroll
   for (int j = 0; j < VPT; ++j)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) ss += h[j][k] * h[j][k];
+    for (int k = 0; k < 8; ++k) {
+      if (p.res) {
+        h[j][k] += r[j][k];
+        if constexpr (HBF) h[j][k] = bf16_round(h[j][k]);
+      }
+      ss += h[j][k] * h[j][k];
+    }
   if (p.h) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if constexpr (VEC) {
-        if (live && col(j, 0) < C) store8<HBF>(p.h, oh + col(j, 0), h[j]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (live && col(j, k) < C) store1<HBF>(p.h, oh + col(j, k), h[j][k]);
-      }
-    }
+    for (int j = 0; j < VPT; ++j)
+      if (count(j) > 0) store8<HBF, AL>(p.h, oh + col(j), count(j), h[j]);
   }
   ss = row_sum<TPR>(ss, reinterpret_cast<float*>(red));
   const float rstd = norm_rstd(ss, C, p.eps);
@@ -258,40 +260,19 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
   // y in place of h
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    if constexpr (VEC) {
-      if (live && col(j, 0) < C) {
-        float g[8];
-        gamma8(p.gamma, p.gamma_bf16, col(j, 0), g);
+    if (count(j) > 0) {
+      float g[8];
+      gamma8<AL>(p.gamma, p.gamma_bf16, col(j), count(j), g);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[j][k] = (h[j][k] * rstd) * g[k];
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (live && col(j, k) < C)
-          h[j][k] = (h[j][k] * rstd) * gamma1(p.gamma, p.gamma_bf16, col(j, k));
+      for (int k = 0; k < 8; ++k) h[j][k] = k < count(j) ? (h[j][k] * rstd) * g[k] : 0.0f;
     }
   }
   if (p.y) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      if constexpr (VEC) {
-        if (live && col(j, 0) < C) {
-          if (p.y_bf16)
-            store8<true>(p.y, row * p.ldy + col(j, 0), h[j]);
-          else
-            store8<false>(p.y, row * p.ldy + col(j, 0), h[j]);
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (live && col(j, k) < C) {
-            if (p.y_bf16)
-              store1<true>(p.y, row * p.ldy + col(j, k), h[j][k]);
-            else
-              store1<false>(p.y, row * p.ldy + col(j, k), h[j][k]);
-          }
-      }
+      if (count(j) == 0) continue;
+      if (p.y_bf16) store8<true, AL>(p.y, row * p.ldy + col(j), count(j), h[j]);
+      else store8<false, AL>(p.y, row * p.ldy + col(j), count(j), h[j]);
     }
   }
   if constexpr (MODE == kQNone) return;
@@ -318,24 +299,14 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
     }
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      if constexpr (VEC) {
-        if (live && col(j, 0) < C) {
-          const u32x2 c = codes8(h[j], s, e5m2, sat, MODE == kQTensor && p.sat);
-          __builtin_nontemporal_store(c, reinterpret_cast<u32x2*>(p.q + row * p.ldq + col(j, 0)));
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (live && col(j, k) < C) {
-            const float v = h[j][k] * s;
-            p.q[row * p.ldq + col(j, k)] = (uint8_t)code1(v, e5m2);
-            if (MODE == kQTensor && p.sat) sat += sat1(v, e5m2);
-          }
-      }
+      if (count(j) == 0) continue;
+      // (elements past the row are zeros: they add nothing to the count)
+      const u32x2 c = codes8(h[j], s, e5m2, sat, MODE == kQTensor && p.sat);
+      store_codes<AL>(p.q + row * p.ldq + col(j), count(j), c);
     }
     if constexpr (MODE == kQTensor) commit(amax, sat, p.amax, p.sat, red);
   } else if constexpr (MODE == kQMx) {
-    // a block of 32 is 4 consecutive lanes (VEC only; C is a multiple of 32)
+    // a block of 32 is 4 consecutive lanes (AL only; C is a multiple of 32)
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       uint32_t a = 0;
@@ -343,8 +314,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
       for (int k = 0; k < 8; ++k) a = max(a, abs_bits(h[j][k]));
       a = max(a, (uint32_t)__shfl_xor((int)a, 1));
       a = max(a, (uint32_t)__shfl_xor((int)a, 2));
-      const int64_t c0 = col(j, 0);
-      if (!live || c0 >= C) continue;
+      const int64_t c0 = col(j);
+      if (count(j) == 0) continue;
       const uint32_t code = mx_code(a, p.fmt == kE2M1 ? 2u : e5m2 ? 15u : 8u);
       if ((t & 3) == 0) p.mx_scales[row * p.ldms + c0 / 32] = (uint8_t)code;
       if (p.fmt == kE2M1) {
@@ -354,7 +325,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
         u32x2 c = {0x7F7F7F7Fu, 0x7F7F7F7Fu};
         uint32_t unused = 0;
         if (code != 255u) c = codes8(h[j], __uint_as_float((254u - code) << 23), e5m2, unused, false);
-        __builtin_nontemporal_store(c, reinterpret_cast<u32x2*>(p.q + row * p.ldq + c0));
+        store_codes<true>(p.q + row * p.ldq + c0, 8, c);
       }
     }
   }
@@ -448,7 +419,7 @@ __global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormArgs p) {
 // keeps its share of dgamma in registers: partial [gridDim.x][C] in `work`, summed by
 // norm_dgamma_kernel in a fixed order (no atomics: the same inputs give the same
 // bits).
-template <bool XBF, bool HBF, int TPR, int VPT, bool VEC>
+template <bool XBF, bool HBF, int TPR, int VPT, bool AL>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwdArgs p) {
   constexpr int NT = TPR > 256 ? TPR : 256;
   constexpr int RPB = NT / TPR;
@@ -456,8 +427,10 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd
   __shared__ float dg_lds[RPB > 1 ? TPR * VPT * 8 : 1];
   const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
   const int64_t C = p.cols;
-  auto col = [&](int j, int k) -> int64_t {
-    return VEC ? ((int64_t)t + TPR * j) * 8 + k : (int64_t)(j * 8 + k) * TPR + t;
+  auto col = [&](int j) -> int64_t { return ((int64_t)t + TPR * j) * 8; };
+  auto count = [&](int j) -> int {
+    const int64_t left = C - col(j);
+    return left <= 0 ? 0 : AL || left >= 8 ? 8 : (int)left;
   };
   const bool e5m2 = p.fmt == kE5M2;
   float s = 1.0f;
@@ -480,39 +453,18 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd
     for (int j = 0; j < VPT; ++j) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) xh[j][k] = g[j][k] = dr[j][k] = 0.0f;
-      if constexpr (VEC) {
-        if (live && col(j, 0) < C) {
-          load8<HBF>(p.h, row * p.ldh + col(j, 0), xh[j]);
-          load8<XBF>(p.dy, row * p.lddy + col(j, 0), g[j]);
-          if (p.dres) load8<HBF>(p.dres, row * p.lddr + col(j, 0), dr[j]);
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (live && col(j, k) < C) {
-            xh[j][k] = load1<HBF>(p.h, row * p.ldh + col(j, k));
-            g[j][k] = load1<XBF>(p.dy, row * p.lddy + col(j, k));
-            if (p.dres) dr[j][k] = load1<HBF>(p.dres, row * p.lddr + col(j, k));
-          }
+      if (live && count(j) > 0) {
+        load8<HBF, AL>(p.h, row * p.ldh + col(j), count(j), xh[j]);
+        load8<XBF, AL>(p.dy, row * p.lddy + col(j), count(j), g[j]);
+        if (p.dres) load8<HBF, AL>(p.dres, row * p.lddr + col(j), count(j), dr[j]);
       }
     }
     const float rstd = live ? p.rstd[row] : 0.0f;
     float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      float gm[8];
-      if constexpr (VEC) {
-        if (col(j, 0) < C) {
-          gamma8(p.gamma, p.gamma_bf16, col(j, 0), gm);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) gm[k] = 0.0f;
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          gm[k] = col(j, k) < C ? gamma1(p.gamma, p.gamma_bf16, col(j, k)) : 0.0f;
-      }
+      float gm[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      if (count(j) > 0) gamma8<AL>(p.gamma, p.gamma_bf16, col(j), count(j), gm);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         xh[j][k] *= rstd;
@@ -524,29 +476,16 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd
     const float mean = row_sum<TPR>(dot, reinterpret_cast<float*>(red)) / (float)C;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
+      if (!live || count(j) == 0) continue;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) g[j][k] = rstd * (g[j][k] - xh[j][k] * mean) + dr[j][k];
-      if constexpr (VEC) {
-        if (live && col(j, 0) < C) {
-          store8<HBF>(p.dx, row * p.lddx + col(j, 0), g[j]);
-          if (p.q) {
+      for (int k = 0; k < 8; ++k)
+        g[j][k] = AL || k < count(j) ? rstd * (g[j][k] - xh[j][k] * mean) + dr[j][k] : 0.0f;
+      store8<HBF, AL>(p.dx, row * p.lddx + col(j), count(j), g[j]);
+      if (p.q) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) amax = max(amax, abs_bits(g[j][k]));
-            const u32x2 c = codes8(g[j], s, e5m2, sat, p.sat != nullptr);
-            __builtin_nontemporal_store(c, reinterpret_cast<u32x2*>(p.q + row * p.ldq + col(j, 0)));
-          }
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (live && col(j, k) < C) {
-            store1<HBF>(p.dx, row * p.lddx + col(j, k), g[j][k]);
-            if (p.q) {
-              amax = max(amax, abs_bits(g[j][k]));
-              p.q[row * p.ldq + col(j, k)] = (uint8_t)code1(g[j][k] * s, e5m2);
-              if (p.sat) sat += sat1(g[j][k] * s, e5m2);
-            }
-          }
+        for (int k = 0; k < 8; ++k) amax = max(amax, abs_bits(g[j][k]));
+        const u32x2 c = codes8(g[j], s, e5m2, sat, p.sat != nullptr);
+        store_codes<AL>(p.q + row * p.ldq + col(j), count(j), c);
       }
     }
   }
@@ -570,14 +509,14 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd
       for (int j = 0; j < VPT; ++j)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (col(j, k) < C) out[col(j, k)] = dg_lds[(j * 8 + k) * TPR + t];
+          if (k < count(j)) out[col(j) + k] = dg_lds[(j * 8 + k) * TPR + t];
     }
   } else {
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (col(j, k) < C) out[col(j, k)] = acc[j][k];
+        if (k < count(j)) out[col(j) + k] = acc[j][k];
   }
   if (p.q) commit(amax, sat, p.amax, p.sat, red);
 }
@@ -666,12 +605,12 @@ static RowShape row_shape(int64_t rows, int64_t cols) {
   return {1024, 0};
 }
 
-template <bool XBF, bool HBF, int MODE, bool VEC>
+template <bool XBF, bool HBF, int MODE, bool AL>
 static hipError_t launch_fwd(const NormArgs& a, RowShape sh, hipStream_t stream) {
 #define FP8DS_NORM_CASE(T, V)                                                                    \
   if (sh.tpr == T && sh.vpt == V) {                                                              \
     const int rpb = T > 256 ? 1 : 256 / T;                                                       \
-    hipLaunchKernelGGL((norm_fwd_kernel<XBF, HBF, T, V, MODE, VEC>),                              \
+    hipLaunchKernelGGL((norm_fwd_kernel<XBF, HBF, T, V, MODE, AL>),                              \
                        dim3((unsigned)((a.rows + rpb - 1) / rpb)), dim3(T > 256 ? T : 256), 0,   \
                        stream, a);                                                               \
     return hipGetLastError();                                                                    \
@@ -729,11 +668,11 @@ int norm_bwd_parts(int64_t rows, int64_t cols) {
   return (int)(blocks < 1024 ? blocks : 1024);
 }
 
-template <bool XBF, bool HBF, bool VEC>
+template <bool XBF, bool HBF, bool AL>
 static hipError_t launch_bwd(const NormBwdArgs& a, RowShape sh, int parts, hipStream_t stream) {
 #define FP8DS_NORM_CASE(T, V)                                                                     \
   if (sh.tpr == T && sh.vpt == V) {                                                               \
-    hipLaunchKernelGGL((norm_bwd_kernel<XBF, HBF, T, V, VEC>), dim3((unsigned)parts),             \
+    hipLaunchKernelGGL((norm_bwd_kernel<XBF, HBF, T, V, AL>), dim3((unsigned)parts),             \
                        dim3(T > 256 ? T : 256), 0, stream, a);                                    \
     return hipGetLastError();                                                                     \
   }
