@@ -55,32 +55,41 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
 
-// n (1 .. 8; 8 = a whole group) elements at i.  AL: 16-byte aligned, whole groups only.
+// Eight elements as they lie in memory.  All of a row's loads are issued before any is
+// unpacked, and without a branch between them (each would wait for the load before it):
+// groups past the row's end read its last whole group, and are not used.
+template <bool BF>
+struct Raw8 {
+  u32x4 v[BF ? 1 : 2];
+};
+
 template <bool BF, bool AL>
-__device__ __forceinline__ void load8(const void* p, int64_t i, int n, float (&v)[8],
-                                      bool keep = false) {
+__device__ __forceinline__ Raw8<BF> load8(const void* p, int64_t i) {
   using V = std::conditional_t<AL, u32x4, u32x4_any>;
-  if (!AL && n < 8) {
+  const V* s = BF ? reinterpret_cast<const V*>(static_cast<const uint16_t*>(p) + i)
+                  : reinterpret_cast<const V*>(static_cast<const float*>(p) + i);
+  Raw8<BF> r;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = k < n ? load1<BF>(p, i + k) : 0.0f;
-  } else if constexpr (BF) {
-    const V* s = reinterpret_cast<const V*>(static_cast<const uint16_t*>(p) + i);
-    const u32x4 d = AL && !keep ? (u32x4)__builtin_nontemporal_load(s) : (u32x4)*s;
+  for (int k = 0; k < (BF ? 1 : 2); ++k) r.v[k] = AL ? (u32x4)__builtin_nontemporal_load(s + k) : (u32x4)s[k];
+  return r;
+}
+
+// The first n of them as floats, zeros after.
+template <bool BF, bool AL>
+__device__ __forceinline__ void unpack8(const Raw8<BF>& r, int n, float (&v)[8]) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = bf16_lo(d[k]);
-      v[2 * k + 1] = bf16_hi(d[k]);
-    }
-  } else {
-    const V* s = reinterpret_cast<const V*>(static_cast<const float*>(p) + i);
-    const u32x4 a = AL && !keep ? (u32x4)__builtin_nontemporal_load(s) : (u32x4)s[0];
-    const u32x4 b = AL && !keep ? (u32x4)__builtin_nontemporal_load(s + 1) : (u32x4)s[1];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = __uint_as_float(a[k]);
-      v[4 + k] = __uint_as_float(b[k]);
-    }
+  for (int k = 0; k < 8; ++k) {
+    float x;
+    if constexpr (BF) x = k & 1 ? bf16_hi(r.v[0][k >> 1]) : bf16_lo(r.v[0][k >> 1]);
+    else x = __uint_as_float(r.v[k >> 2][k & 3]);
+    v[k] = n == 8 ? x : 0.0f;
   }
+}
+// A row's last n < 8 elements, one by one.
+template <bool BF>
+__device__ __forceinline__ void load_tail(const void* p, int64_t i, int n, float (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 7; ++k) v[k] = k < n ? load1<BF>(p, i + k) : 0.0f;
 }
 
 template <bool BF, bool AL>
@@ -129,11 +138,21 @@ __device__ __forceinline__ void store_codes(uint8_t* q, int n, const u32x2& c) {
   }
 }
 
-// gamma is read by every row: an ordinary (cached) load.
+// gamma is read by every row: ordinary (cached) loads, of either type without a branch
+// (BF16 reads its piece twice).
 template <bool AL>
-__device__ __forceinline__ void gamma8(const void* g, bool bf, int64_t i, int n, float (&v)[8]) {
-  if (bf) load8<true, AL>(g, i, n, v, true);
-  else load8<false, AL>(g, i, n, v, true);
+__device__ __forceinline__ Raw8<false> gamma8(const void* g, bool bf, int64_t i) {
+  using V = std::conditional_t<AL, u32x4, u32x4_any>;
+  const char* s = static_cast<const char*>(g) + (i << (bf ? 1 : 2));
+  Raw8<false> r;
+  r.v[0] = *reinterpret_cast<const V*>(s);
+  r.v[1] = *reinterpret_cast<const V*>(s + (bf ? 0 : 16));
+  return r;
+}
+template <bool AL>
+__device__ __forceinline__ void unpack_gamma(const Raw8<false>& r, bool bf, int n, float (&v)[8]) {
+  if (bf) unpack8<true, AL>(Raw8<true>{{r.v[0]}}, n, v);
+  else unpack8<false, AL>(r, n, v);
 }
 __device__ __forceinline__ float gamma1(const void* g, bool bf, int64_t i) {
   return bf ? load1<true>(g, i) : load1<false>(g, i);
@@ -183,18 +202,36 @@ __device__ __forceinline__ float norm_rstd(float ss, int64_t C, float eps) {
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// Eight FP8 codes of v s (bytes in order), and what they add to the saturation count.
-__device__ __forceinline__ u32x2 codes8(const float (&v)[8], float s, bool e5m2, uint32_t& sat,
-                                        bool want_sat) {
-  float t[8];
+// FP8 codes of the N groups of v s, and what they add to the saturation count.  `amax`:
+// the largest |v| bits of this thread.  Without a NaN among the values, and with a scale
+// that makes none of them (Inf * 0), the packed converts alone encode.
+template <int FMT, int N>
+__device__ __forceinline__ void codes_fmt(const float (&v)[N][8], float s, uint32_t amax, u32x2 (&c)[N],
+                                          uint32_t& sat, bool want_sat) {
+  const uint32_t sb = __float_as_uint(s) & 0x7FFFFFFFu;
+  const bool slow = amax > 0x7F800000u || sb >= 0x7F800000u || sb == 0u;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) t[k] = v[k] * s;
-  if (e5m2) {
-    if (want_sat) sat += sat4<kE5M2>(t[0], t[1], t[2], t[3]) + sat4<kE5M2>(t[4], t[5], t[6], t[7]);
-    return u32x2{encode4<kE5M2>(t[0], t[1], t[2], t[3]), encode4<kE5M2>(t[4], t[5], t[6], t[7])};
+  for (int j = 0; j < N; ++j) {
+    float t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = v[j][k] * s;
+    c[j] = u32x2{encode4_hw<FMT>(t[0], t[1], t[2], t[3]), encode4_hw<FMT>(t[4], t[5], t[6], t[7])};
+    if (want_sat) sat += sat4<FMT>(t[0], t[1], t[2], t[3]) + sat4<FMT>(t[4], t[5], t[6], t[7]);
   }
-  if (want_sat) sat += sat4<kE4M3>(t[0], t[1], t[2], t[3]) + sat4<kE4M3>(t[4], t[5], t[6], t[7]);
-  return u32x2{encode4<kE4M3>(t[0], t[1], t[2], t[3]), encode4<kE4M3>(t[4], t[5], t[6], t[7])};
+  if (slow) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        c[j][q] = encode4_sw<FMT>(v[j][4 * q] * s, v[j][4 * q + 1] * s, v[j][4 * q + 2] * s,
+                                  v[j][4 * q + 3] * s);
+  }
+}
+template <int N>
+__device__ __forceinline__ void codes8(const float (&v)[N][8], float s, bool e5m2, uint32_t amax,
+                                       u32x2 (&c)[N], uint32_t& sat, bool want_sat) {
+  if (e5m2) codes_fmt<kE5M2>(v, s, amax, c, sat, want_sat);
+  else codes_fmt<kE4M3>(v, s, amax, c, sat, want_sat);
 }
 __device__ __forceinline__ uint32_t code1(float t, bool e5m2) {
   return e5m2 ? encode_fp8<kE5M2>(t) : encode_fp8<kE4M3>(t);
@@ -228,27 +265,46 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
     const int64_t left = C - col(j);
     return !live || left <= 0 ? 0 : AL || left >= 8 ? 8 : (int)left;
   };
-  const int64_t ox = row * p.ldx, orr = row * p.ldr, oh = row * p.ldh;
-  float h[VPT][8], r[VPT][8];
+  auto at = [&](int j) -> int64_t { return col(j) + 8 <= C ? col(j) : C - 8; };
+  const int64_t from = live ? row : p.rows - 1;  // (rows past the end are not stored)
+  const int64_t ox = from * p.ldx, orr = from * p.ldr, oh = row * p.ldh;
+  Raw8<XBF> rx[VPT];
+  Raw8<HBF> rr[VPT];
+  Raw8<false> rg[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) rx[j] = load8<XBF, AL>(p.x, ox + at(j));
+  if (p.res) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) rr[j] = load8<HBF, AL>(p.res, orr + at(j));
+  }
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) rg[j] = gamma8<AL>(p.gamma, p.gamma_bf16, at(j));
+  // (before any store: a wait for a later load would wait for the stores too)
+  const float given = MODE == kQTensor ? *p.scale_in : 1.0f;
+  float h[VPT][8];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    const int n = count(j);
+    unpack8<XBF, AL>(rx[j], count(j), h[j]);
+    if (!AL && count(j) > 0 && count(j) < 8) load_tail<XBF>(p.x, ox + col(j), count(j), h[j]);
+  }
+  if (p.res) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) h[j][k] = r[j][k] = 0.0f;
-    if (n > 0) load8<XBF, AL>(p.x, ox + col(j), n, h[j]);
-    if (n > 0 && p.res) load8<HBF, AL>(p.res, orr + col(j), n, r[j]);
+    for (int j = 0; j < VPT; ++j) {
+      float r[8];
+      unpack8<HBF, AL>(rr[j], count(j), r);
+      if (!AL && count(j) > 0 && count(j) < 8) load_tail<HBF>(p.res, orr + col(j), count(j), r);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        h[j][k] += r[k];
+        if constexpr (HBF) h[j][k] = bf16_round(h[j][k]);
+      }
+    }
   }
   float ss = 0.0f;
 #pragma unroll
   for (int j = 0; j < VPT; ++j)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (p.res) {
-        h[j][k] += r[j][k];
-        if constexpr (HBF) h[j][k] = bf16_round(h[j][k]);
-      }
-      ss += h[j][k] * h[j][k];
-    }
+    for (int k = 0; k < 8; ++k) ss += h[j][k] * h[j][k];
   if (p.h) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
@@ -260,12 +316,15 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
   // y in place of h
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    if (count(j) > 0) {
-      float g[8];
-      gamma8<AL>(p.gamma, p.gamma_bf16, col(j), count(j), g);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) h[j][k] = k < count(j) ? (h[j][k] * rstd) * g[k] : 0.0f;
+    float g[8];
+    unpack_gamma<AL>(rg[j], p.gamma_bf16, count(j), g);
+    if (!AL && count(j) > 0 && count(j) < 8) {
+      if (p.gamma_bf16) load_tail<true>(p.gamma, col(j), count(j), g);
+      else load_tail<false>(p.gamma, col(j), count(j), g);
     }
+    // (past the row h is 0, but r may be infinite)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[j][k] = k < count(j) ? (h[j][k] * rstd) * g[k] : 0.0f;
   }
   if (p.y) {
 #pragma unroll
@@ -278,17 +337,17 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
   if constexpr (MODE == kQNone) return;
   const bool e5m2 = p.fmt == kE5M2;
   if constexpr (MODE == kQTensor || MODE == kQRow) {
-    uint32_t amax = 0, sat = 0;
+    uint32_t mine = 0, amax = 0, sat = 0;
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) amax = max(amax, abs_bits(h[j][k]));
+      for (int k = 0; k < 8; ++k) mine = max(mine, abs_bits(h[j][k]));
     float s;
     if constexpr (MODE == kQTensor) {
-      s = *p.scale_in;
+      s = given;
       if (p.scale_used && blockIdx.x == 0 && threadIdx.x == 0) *p.scale_used = s;
     } else {
-      amax = canonical_amax_bits(row_max<TPR>(amax, red));
+      amax = canonical_amax_bits(row_max<TPR>(mine, red));
       s = scale_from_amax(__uint_as_float(amax), e5m2 ? FmtTraits<kE5M2>::kMax : FmtTraits<kE4M3>::kMax,
                           p.margin);
       if (live && t == 0) {
@@ -297,14 +356,13 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
         if (p.amax) p.amax[row] = __uint_as_float(amax);
       }
     }
+    // (elements past the row are zeros: they add nothing to the count)
+    u32x2 c[VPT];
+    codes8(h, s, e5m2, mine, c, sat, MODE == kQTensor && p.sat);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (count(j) == 0) continue;
-      // (elements past the row are zeros: they add nothing to the count)
-      const u32x2 c = codes8(h[j], s, e5m2, sat, MODE == kQTensor && p.sat);
-      store_codes<AL>(p.q + row * p.ldq + col(j), count(j), c);
-    }
-    if constexpr (MODE == kQTensor) commit(amax, sat, p.amax, p.sat, red);
+    for (int j = 0; j < VPT; ++j)
+      if (count(j) > 0) store_codes<AL>(p.q + row * p.ldq + col(j), count(j), c[j]);
+    if constexpr (MODE == kQTensor) commit(mine, sat, p.amax, p.sat, red);
   } else if constexpr (MODE == kQMx) {
     // a block of 32 is 4 consecutive lanes (AL only; C is a multiple of 32)
 #pragma unroll
@@ -322,10 +380,15 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
         const uint32_t c = code == 255u ? kFp4NanBlock : fp4_codes8(h[j], code);
         *reinterpret_cast<uint32_t*>(p.q + row * p.ldq + c0 / 2) = c;
       } else {
-        u32x2 c = {0x7F7F7F7Fu, 0x7F7F7F7Fu};
+        // (with a finite block no product is NaN)
+        float u[1][8];
+        u32x2 c[1];
         uint32_t unused = 0;
-        if (code != 255u) c = codes8(h[j], __uint_as_float((254u - code) << 23), e5m2, unused, false);
-        store_codes<true>(p.q + row * p.ldq + c0, 8, c);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[0][k] = h[j][k];
+        codes8(u, mx_multiplier(code == 255u ? 127u : code), e5m2, 0u, c, unused, false);
+        if (code == 255u) c[0] = u32x2{0x7F7F7F7Fu, 0x7F7F7F7Fu};
+        store_codes<true>(p.q + row * p.ldq + c0, 8, c[0]);
       }
     }
   }
@@ -445,49 +508,87 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(NormBwd
     for (int k = 0; k < 8; ++k) acc[j][k] = 0.0f;
   uint32_t amax = 0, sat = 0;
   const int64_t step = (int64_t)gridDim.x * RPB;
+  auto at = [&](int j) -> int64_t { return col(j) + 8 <= C ? col(j) : C - 8; };
+  struct RowData {
+    Raw8<HBF> h[VPT], dr[VPT];
+    Raw8<XBF> dy[VPT];
+    float rstd;
+  };
+  // a row's loads; rows past the end read the last one, and are not used
+  auto load_row = [&](int64_t row, RowData& d) {
+    row = row < p.rows ? row : p.rows - 1;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) d.h[j] = load8<HBF, AL>(p.h, row * p.ldh + at(j));
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) d.dy[j] = load8<XBF, AL>(p.dy, row * p.lddy + at(j));
+    if (p.dres) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) d.dr[j] = load8<HBF, AL>(p.dres, row * p.lddr + at(j));
+    }
+    d.rstd = p.rstd[row];
+  };
+  Raw8<false> rg[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) rg[j] = gamma8<AL>(p.gamma, p.gamma_bf16, at(j));
+  // The next row is on its way while this one is computed, as far as the registers go.
+  constexpr bool kAhead = VPT * ((HBF ? 8 : 16) + (XBF ? 4 : 8)) <= 32;
+  RowData now;
+  if constexpr (kAhead) load_row((int64_t)blockIdx.x * RPB + slot, now);
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.rows; r0 += step) {
     const int64_t row = r0 + slot;
     const bool live = row < p.rows;
-    float xh[VPT][8], g[VPT][8], dr[VPT][8];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) xh[j][k] = g[j][k] = dr[j][k] = 0.0f;
-      if (live && count(j) > 0) {
-        load8<HBF, AL>(p.h, row * p.ldh + col(j), count(j), xh[j]);
-        load8<XBF, AL>(p.dy, row * p.lddy + col(j), count(j), g[j]);
-        if (p.dres) load8<HBF, AL>(p.dres, row * p.lddr + col(j), count(j), dr[j]);
-      }
-    }
-    const float rstd = live ? p.rstd[row] : 0.0f;
+    RowData next;
+    if constexpr (kAhead) load_row(row + step, next);
+    else load_row(row, now);
+    float xh[VPT][8], g[VPT][8];
     float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      float gm[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      if (count(j) > 0) gamma8<AL>(p.gamma, p.gamma_bf16, col(j), count(j), gm);
+      const int n = live ? count(j) : 0;
+      float gm[8];
+      unpack8<HBF, AL>(now.h[j], n, xh[j]);
+      unpack8<XBF, AL>(now.dy[j], n, g[j]);
+      unpack_gamma<AL>(rg[j], p.gamma_bf16, n, gm);
+      if (!AL && n > 0 && n < 8) {
+        load_tail<HBF>(p.h, row * p.ldh + col(j), n, xh[j]);
+        load_tail<XBF>(p.dy, row * p.lddy + col(j), n, g[j]);
+        if (p.gamma_bf16) load_tail<true>(p.gamma, col(j), n, gm);
+        else load_tail<false>(p.gamma, col(j), n, gm);
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        xh[j][k] *= rstd;
+        xh[j][k] = k < n ? xh[j][k] * now.rstd : 0.0f;  // (rstd may be infinite)
         acc[j][k] += g[j][k] * xh[j][k];
         g[j][k] *= gm[k];
         dot += g[j][k] * xh[j][k];
       }
     }
     const float mean = row_sum<TPR>(dot, reinterpret_cast<float*>(red)) / (float)C;
+    uint32_t mine = 0;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      if (!live || count(j) == 0) continue;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        g[j][k] = AL || k < count(j) ? rstd * (g[j][k] - xh[j][k] * mean) + dr[j][k] : 0.0f;
-      store8<HBF, AL>(p.dx, row * p.lddx + col(j), count(j), g[j]);
-      if (p.q) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) amax = max(amax, abs_bits(g[j][k]));
-        const u32x2 c = codes8(g[j], s, e5m2, sat, p.sat != nullptr);
-        store_codes<AL>(p.q + row * p.ldq + col(j), count(j), c);
+      const int n = live ? count(j) : 0;
+      float dr[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      if (p.dres) {
+        unpack8<HBF, AL>(now.dr[j], n, dr);
+        if (!AL && n > 0 && n < 8) load_tail<HBF>(p.dres, row * p.lddr + col(j), n, dr);
       }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        g[j][k] = k < n ? now.rstd * (g[j][k] - xh[j][k] * mean) + dr[k] : 0.0f;
+        mine = max(mine, abs_bits(g[j][k]));
+      }
+      if (n > 0) store8<HBF, AL>(p.dx, row * p.lddx + col(j), n, g[j]);
     }
+    if (p.q) {
+      amax = max(amax, mine);
+      u32x2 c[VPT];
+      codes8(g, s, e5m2, mine, c, sat, p.sat != nullptr);
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        if (live && count(j) > 0) store_codes<AL>(p.q + row * p.ldq + col(j), count(j), c[j]);
+    }
+    if constexpr (kAhead) now = next;
   }
   // dgamma: the slots of a workgroup one after the other, then one partial row
   float* out = p.work + (int64_t)blockIdx.x * C;
@@ -594,6 +695,7 @@ struct RowShape {
 };
 static RowShape row_shape(int64_t rows, int64_t cols) {
   const int64_t g = (cols + 7) / 8;
+  if (cols < 8) return {1024, 0};  // no whole group to read
   if (g <= 16) return {16, 1};
   if (g <= 64) return {64, 1};
   if (g <= 128) return {64, 2};
@@ -654,6 +756,7 @@ hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t stream) {
 // 256 registers, take up to 16384 columns; 1024 threads (128 registers) would spill.
 static RowShape bwd_shape(int64_t cols) {
   const int64_t g = (cols + 7) / 8;
+  if (cols < 8) return {1024, 0};
   if (g <= 1024) return row_shape(1 << 20, cols);
   if (g <= 2048) return {512, 4};
   return {1024, 0};
