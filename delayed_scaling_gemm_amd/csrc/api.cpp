@@ -742,7 +742,7 @@ int fp8ds_rmsnorm(const void* x, fp8ds_dtype xt, int64_t ldx, const void* residu
   a.mode = cast ? 1 : 0;
   a.fmt = (int)fmt;
   a.scale_in = scale; a.scale_used = scale_used; a.amax = amax; a.sat = sat_count;
-  return hip_status(fp8ds::launch_norm_fwd(a, stream), who);
+  return hip_status(fp8ds::launch_norm_fwd(a, num_cus(), stream), who);
 }
 
 int fp8ds_rmsnorm_rowwise(const void* x, fp8ds_dtype xt, int64_t ldx, const void* residual,
@@ -764,7 +764,7 @@ int fp8ds_rmsnorm_rowwise(const void* x, fp8ds_dtype xt, int64_t ldx, const void
   a.mode = 2;
   a.fmt = (int)fmt; a.margin = margin;
   a.scale_out = scale; a.scale_inv = scale_inv; a.amax = amax;
-  return hip_status(fp8ds::launch_norm_fwd(a, stream), who);
+  return hip_status(fp8ds::launch_norm_fwd(a, num_cus(), stream), who);
 }
 
 int fp8ds_rmsnorm_mx(const void* x, fp8ds_dtype xt, int64_t ldx, const void* residual, int64_t ldr,
@@ -792,7 +792,7 @@ int fp8ds_rmsnorm_mx(const void* x, fp8ds_dtype xt, int64_t ldx, const void* res
   a.mode = 3;
   a.fmt = (int)fmt;
   a.mx_scales = scales; a.ldms = ld_scales;
-  return hip_status(fp8ds::launch_norm_fwd(a, stream), who);
+  return hip_status(fp8ds::launch_norm_fwd(a, num_cus(), stream), who);
 }
 
 int64_t fp8ds_rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {

@@ -192,7 +192,7 @@ struct NormArgs {
   int64_t ldms;
   bool vec;              // every row 16-byte aligned and cols % 8 == 0
 };
-hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t stream);
+hipError_t launch_norm_fwd(const NormArgs& a, int num_cus, hipStream_t stream);
 
 struct NormBwdArgs {
   const void* dy;        // [rows][lddy]

@@ -19,8 +19,8 @@
 //
 // Design for gfx950: both directions are HBM-bound, so a row is read once and held
 // in registers between its reduction and its output.  TPR threads share a row (16,
-// 64, 256 or 1024, so that a thread holds 1 to 4 groups of 8 elements), and a
-// workgroup takes 256 / TPR rows.  A group of 8 consecutive elements per lane makes
+// 64, 256 or 1024, so that a thread holds 1 to 4 groups of 8 elements), a workgroup
+// takes 256 / TPR rows at a time and goes on to others, the next ones' loads in flight.  A group of 8 consecutive elements per lane makes
 // 16-byte BF16 accesses, at the elements' alignment where rows have no better; a row that
 // is no multiple of 8 long has its last elements taken one by one.
 
@@ -255,143 +255,164 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
   constexpr int NT = TPR > 256 ? TPR : 256;
   constexpr int RPB = NT / TPR;
   __shared__ uint32_t red[2 * (NT / 64)];
-  const int t = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-  const bool live = row < p.rows;
+  const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
   const int64_t C = p.cols;
-  // group j of this thread: its first column, and how many elements it has
+  // group j of this thread: its first column, where it is read, how many elements it has
   auto col = [&](int j) -> int64_t { return ((int64_t)t + TPR * j) * 8; };
+  auto at = [&](int j) -> int64_t { return col(j) + 8 <= C ? col(j) : C - 8; };
   auto count = [&](int j) -> int {
     const int64_t left = C - col(j);
-    return !live || left <= 0 ? 0 : AL || left >= 8 ? 8 : (int)left;
+    return left <= 0 ? 0 : AL || left >= 8 ? 8 : (int)left;
   };
-  auto at = [&](int j) -> int64_t { return col(j) + 8 <= C ? col(j) : C - 8; };
-  const int64_t from = live ? row : p.rows - 1;  // (rows past the end are not stored)
-  const int64_t ox = from * p.ldx, orr = from * p.ldr, oh = row * p.ldh;
-  Raw8<XBF> rx[VPT];
-  Raw8<HBF> rr[VPT];
+  struct RowData {
+    Raw8<XBF> x[VPT];
+    Raw8<HBF> res[VPT];
+  };
+  // a row's loads; rows past the end read the last one, and are not used
+  auto load_row = [&](int64_t row, RowData& d) {
+    row = row < p.rows ? row : p.rows - 1;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) d.x[j] = load8<XBF, AL>(p.x, row * p.ldx + at(j));
+    if (p.res) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) d.res[j] = load8<HBF, AL>(p.res, row * p.ldr + at(j));
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  // The next row is on its way while this one is computed, as far as the registers go.
+  constexpr bool kAhead = VPT * (XBF ? 4 : 8) + VPT * (HBF ? 4 : 8) <= 32;
+  RowData now;
+  load_row((int64_t)blockIdx.x * RPB + slot, now);
   Raw8<false> rg[VPT];
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) rx[j] = load8<XBF, AL>(p.x, ox + at(j));
-  if (p.res) {
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) rr[j] = load8<HBF, AL>(p.res, orr + at(j));
-  }
-#pragma unroll
   for (int j = 0; j < VPT; ++j) rg[j] = gamma8<AL>(p.gamma, p.gamma_bf16, at(j));
-  // (before any store: a wait for a later load would wait for the stores too)
+  const bool e5m2 = p.fmt == kE5M2;
   const float given = MODE == kQTensor ? *p.scale_in : 1.0f;
-  float h[VPT][8];
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    unpack8<XBF, AL>(rx[j], count(j), h[j]);
-    if (!AL && count(j) > 0 && count(j) < 8) load_tail<XBF>(p.x, ox + col(j), count(j), h[j]);
-  }
-  if (p.res) {
+  if (MODE == kQTensor && p.scale_used && blockIdx.x == 0 && threadIdx.x == 0) *p.scale_used = given;
+  uint32_t amax = 0, sat = 0;  // of all this workgroup's rows (kQTensor)
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.rows; r0 += step) {
+    const int64_t row = r0 + slot;
+    const bool live = row < p.rows;
+    RowData next;
+    if constexpr (kAhead) {
+      if (r0 + step < p.rows) load_row(row + step, next);
+    }
+    float h[VPT][8];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      float r[8];
-      unpack8<HBF, AL>(rr[j], count(j), r);
-      if (!AL && count(j) > 0 && count(j) < 8) load_tail<HBF>(p.res, orr + col(j), count(j), r);
+      const int n = live ? count(j) : 0;
+      unpack8<XBF, AL>(now.x[j], n, h[j]);
+      if (!AL && n > 0 && n < 8) load_tail<XBF>(p.x, row * p.ldx + col(j), n, h[j]);
+    }
+    if (p.res) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int n = live ? count(j) : 0;
+        float r[8];
+        unpack8<HBF, AL>(now.res[j], n, r);
+        if (!AL && n > 0 && n < 8) load_tail<HBF>(p.res, row * p.ldr + col(j), n, r);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          h[j][k] += r[k];
+          if constexpr (HBF) h[j][k] = bf16_round(h[j][k]);
+        }
+      }
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ss += h[j][k] * h[j][k];
+    if (p.h) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        if (live && count(j) > 0) store8<HBF, AL>(p.h, row * p.ldh + col(j), count(j), h[j]);
+    }
+    ss = row_sum<TPR>(ss, reinterpret_cast<float*>(red));
+    const float rstd = norm_rstd(ss, C, p.eps);
+    if (p.rstd && live && t == 0) p.rstd[row] = rstd;
+    // y in place of h
+    uint32_t mine = 0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int n = live ? count(j) : 0;
+      float g[8];
+      unpack_gamma<AL>(rg[j], p.gamma_bf16, n, g);
+      if (!AL && n > 0 && n < 8) {
+        if (p.gamma_bf16) load_tail<true>(p.gamma, col(j), n, g);
+        else load_tail<false>(p.gamma, col(j), n, g);
+      }
+      // (past the row h is 0, but r may be infinite)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        h[j][k] += r[k];
-        if constexpr (HBF) h[j][k] = bf16_round(h[j][k]);
+        h[j][k] = k < n ? (h[j][k] * rstd) * g[k] : 0.0f;
+        mine = max(mine, abs_bits(h[j][k]));
       }
     }
-  }
-  float ss = 0.0f;
+    if (p.y) {
 #pragma unroll
-  for (int j = 0; j < VPT; ++j)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) ss += h[j][k] * h[j][k];
-  if (p.h) {
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-      if (count(j) > 0) store8<HBF, AL>(p.h, oh + col(j), count(j), h[j]);
-  }
-  ss = row_sum<TPR>(ss, reinterpret_cast<float*>(red));
-  const float rstd = norm_rstd(ss, C, p.eps);
-  if (p.rstd && live && t == 0) p.rstd[row] = rstd;
-  // y in place of h
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    float g[8];
-    unpack_gamma<AL>(rg[j], p.gamma_bf16, count(j), g);
-    if (!AL && count(j) > 0 && count(j) < 8) {
-      if (p.gamma_bf16) load_tail<true>(p.gamma, col(j), count(j), g);
-      else load_tail<false>(p.gamma, col(j), count(j), g);
-    }
-    // (past the row h is 0, but r may be infinite)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) h[j][k] = k < count(j) ? (h[j][k] * rstd) * g[k] : 0.0f;
-  }
-  if (p.y) {
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (count(j) == 0) continue;
-      if (p.y_bf16) store8<true, AL>(p.y, row * p.ldy + col(j), count(j), h[j]);
-      else store8<false, AL>(p.y, row * p.ldy + col(j), count(j), h[j]);
-    }
-  }
-  if constexpr (MODE == kQNone) return;
-  const bool e5m2 = p.fmt == kE5M2;
-  if constexpr (MODE == kQTensor || MODE == kQRow) {
-    uint32_t mine = 0, amax = 0, sat = 0;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mine = max(mine, abs_bits(h[j][k]));
-    float s;
-    if constexpr (MODE == kQTensor) {
-      s = given;
-      if (p.scale_used && blockIdx.x == 0 && threadIdx.x == 0) *p.scale_used = s;
-    } else {
-      amax = canonical_amax_bits(row_max<TPR>(mine, red));
-      s = scale_from_amax(__uint_as_float(amax), e5m2 ? FmtTraits<kE5M2>::kMax : FmtTraits<kE4M3>::kMax,
-                          p.margin);
-      if (live && t == 0) {
-        p.scale_out[row] = s;
-        if (p.scale_inv) p.scale_inv[row] = __fdiv_rn(1.0f, s);
-        if (p.amax) p.amax[row] = __uint_as_float(amax);
+      for (int j = 0; j < VPT; ++j) {
+        if (!live || count(j) == 0) continue;
+        if (p.y_bf16) store8<true, AL>(p.y, row * p.ldy + col(j), count(j), h[j]);
+        else store8<false, AL>(p.y, row * p.ldy + col(j), count(j), h[j]);
       }
     }
-    // (elements past the row are zeros: they add nothing to the count)
-    u32x2 c[VPT];
-    codes8(h, s, e5m2, mine, c, sat, MODE == kQTensor && p.sat);
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-      if (count(j) > 0) store_codes<AL>(p.q + row * p.ldq + col(j), count(j), c[j]);
-    if constexpr (MODE == kQTensor) commit(mine, sat, p.amax, p.sat, red);
-  } else if constexpr (MODE == kQMx) {
-    // a block of 32 is 4 consecutive lanes (AL only; C is a multiple of 32)
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      uint32_t a = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) a = max(a, abs_bits(h[j][k]));
-      a = max(a, (uint32_t)__shfl_xor((int)a, 1));
-      a = max(a, (uint32_t)__shfl_xor((int)a, 2));
-      const int64_t c0 = col(j);
-      if (count(j) == 0) continue;
-      const uint32_t code = mx_code(a, p.fmt == kE2M1 ? 2u : e5m2 ? 15u : 8u);
-      if ((t & 3) == 0) p.mx_scales[row * p.ldms + c0 / 32] = (uint8_t)code;
-      if (p.fmt == kE2M1) {
-        const uint32_t c = code == 255u ? kFp4NanBlock : fp4_codes8(h[j], code);
-        *reinterpret_cast<uint32_t*>(p.q + row * p.ldq + c0 / 2) = c;
+    if constexpr (MODE == kQTensor || MODE == kQRow) {
+      float s = given;
+      if constexpr (MODE == kQTensor) {
+        amax = max(amax, mine);
       } else {
-        // (with a finite block no product is NaN)
-        float u[1][8];
-        u32x2 c[1];
-        uint32_t unused = 0;
+        const uint32_t a = canonical_amax_bits(row_max<TPR>(mine, red));
+        s = scale_from_amax(__uint_as_float(a),
+                            e5m2 ? FmtTraits<kE5M2>::kMax : FmtTraits<kE4M3>::kMax, p.margin);
+        if (live && t == 0) {
+          p.scale_out[row] = s;
+          if (p.scale_inv) p.scale_inv[row] = __fdiv_rn(1.0f, s);
+          if (p.amax) p.amax[row] = __uint_as_float(a);
+        }
+      }
+      // (elements past the row are zeros: they add nothing to the count)
+      u32x2 c[VPT];
+      codes8(h, s, e5m2, mine, c, sat, MODE == kQTensor && p.sat);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) u[0][k] = h[j][k];
-        codes8(u, mx_multiplier(code == 255u ? 127u : code), e5m2, 0u, c, unused, false);
-        if (code == 255u) c[0] = u32x2{0x7F7F7F7Fu, 0x7F7F7F7Fu};
-        store_codes<true>(p.q + row * p.ldq + c0, 8, c[0]);
+      for (int j = 0; j < VPT; ++j)
+        if (live && count(j) > 0) store_codes<AL>(p.q + row * p.ldq + col(j), count(j), c[j]);
+    } else if constexpr (MODE == kQMx) {
+      // a block of 32 is 4 consecutive lanes (AL only; C is a multiple of 32)
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        uint32_t a = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a = max(a, abs_bits(h[j][k]));
+        a = max(a, (uint32_t)__shfl_xor((int)a, 1));
+        a = max(a, (uint32_t)__shfl_xor((int)a, 2));
+        const int64_t c0 = col(j);
+        if (!live || count(j) == 0) continue;
+        const uint32_t code = mx_code(a, p.fmt == kE2M1 ? 2u : e5m2 ? 15u : 8u);
+        if ((t & 3) == 0) p.mx_scales[row * p.ldms + c0 / 32] = (uint8_t)code;
+        if (p.fmt == kE2M1) {
+          const uint32_t c = code == 255u ? kFp4NanBlock : fp4_codes8(h[j], code);
+          *reinterpret_cast<uint32_t*>(p.q + row * p.ldq + c0 / 2) = c;
+        } else {
+          // (with a finite block no product is NaN)
+          float u[1][8];
+          u32x2 c[1];
+          uint32_t unused = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) u[0][k] = h[j][k];
+          codes8(u, mx_multiplier(code == 255u ? 127u : code), e5m2, 0u, c, unused, false);
+          if (code == 255u) c[0] = u32x2{0x7F7F7F7Fu, 0x7F7F7F7Fu};
+          store_codes<true>(p.q + row * p.ldq + c0, 8, c[0]);
+        }
       }
     }
+    if constexpr (kAhead) {
+      now = next;
+    } else {
+      if (r0 + step < p.rows) load_row(row + step, now);
+    }
   }
+  if constexpr (MODE == kQTensor) commit(amax, sat, p.amax, p.sat, red);
 }
 
 // Rows longer than a workgroup's registers hold: one workgroup per row passes over
@@ -708,13 +729,14 @@ static RowShape row_shape(int64_t rows, int64_t cols) {
 }
 
 template <bool XBF, bool HBF, int MODE, bool AL>
-static hipError_t launch_fwd(const NormArgs& a, RowShape sh, hipStream_t stream) {
+static hipError_t launch_fwd(const NormArgs& a, RowShape sh, int num_cus, hipStream_t stream) {
 #define FP8DS_NORM_CASE(T, V)                                                                    \
   if (sh.tpr == T && sh.vpt == V) {                                                              \
-    const int rpb = T > 256 ? 1 : 256 / T;                                                       \
+    const int64_t rpb = T > 256 ? 1 : 256 / T, blocks = (a.rows + rpb - 1) / rpb;                \
+    const int64_t most = (int64_t)num_cus * (T > 256 ? 2 : 8);                                   \
     hipLaunchKernelGGL((norm_fwd_kernel<XBF, HBF, T, V, MODE, AL>),                              \
-                       dim3((unsigned)((a.rows + rpb - 1) / rpb)), dim3(T > 256 ? T : 256), 0,   \
-                       stream, a);                                                               \
+                       dim3((unsigned)(blocks < most ? blocks : most)), dim3(T > 256 ? T : 256), \
+                       0, stream, a);                                                            \
     return hipGetLastError();                                                                    \
   }
   FP8DS_NORM_CASE(16, 1)
@@ -733,23 +755,23 @@ static hipError_t launch_fwd(const NormArgs& a, RowShape sh, hipStream_t stream)
 }
 
 template <bool XBF, bool HBF>
-static hipError_t launch_fwd_t(const NormArgs& a, RowShape sh, hipStream_t s) {
+static hipError_t launch_fwd_t(const NormArgs& a, RowShape sh, int n, hipStream_t s) {
   switch (a.mode) {
-    case kQNone: return a.vec ? launch_fwd<XBF, HBF, kQNone, true>(a, sh, s)
-                              : launch_fwd<XBF, HBF, kQNone, false>(a, sh, s);
-    case kQTensor: return a.vec ? launch_fwd<XBF, HBF, kQTensor, true>(a, sh, s)
-                                : launch_fwd<XBF, HBF, kQTensor, false>(a, sh, s);
-    case kQRow: return a.vec ? launch_fwd<XBF, HBF, kQRow, true>(a, sh, s)
-                             : launch_fwd<XBF, HBF, kQRow, false>(a, sh, s);
-    default: return launch_fwd<XBF, HBF, kQMx, true>(a, sh, s);
+    case kQNone: return a.vec ? launch_fwd<XBF, HBF, kQNone, true>(a, sh, n, s)
+                              : launch_fwd<XBF, HBF, kQNone, false>(a, sh, n, s);
+    case kQTensor: return a.vec ? launch_fwd<XBF, HBF, kQTensor, true>(a, sh, n, s)
+                                : launch_fwd<XBF, HBF, kQTensor, false>(a, sh, n, s);
+    case kQRow: return a.vec ? launch_fwd<XBF, HBF, kQRow, true>(a, sh, n, s)
+                             : launch_fwd<XBF, HBF, kQRow, false>(a, sh, n, s);
+    default: return launch_fwd<XBF, HBF, kQMx, true>(a, sh, n, s);
   }
 }
 
-hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t stream) {
+hipError_t launch_norm_fwd(const NormArgs& a, int num_cus, hipStream_t stream) {
   const RowShape sh = row_shape(a.rows, a.cols);
-  if (a.x_bf16 && a.h_bf16) return launch_fwd_t<true, true>(a, sh, stream);
-  if (a.x_bf16) return launch_fwd_t<true, false>(a, sh, stream);
-  return launch_fwd_t<false, false>(a, sh, stream);
+  if (a.x_bf16 && a.h_bf16) return launch_fwd_t<true, true>(a, sh, num_cus, stream);
+  if (a.x_bf16) return launch_fwd_t<true, false>(a, sh, num_cus, stream);
+  return launch_fwd_t<false, false>(a, sh, num_cus, stream);
 }
 
 // The backward pass holds four values per element: 512 threads, whose waves may have
