@@ -126,6 +126,11 @@ __global__ __launch_bounds__(256) void mxfp4_cast_transpose_kernel(
   __syncthreads();
   // one unit: dword column `dc` (two BF16 columns, or one FP32 column), row block `rb`
   constexpr int W = BF16 ? 2 : 1;  // columns per unit
+  // (the 8 pieces of a pair of columns change places with the pair: in order, all the lanes
+  // of a store would meet in the same banks)
+  auto slot = [](int c, int rb) {
+    return (c >> 1) * 128 + (((c & 1) * 4 + rb) ^ ((c >> 1) & 7)) * 16;
+  };
 #pragma unroll 1
   for (int u = tid; u < RD * 4; u += 256) {
     const int dc = u % RD, rb = u / RD;
@@ -133,6 +138,7 @@ __global__ __launch_bounds__(256) void mxfp4_cast_transpose_kernel(
     uint32_t d[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) d[i] = tile[(rb * 32 + i) * RD + dc];
+    uint32_t scale_codes = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       uint32_t a = 0;
@@ -152,9 +158,10 @@ __global__ __launch_bounds__(256) void mxfp4_cast_transpose_kernel(
         for (int i = 0; i < 8; ++i) g[i] = f[8 * k + i];
         o[k] = code == 255u ? kFp4NanBlock : fp4_codes8(g, code);
       }
-      *reinterpret_cast<u32x4*>(&codes_t[c * 64 + rb * 16]) = o;
-      scales_t[(c0 + c) * (rows / 32) + r0 / 32 + rb] = (uint8_t)code;
+      *reinterpret_cast<u32x4*>(&codes_t[slot(c, rb)]) = o;
+      scale_codes |= code << (8 * w);
     }
+    tile[rb * 32 * RD + dc] = scale_codes;  // (these 32 dwords are this thread's own)
   }
   __syncthreads();
 #pragma unroll
@@ -162,7 +169,20 @@ __global__ __launch_bounds__(256) void mxfp4_cast_transpose_kernel(
     const int u = 256 * i + tid, c = u >> 2, rb = u & 3;
     if (rb * 32 < nr && c < nc)
       *reinterpret_cast<u32x4*>(qt + (c0 + c) * (rows / 2) + r0 / 2 + rb * 16) =
-          *reinterpret_cast<const u32x4*>(&codes_t[u * 16]);
+          *reinterpret_cast<const u32x4*>(&codes_t[slot(c, rb)]);
+  }
+  // the scale codes of a column of the tile: one dword where they are four and aligned
+  // (a byte at a time, each in a line of its own, the stores cost 10% of the call)
+  if (tid < nc) {
+    uint8_t* to = scales_t + (c0 + tid) * (rows / 32) + r0 / 32;
+    uint32_t four = 0;
+#pragma unroll
+    for (int rb = 0; rb < 4; ++rb)
+      four |= (tile[rb * 32 * RD + tid / W] >> (8 * (tid % W)) & 255u) << (8 * rb);
+    if (nr == T && (reinterpret_cast<uintptr_t>(to) & 3) == 0)
+      *reinterpret_cast<uint32_t*>(to) = four;
+    else
+      for (int rb = 0; rb * 32 < nr; ++rb) to[rb] = (uint8_t)(four >> (8 * rb));
   }
 }
 
