@@ -244,6 +244,8 @@ def _need(t, name, dtypes, n, contiguous=True):
         if not t.is_contiguous():
             raise ValueError(f"{name}: expected a contiguous tensor")
         avail = t.numel()
+    elif t.numel() >= n and t.is_contiguous():
+        return
     else:  # addressed through leading dimensions: what the storage holds past data_ptr
         avail = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
     if avail < n:

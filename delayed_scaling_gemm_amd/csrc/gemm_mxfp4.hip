@@ -364,6 +364,21 @@ __device__ __forceinline__ v16f mfma_tile(const v8i& b, const v8i& a, const v16f
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 4, kMfmaFormat<FA>, OP, sb, OP, sa);
 }
 
+// Tile of workgroup wg.  XCD x = wg % 8 takes a contiguous share of the tiles, which are
+// numbered down groups of ROWS tile rows, so that the tiles an XCD works on at a time are
+// near a square: 4 x 8 of the 32 of 256 x 256 (8 x 4: 258 us instead of 254 at
+// 8192 x 14336 x 4096, 172 instead of 168 at 16384 x 4096 x 4096; 2 x 16: 258 and 171),
+// 8 x 8 of the 64 of 128 x 128 (4 x 16: 47 us instead of 44 at 1000 x 14336 x 4096).
+template <int ROWS>
+__device__ __forceinline__ void tile_of(int wg, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int total = tiles_m * tiles_n, x = wg & 7;
+  const int i = total < 8 ? wg : x * (total >> 3) + min(x, total & 7) + (wg >> 3);
+  const int first = i / (ROWS * tiles_n) * ROWS, rows = min(tiles_m - first, ROWS);
+  const int j = i - first * tiles_n;
+  tm = first + j % rows;
+  tn = j / rows;
+}
+
 // The stages are variables of their own, and the loop names them: the compiler then knows
 // that a fragment read does not touch a buffer being loaded, and does not wait for the
 // loads in flight before each of them.
@@ -387,7 +402,7 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void gemm_mxfp4_tile_kernel(Mxfp4G
   const int r = lane & 31, h = lane >> 5;
   const int wm = (w / GN) * WM, wn = (w % GN) * WN;
   int tm, tn;
-  tile_coords(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  tile_of<BM == 256 ? 4 : 8>(blockIdx.x, tiles_m, tiles_n, tm, tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int row_a = (int)(FA == kE2M1 ? p.K / 2 : p.K), row_b = (int)(p.K / 2);
   const int nblk = (int)(p.K / 32);
