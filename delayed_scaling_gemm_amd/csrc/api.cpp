@@ -866,7 +866,10 @@ namespace {
 
 constexpr int kMaxGrads = 4096;
 constexpr int kNormBlocks = 1024;                      // partial sums per launch
-constexpr int64_t kSingleElems = 65536;                // up to here one workgroup takes the norm
+// Up to here one workgroup takes the norm: 24 thousand elements 4.7 us against 5.8 in two
+// launches; 60 thousand 6.4 against 6.0, but a second launch costs the host 1.5 us more;
+// 128 thousand 6.9 against 5.8.
+constexpr int64_t kSingleElems = 65536;
 
 int check_grads(const char* who, int n, const void* const* grads, const fp8ds_dtype* types,
                 const int64_t* counts, void* const* out, const fp8ds_dtype* out_types) {

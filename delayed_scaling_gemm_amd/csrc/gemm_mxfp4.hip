@@ -86,7 +86,10 @@ struct RowPtr {
 // A workgroup of KW waves makes 16 MT x 16 NT outputs; the waves share K, a span each at a
 // time, straight from memory to registers, and their sums are joined in LDS in a fixed
 // order.  A wave has the loads of its next span in flight while it multiplies: with few
-// rows the product is the reading of B, (1/2 + 1/32) byte per weight.
+// rows the product is the reading of B, (1/2 + 1/32) byte per weight.  Measured: 1 token x
+// 14336 x 4096 8.4 us (FP8 A 9.3), 3.7 TB/s of B; in a program whose B comes from HBM each
+// time 10.3 us.  What is over the copy's 6.1 us is the launch, the first loads' latency and
+// the join: with 4 waves a K of 4096 is two spans for each.
 template <int FA, int MT, int NT, int KW>
 __global__ __launch_bounds__(64 * KW) void gemm_mxfp4_direct_kernel(Mxfp4Gemm p) {
   constexpr int BM = 16 * MT, BN = 16 * NT;
@@ -184,6 +187,16 @@ __global__ __launch_bounds__(64 * KW) void gemm_mxfp4_direct_kernel(Mxfp4Gemm p)
 // L2 serves rows of 64 bytes at half the rate of 128: 132 us became 164 at
 // 4096 x 4096 x 16384.  Two buffers for FP8 x FP4: 416 us instead of 395 at
 // 8192 x 14336 x 4096.
+//
+// Measured with random codes (FP4 x FP4, M x N x K): 4096 x 4096 x 16384 130 us = 4.2 PFLOP/s,
+// 8192 x 14336 x 4096 254 us = 3.8, 16384 x 4096 x 4096 168 us = 3.3; FP8 x FP4
+// 8192 x 14336 x 4096 372 us = 2.6.  The instruction alone, fed from registers with random
+// codes, reaches 6.6 (4.2 for FP8 x FP8): the chip lowers its clock under it.  The matrix
+// unit is busy 65, 56 and 47% of the time.  What holds it up: LDS, of whose time a step of
+// MFMAs (512 cycles of a SIMD) takes 384 for fragment reads and 128 for the next stage's
+// arrival; and at K = 4096 the start and end of each tile, 5 to 9 us a round of tiles, of
+// which the stores of C are 1.5 to 3.5.  Waves of 128 x 128 outputs (4 a workgroup) read
+// 2/3 of the fragments and were no faster; nor did a higher wave priority around the MFMAs help.
 template <int FA>
 struct Stage {
   static constexpr int K = FA == kE2M1 ? 256 : 128;

@@ -13,6 +13,9 @@
 // Design for gfx950: HBM-bound (BF16: 2 B read, 17/32 B written per element and copy).
 // Lanes take consecutive 16-byte pieces, the 4 (BF16) or 8 (FP32) lanes of a block
 // join its amax by shuffles, and gfx950's packed conversion makes the codes.
+//
+// Measured in BF16: 14336 x 4096 cast 26.5 us and back 26.2 us, 5.6 and 5.7 TB/s (a copy of
+// 1 GiB: 5.1); with the transposed copy 16384 x 4096 48 us, 4.3 TB/s of 49/16 B per element.
 
 #include "cast_common.h"
 #include "fp4_common.h"
@@ -89,6 +92,11 @@ __global__ __launch_bounds__(256) void mxfp4_cast_kernel(const void* __restrict_
 // amax needs no exchange.  The 16 code bytes of a column block go through LDS once more
 // so that a wave writes runs of 64 bytes.  rows and cols are multiples of 32; the last
 // tiles may be partial, a 32 x 32 block never is.
+// It moves 7% more than it has to: the 4 scale codes of a column are a write of 32 bytes.
+// Tried and slower for 16384 x 4096: tiles dealt out so that each XCD has neighbours, whose
+// parts of lines could meet in its L2 (56 to 59 us, then 52), workgroups that go on to
+// further tiles with the next one's loads in flight (61 us), and BF16 pairs converted
+// without widening (1% slower).
 template <bool BF16>
 __global__ __launch_bounds__(256) void mxfp4_cast_transpose_kernel(
     const void* __restrict__ xp, int64_t rows, int64_t cols, uint8_t* __restrict__ q,
