@@ -287,13 +287,19 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
     }
   };
   const int64_t step = (int64_t)gridDim.x * RPB;
-  // The next row is on its way while this one is computed, as far as the registers go.
-  constexpr bool kAhead = VPT * (XBF ? 4 : 8) + VPT * (HBF ? 4 : 8) <= 32;
+  // The next row is on its way while this one is computed, as far as the registers go: not
+  // where 1024 threads, of 128 registers each, hold 4 groups (4096 x 20480: 243 us with it,
+  // 184 without).  Those take gamma anew for each row, too, after its reduction (129).
+  constexpr bool kFull = TPR == 1024 && VPT == 4;
+  constexpr bool kAhead = !kFull && VPT * (XBF ? 4 : 8) + VPT * (HBF ? 4 : 8) <= 32;
   RowData now;
   load_row((int64_t)blockIdx.x * RPB + slot, now);
   Raw8<false> rg[VPT];
+  auto load_gamma = [&] {
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) rg[j] = gamma8<AL>(p.gamma, p.gamma_bf16, at(j));
+    for (int j = 0; j < VPT; ++j) rg[j] = gamma8<AL>(p.gamma, p.gamma_bf16, at(j));
+  };
+  if constexpr (!kFull) load_gamma();
   const bool e5m2 = p.fmt == kE5M2;
   const float given = MODE == kQTensor ? *p.scale_in : 1.0f;
   if (MODE == kQTensor && p.scale_used && blockIdx.x == 0 && threadIdx.x == 0) *p.scale_used = given;
@@ -339,6 +345,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
     ss = row_sum<TPR>(ss, reinterpret_cast<float*>(red));
     const float rstd = norm_rstd(ss, C, p.eps);
     if (p.rstd && live && t == 0) p.rstd[row] = rstd;
+    if constexpr (kFull) load_gamma();
     // y in place of h
     uint32_t mine = 0;
 #pragma unroll
@@ -737,12 +744,15 @@ static RowShape row_shape(int64_t cols) {
   return {1024, 0};
 }
 
+// Workgroups: as many as run at once, 8 per CU of 256 threads, one of 1024 (two: 512 x 16384
+// 16.1 us, one 12.3).  Reading a row twice from memory, as longer ones are, took 347 us for
+// 4096 x 20480 and 534 for 4096 x 32768; in registers 129 and 176.
 template <bool XBF, bool HBF, int MODE, bool AL>
 static hipError_t launch_fwd(const NormArgs& a, RowShape sh, int num_cus, hipStream_t stream) {
 #define FP8DS_NORM_CASE(T, V)                                                                    \
   if (sh.tpr == T && sh.vpt == V) {                                                              \
     const int64_t rpb = T > 256 ? 1 : 256 / T, blocks = (a.rows + rpb - 1) / rpb;                \
-    const int64_t most = (int64_t)num_cus * (T > 256 ? 2 : 8);                                   \
+    const int64_t most = (int64_t)num_cus * (T > 256 ? 1 : 8);                                   \
     hipLaunchKernelGGL((norm_fwd_kernel<XBF, HBF, T, V, MODE, AL>),                              \
                        dim3((unsigned)(blocks < most ? blocks : most)), dim3(T > 256 ? T : 256), \
                        0, stream, a);                                                            \
@@ -783,7 +793,8 @@ hipError_t launch_norm_fwd(const NormArgs& a, int num_cus, hipStream_t stream) {
 }
 
 // The backward pass holds four values per element: 512 threads, whose waves may have
-// 256 registers, take up to 16384 columns; 1024 threads (128 registers) would spill.
+// 256 registers, take up to 16384 columns (4096 x 16384: 134 us, read twice 362); 1024
+// threads (128 registers) would spill.
 static RowShape bwd_shape(int64_t cols) {
   const int64_t g = (cols + 7) / 8;
   if (cols < 8) return {1024, 0};
