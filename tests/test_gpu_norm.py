@@ -358,3 +358,26 @@ def test_graph_replays_and_streams():
         both()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (h, q, am, r, dx, dg))), k
+
+
+@pytest.mark.parametrize("ht", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [4096, 12288, 16400, 20481, 32768])
+def test_many_rows_equal_few_at_a_time(cols, ht):
+    """Workgroups that go on to further rows give what they give for the first."""
+    rows, part = 600, 75
+    x, res, g = make(rows, cols, "bf16", ht, cols)
+    s = torch.full((1,), 8.0, device=DEV)
+
+    def run(a, b):
+        n = b - a
+        h, y = torch.empty(n, cols, dtype=TYPES[ht], device=DEV), torch.empty(n, cols, device=DEV)
+        q = torch.empty(n, cols, dtype=torch.uint8, device=DEV)
+        r, am = torch.empty(n, device=DEV), torch.zeros(1, device=DEV)
+        dsg.fp8ds_rmsnorm(x[a:b], g, EPS, res[a:b], h, y, r, dsg.E4M3, s, q, None, am)
+        return h, y, q, r, am
+
+    whole = run(0, rows)
+    parts = [run(a, a + part) for a in range(0, rows, part)]
+    for i in range(4):
+        assert torch.equal(whole[i], torch.cat([p[i] for p in parts]))
+    assert torch.equal(whole[4], torch.stack([p[4] for p in parts]).max(0).values)
