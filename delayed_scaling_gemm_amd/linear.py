@@ -36,13 +36,14 @@ from . import (ALGO_MAX, E2M1, E4M3, E5M2, HEALTH_COUNTS, HEALTH_NAMES, MMA_EXAC
                OP_T, fp8ds_adamw, fp8ds_cast_acc, fp8ds_cast_health, fp8ds_cast_mx,
                fp8ds_cast_mxfp4, fp8ds_gemm, fp8ds_gemm_acc, fp8ds_gemm_mx, fp8ds_gemm_mxfp4,
                fp8ds_scale_update, fp8ds_scale_update_clear)
+from .buffers import Buffers
 
 X, W, DY = 0, 1, 2
 # shortest forward reduction that runs on the FP8 matrix instructions by default
 FP8_FWD_MIN_K = 4096
 
 
-class DelayedScalingLinear:
+class DelayedScalingLinear(Buffers):
     """Delayed-scaling state of one Linear (history ring, cursor and scale per
     tensor X, W, dY) and its fwd(+bwd) step."""
 
@@ -73,7 +74,7 @@ class DelayedScalingLinear:
         self.algo = algo
         self.margin = margin
         self.fmts = tuple(fmts)
-        self.device = torch.device(device)
+        super().__init__(device)
         f32 = dict(dtype=torch.float32, device=self.device)
         self.history = torch.zeros(3, hist_len, **f32)
         self.cursor = torch.zeros(3, dtype=torch.int32, device=self.device)
@@ -93,7 +94,6 @@ class DelayedScalingLinear:
         # top-binade values (fp8ds_cast_health) into counts[X | W | DY]
         self.counts = (torch.zeros(3, HEALTH_COUNTS, dtype=torch.int64, device=self.device)
                        if health else None)
-        self._bufs = {}
 
     # views of an accumulator set
     def _amax_of(self, slot):
@@ -157,13 +157,6 @@ class DelayedScalingLinear:
         rep["step"] = self.health_step
         return rep
 
-    def _buf(self, name, shape, dtype):
-        t = self._bufs.get(name)
-        if t is None or tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-            t = torch.empty(shape, dtype=dtype, device=self.device)
-            self._bufs[name] = t
-        return t
-
     def state(self):
         """Copies of the scaling state (history, cursor, scale)."""
         return self.history.clone(), self.cursor.clone(), self.scale.clone()
@@ -207,10 +200,10 @@ class DelayedScalingLinear:
         K2, N = w.shape
         assert K == K2, "x is [M, in] and w is [in, out]"
         u8 = torch.uint8
-        xq = self._buf("xq", (M, K), u8)
-        wq = self._buf("wq", (K, N), u8)
-        wqt = self._buf("wqt", (N, K), u8)
-        y = self._buf("y", (M, N), torch.bfloat16)
+        xq = self._buf("xq", (M, K), u8, stream)
+        wq = self._buf("wq", (K, N), u8, stream)
+        wqt = self._buf("wqt", (N, K), u8, stream)
+        y = self._buf("y", (M, N), torch.bfloat16, stream)
         slot = self._slot
         s, su, am = self.scale, self.scale_used, self._amax_of(slot)
         amax_y = self._acc[slot, 3:4].view(torch.float32)
@@ -232,9 +225,9 @@ class DelayedScalingLinear:
         n_upd = 2
         if dy is not None:
             assert tuple(dy.shape) == (M, N)
-            dyq = self._buf("dyq", (M, N), u8)
-            dx = self._buf("dx", (M, K), torch.bfloat16)
-            dw = self._buf("dw", (K, N), torch.bfloat16)
+            dyq = self._buf("dyq", (M, N), u8, stream)
+            dx = self._buf("dx", (M, K), torch.bfloat16, stream)
+            dw = self._buf("dw", (K, N), torch.bfloat16, stream)
             self._cast(DY, dy, dyq, None, stream)
             # dX[M, K] = dYq[M, N] . Wq^T   (Wq stored [K, N] = [N' x K'] -> op T)
             fp8ds_gemm(OP_N, OP_T, M, K, N, dyq, self.fmts[DY], N, su[DY:DY + 1], wq, self.fmts[W],
@@ -268,14 +261,14 @@ class DelayedScalingLinear:
         ``grad_coef`` (device scalar of :func:`fp8ds_grad_norm`) clips the gradient;
         with ``grad_norm``, the norm of the same call, it is that norm's finiteness and
         not this dW's that decides, so that one bad tensor skips every layer's step."""
-        dw = self._bufs.get("dw")
+        dw = self._held("dw", stream)
         if dw is None or tuple(dw.shape) != tuple(w.shape):
             raise RuntimeError("adamw_step needs the dW of a preceding fwd+bwd step of this shape")
         if w.dtype != torch.float32:
             raise TypeError("the master weights must be fp32")
         K, N = w.shape
-        wq = self._buf("wq", (K, N), torch.uint8)
-        wqt = self._buf("wqt", (N, K), torch.uint8)
+        wq = self._buf("wq", (K, N), torch.uint8, stream)
+        wqt = self._buf("wqt", (N, K), torch.uint8, stream)
         # the new weights' amax and saturation go into the next step's set
         s, su = self.scale, self.scale_used
         am, sat = self._amax_of(self._slot), self._sat_of(self._slot)
@@ -286,7 +279,7 @@ class DelayedScalingLinear:
         self._w_prepared = w
 
 
-class BatchedDelayedScalingLinear:
+class BatchedDelayedScalingLinear(Buffers):
     """Forward pass of ``batch`` independent small Linears, each with its own
     delayed-scaling state for X and W.
 
@@ -311,7 +304,7 @@ class BatchedDelayedScalingLinear:
         self.algo = algo
         self.margin = margin
         self.fmt = fmt
-        self.device = torch.device(device)
+        super().__init__(device)
         f32 = dict(dtype=torch.float32, device=self.device)
         n = 2 * batch
         self.history = torch.zeros(n, hist_len, **f32)
@@ -321,14 +314,6 @@ class BatchedDelayedScalingLinear:
         self.amax = torch.zeros(n, **f32)
         self.sat = torch.zeros(n, dtype=torch.int64, device=self.device)
         self.amax_y = torch.zeros(batch, **f32)
-        self._bufs = {}
-
-    def _buf(self, name, shape, dtype):
-        t = self._bufs.get(name)
-        if t is None or tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-            t = torch.empty(shape, dtype=dtype, device=self.device)
-            self._bufs[name] = t
-        return t
 
     def takes_fused(self, x, w) -> bool:
         """Whether ``step`` runs as the one-launch fused kernel for these inputs."""
@@ -346,9 +331,9 @@ class BatchedDelayedScalingLinear:
         B, M, K = x.shape
         B2, K2, N = w.shape
         assert B == B2 == self.batch and K == K2
-        xq = self._buf("xq", (B, M, K), torch.uint8)
-        wq = self._buf("wq", (B, K, N), torch.uint8)
-        y = self._buf("y", (B, M, N), torch.bfloat16)
+        xq = self._buf("xq", (B, M, K), torch.uint8, stream)
+        wq = self._buf("wq", (B, K, N), torch.uint8, stream)
+        y = self._buf("y", (B, M, N), torch.bfloat16, stream)
         s, su, am, sat = self.scale, self.scale_used, self.amax, self.sat
         if self.takes_fused(x, w):
             fp8ds_linear_batched(x, w, self.fmt, self.fmt, self.history, self.cursor, self.algo,
@@ -364,7 +349,7 @@ class BatchedDelayedScalingLinear:
         return {"xq": xq, "wq": wq, "y": y}
 
 
-class MXLinear:
+class MXLinear(Buffers):
     """The same Linear step in MXFP8 ("FP8 混合精度训练工程实践" §九: blocks of 32
     values along the contraction sharing an E8M0 scale).  There is no scaling
     state: every block's scale comes from the block itself.  Each tensor is cast
@@ -380,23 +365,17 @@ class MXLinear:
 
     def __init__(self, fmts=(E4M3, E4M3, E5M2), device="cuda", mma: int = MMA_EXACT):
         self.fmts = tuple(fmts)
-        self.device = torch.device(device)
+        super().__init__(device)
         self.mma = mma
-        self._bufs = {}
         self.amax_y = torch.zeros(1, dtype=torch.float32, device=self.device)
-
-    def _buf(self, name, shape, dtype):
-        b = self._bufs.get(name)
-        if b is None or tuple(b.shape) != tuple(shape) or b.dtype != dtype:
-            b = torch.empty(shape, dtype=dtype, device=self.device)
-            self._bufs[name] = b
-        return b
 
     def _cast(self, t, name, x, stream):
         r, c = x.shape
         u8 = torch.uint8
-        q, s = self._buf(name + "q", (r, c), u8), self._buf(name + "s", (r, c // 32), u8)
-        qt, st = self._buf(name + "qt", (c, r), u8), self._buf(name + "st", (c, r // 32), u8)
+        q = self._buf(name + "q", (r, c), u8, stream)
+        s = self._buf(name + "s", (r, c // 32), u8, stream)
+        qt = self._buf(name + "qt", (c, r), u8, stream)
+        st = self._buf(name + "st", (c, r // 32), u8, stream)
         fp8ds_cast_mx(x, self.fmts[t], q, s, qt, st, stream)
         return q, s, qt, st
 
@@ -412,20 +391,20 @@ class MXLinear:
         bf = torch.bfloat16
         xq, xs, xqt, xst = self._cast(X, "x", x, stream)
         wq, ws, wqt, wst = self._cast(W, "w", w, stream)
-        y = self._buf("y", (M, N), bf)
+        y = self._buf("y", (M, N), bf, stream)
         self._gemm(M, N, K, xq, xs, self.fmts[X], wqt, wst, self.fmts[W], y, stream, self.amax_y)
         out = {"y": y, "xq": xq, "xs": xs, "xqt": xqt, "xst": xst, "wq": wq, "ws": ws,
                "wqt": wqt, "wst": wst}
         if dy is not None:
             dyq, dys, dyqt, dyst = self._cast(DY, "dy", dy, stream)
-            dx, dw = self._buf("dx", (M, K), bf), self._buf("dw", (K, N), bf)
+            dx, dw = self._buf("dx", (M, K), bf, stream), self._buf("dw", (K, N), bf, stream)
             self._gemm(M, K, N, dyq, dys, self.fmts[DY], wq, ws, self.fmts[W], dx, stream)
             self._gemm(K, N, M, xqt, xst, self.fmts[X], dyqt, dyst, self.fmts[DY], dw, stream)
             out.update(dx=dx, dw=dw, dyq=dyq, dys=dys, dyqt=dyqt, dyst=dyst)
         return out
 
 
-class MXFP4Linear:
+class MXFP4Linear(Buffers):
     """The Linear in MXFP4: every operand in blocks of 32 E2M1 elements along the
     contraction, each with its E8M0 scale.
 
@@ -441,21 +420,15 @@ class MXFP4Linear:
     ``fmt`` E4M3 or E5M2, in MXFP8."""
 
     def __init__(self, device="cuda"):
-        self.device = torch.device(device)
-        self._bufs = {}
-
-    def _buf(self, name, shape, dtype):
-        b = self._bufs.get(name)
-        if b is None or b.shape != shape or b.dtype != dtype:
-            b = torch.empty(shape, dtype=dtype, device=self.device)
-            self._bufs[name] = b
-        return b
+        super().__init__(device)
 
     def _cast(self, name, x, stream):
         r, c = x.shape
         u8 = torch.uint8
-        q, s = self._buf(name + "q", (r, c // 2), u8), self._buf(name + "s", (r, c // 32), u8)
-        qt, st = self._buf(name + "qt", (c, r // 2), u8), self._buf(name + "st", (c, r // 32), u8)
+        q = self._buf(name + "q", (r, c // 2), u8, stream)
+        s = self._buf(name + "s", (r, c // 32), u8, stream)
+        qt = self._buf(name + "qt", (c, r // 2), u8, stream)
+        st = self._buf(name + "st", (c, r // 32), u8, stream)
         fp8ds_cast_mxfp4(x, q, s, qt, st, stream)
         return q, s, qt, st
 
@@ -472,20 +445,21 @@ class MXFP4Linear:
     def forward(self, x, fmt=E2M1, stream=None):
         """y [tokens, out] BF16 of ``x`` [tokens, in] with the weights of :meth:`quantize`
         (of the last :meth:`step` where that came later)."""
-        if "wqt" not in self._bufs:
+        wqt, wst = self._held("wqt", stream), self._held("wst", stream)
+        if wqt is None:
             raise RuntimeError("forward() needs the weights of a preceding quantize()")
         K, N = self.shape
         M = x.shape[0]
         if x.shape[1] != K:
             raise ValueError(f"x has {x.shape[1]} features, the weights {K}")
-        xq = self._buf("fq", (M, K // 2 if fmt == E2M1 else K), torch.uint8)
-        xs = self._buf("fs", (M, K // 32), torch.uint8)
+        xq = self._buf("fq", (M, K // 2 if fmt == E2M1 else K), torch.uint8, stream)
+        xs = self._buf("fs", (M, K // 32), torch.uint8, stream)
         if fmt == E2M1:
             fp8ds_cast_mxfp4(x, xq, xs, stream=stream)
         else:
             fp8ds_cast_mx(x, fmt, xq, xs, stream=stream)
-        return self._gemm(M, N, K, xq, xs, fmt, self._bufs["wqt"], self._bufs["wst"],
-                          self._buf("fy", (M, N), torch.bfloat16), stream)
+        return self._gemm(M, N, K, xq, xs, fmt, wqt, wst,
+                          self._buf("fy", (M, N), torch.bfloat16, stream), stream)
 
     def step(self, x, w, dy=None, stream=None):
         """x [M, K], w [K, N] (and dy [M, N]), BF16 or FP32 on the device.  Returns the BF16
@@ -495,12 +469,13 @@ class MXFP4Linear:
         xq, xs, xqt, xst = self._cast("x", x, stream)
         wq, ws, wqt, wst = self._cast("w", w, stream)
         self.shape = (K, N)
-        y = self._gemm(M, N, K, xq, xs, E2M1, wqt, wst, self._buf("y", (M, N), bf), stream)
+        y = self._gemm(M, N, K, xq, xs, E2M1, wqt, wst, self._buf("y", (M, N), bf, stream), stream)
         out = {"y": y, "xq": xq, "xs": xs, "xqt": xqt, "xst": xst, "wq": wq, "ws": ws,
                "wqt": wqt, "wst": wst}
         if dy is not None:
             dyq, dys, dyqt, dyst = self._cast("dy", dy, stream)
-            dx = self._gemm(M, K, N, dyq, dys, E2M1, wq, ws, self._buf("dx", (M, K), bf), stream)
-            dw = self._gemm(K, N, M, xqt, xst, E2M1, dyqt, dyst, self._buf("dw", (K, N), bf), stream)
+            dx, dw = self._buf("dx", (M, K), bf, stream), self._buf("dw", (K, N), bf, stream)
+            self._gemm(M, K, N, dyq, dys, E2M1, wq, ws, dx, stream)
+            self._gemm(K, N, M, xqt, xst, E2M1, dyqt, dyst, dw, stream)
             out.update(dx=dx, dw=dw, dyq=dyq, dys=dys, dyqt=dyqt, dyst=dyst)
         return out
