@@ -2,6 +2,8 @@
 torch's stream calls are stand-ins, only the host's bookkeeping runs)."""
 
 import contextlib
+import gc
+import weakref
 
 import pytest
 import torch
@@ -117,3 +119,27 @@ def test_use_on_a_further_stream_is_recorded(layer, world):
     n = len(world.recorded)
     call(32, FakeStream(9)), call(32, None)
     assert len(world.recorded) == n  # once for each stream
+
+
+@pytest.mark.parametrize("how", ["captured", "prepared"])
+def test_buffers_of_captured_and_prepared_launches_stay(layer, world, monkeypatch, how):
+    """A graph and a prepared launch hold addresses: another shape must not free them."""
+    obj, call = layer
+    call(32, None)
+    if how == "captured":
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+        call(32, None)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    else:
+        launch = dsg.prepare(lambda: call(32, None))
+        assert callable(launch)
+    held = [weakref.ref(t) for t in obj._bufs.values()]
+    call(96, None), call(64, None)
+    gc.collect()
+    assert all(r() is not None for r in held)
+    # and what no graph knows is given up
+    eager = {n: (weakref.ref(t), t.shape) for n, t in obj._bufs.items()}
+    call(128, None)
+    gc.collect()
+    changed = [r for n, (r, shape) in eager.items() if obj._bufs[n].shape != shape]
+    assert changed and all(r() is None for r in changed)

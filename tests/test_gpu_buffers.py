@@ -65,3 +65,35 @@ def test_serving_on_another_stream(make, as_handle):
     assert own == set(layer._bufs)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("make", [mxfp4, stack])
+@pytest.mark.parametrize("how", ["graph", "prepared"])
+def test_replays_after_calls_with_other_token_counts(make, how):
+    C, n = 256, 24
+    layer, call = make(C)
+    x = tokens(n, C)
+    call(x)
+    torch.cuda.synchronize()
+    if how == "graph":
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = call(x)
+        replay = graph.replay
+    else:
+        ys = []
+        replay = dsg.prepare(lambda: ys.append(call(x)))
+        y = ys[0]
+    for k in range(3):
+        call(tokens(100 + k, C))
+        # what the allocator would hand out of memory that the replay still writes
+        others = [torch.full(t.shape, 3, dtype=t.dtype, device=DEV) for t in layer._bufs.values()
+                  for _ in range(4)]
+        others += [torch.full((n, w), 3, dtype=torch.uint8, device=DEV)
+                   for w in (C // 32, C // 2, C, 2 * C) for _ in range(4)]
+        x.copy_(tokens(n, C, seed=k + 1))
+        replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        assert all(bool((o == 3).all()) for o in others)
+        assert torch.equal(got, call(x)), k
