@@ -70,6 +70,7 @@ class NormLinearStack(Buffers):
         self.steps = 0
         self._prepared = False  # optimizer_step wrote this step's FP8 weights
         self._pending = False   # a forward has not met its backward yet
+        self._fresh = False     # a backward's gradients have not been applied yet
 
     def _state(self, which, layer):
         """(scale, scale_used, amax of this step) of X, W or dY of a layer."""
@@ -146,7 +147,7 @@ class NormLinearStack(Buffers):
         fp8ds_scale_update_clear(self.history, self.cursor, self._amax[now], self.fmts, self.algo,
                                  self.margin, self.scale, self._amax[now ^ 1], stream=stream)
         self.steps += 1
-        self._pending = False
+        self._pending, self._fresh = False, True
         return dh
 
     def grads(self, stream=None):
@@ -159,9 +160,13 @@ class NormLinearStack(Buffers):
                        grad_scale=1.0, stream=None):
         """AdamW with the gradients clipped to the global norm ``max_norm`` (gammas without
         decay), and the FP8 weights of the next forward.  ``norm`` and ``coef`` hold the norm
-        (times ``grad_scale``) and the factor; a norm that is not finite skips the step."""
-        if self.steps < 1 or "dg0" not in self._bufs:
-            raise RuntimeError("optimizer_step() needs a preceding backward()")
+        (times ``grad_scale``) and the factor; a norm that is not finite skips the step.
+
+        Once for a :meth:`backward`, before the next :meth:`forward`: it writes the FP8 weights
+        that a pending backward would read."""
+        if self._pending or not self._fresh:
+            raise RuntimeError("optimizer_step() comes once after each backward(), before the next "
+                               "forward()")
         C, u8, g = self.width, torch.uint8, self.grads(stream)
         ws = self._buf("norm_ws", (fp8ds_grad_norm_workspace(),), u8, stream)
         fp8ds_grad_norm(g, max_norm, self.norm, self.coef, ws, grad_scale, stream)
@@ -176,7 +181,7 @@ class NormLinearStack(Buffers):
             fp8ds_adamw(p, g[i], m, v, lr, beta1, beta2, eps, decay, self.steps,
                         grad_scale=grad_scale, grad_amax=self.norm, stream=stream,
                         grad_coef=self.coef, **cast)
-        self._prepared = True
+        self._prepared, self._fresh = True, False
 
     def quantize(self, stream=None):
         """Write the weights' MXFP4 codes for :meth:`decode`."""
