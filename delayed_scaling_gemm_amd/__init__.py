@@ -10,7 +10,7 @@ Functions keep the C names: ``fp8ds_amax``, ``fp8ds_cast``, ``fp8ds_cast_health`
 ``fp8ds_cast_batched``, ``fp8ds_scale_update``, ``fp8ds_gemm``, ``fp8ds_gemm_batched``,
 ``fp8ds_linear_batched``, ``fp8ds_adamw``; around the Linear ``fp8ds_rmsnorm`` (``_rowwise``,
 ``_mx``, ``_bwd``), ``fp8ds_grad_norm``, ``fp8ds_grad_clip``, ``fp8ds_cast_mxfp4``,
-``fp8ds_dequant_mxfp4``, ``fp8ds_gemm_mxfp4``.
+``fp8ds_dequant_mxfp4``, ``fp8ds_gemm_mxfp4`` (``_mma``).
 """
 
 from __future__ import annotations
@@ -122,8 +122,10 @@ def _declare(lib):
     lib.fp8ds_dequant_mxfp4.restype = i32
     lib.fp8ds_dequant_mxfp4.argtypes = [vp, vp, i64, i64, vp, i32, vp]
     lib.fp8ds_gemm_mxfp4.restype = i32
-    lib.fp8ds_gemm_mxfp4.argtypes = [i64, i64, i64, vp, i32, i64, vp, i64, vp, i64, vp, i64, vp,
-                                     i32, i64, vp, vp]
+    gemm4 = [i64, i64, i64, vp, i32, i64, vp, i64, vp, i64, vp, i64, vp, i32, i64, vp]
+    lib.fp8ds_gemm_mxfp4.argtypes = gemm4 + [vp]
+    lib.fp8ds_gemm_mxfp4_mma.restype = i32
+    lib.fp8ds_gemm_mxfp4_mma.argtypes = gemm4 + [i32, vp]
     return lib
 
 
@@ -875,10 +877,11 @@ def fp8ds_dequant_mxfp4(q, scales, y, stream=None):
 
 
 def fp8ds_gemm_mxfp4(M, N, K, a, fa, lda, scales_a, ld_scales_a, b, ldb, scales_b, ld_scales_b, c,
-                     ldc, amax_c=None, stream=None):
+                     ldc, amax_c=None, stream=None, mma=MMA_EXACT):
     """``C = A B^T`` with B [N, K] in MXFP4 and A [M, K] in MXFP4 (``fa`` = E2M1) or MXFP8:
     codes with E8M0 block scales [M, ld_scales_a] / [N, ld_scales_b] along K, a multiple of 32;
-    ``lda`` and ``ldb`` in elements."""
+    ``lda`` and ``ldb`` in elements.  ``mma`` is the datapath of an MXFP8 A: FP32 sums, or
+    (``MMA_FP8``) the FP8 matrix instructions' (``fp8ds_gemm_mxfp4_mma``)."""
     import torch
 
     u8, high = (torch.uint8,), _high()
@@ -890,9 +893,12 @@ def fp8ds_gemm_mxfp4(M, N, K, a, fa, lda, scales_a, ld_scales_a, b, ldb, scales_
         _need(scales_b, "scales_b", u8, _span(N, K // 32, ld_scales_b), contiguous=False)
     _need(c, "c", high, _span(M, N, ldc), contiguous=False)
     _need(amax_c, "amax_c", (torch.float32,), 1)
-    _call("fp8ds_gemm_mxfp4", M, N, K, _ptr(a), fa, lda, _ptr(scales_a), ld_scales_a, _ptr(b), ldb,
-          _ptr(scales_b), ld_scales_b, _ptr(c), _dtype_code(c), ldc, _ptr(amax_c),
-          _stream(stream))
+    args = (M, N, K, _ptr(a), fa, lda, _ptr(scales_a), ld_scales_a, _ptr(b), ldb, _ptr(scales_b),
+            ld_scales_b, _ptr(c), _dtype_code(c), ldc, _ptr(amax_c))
+    if mma == MMA_EXACT:
+        _call("fp8ds_gemm_mxfp4", *args, _stream(stream))
+    else:
+        _call("fp8ds_gemm_mxfp4_mma", *args, mma, _stream(stream))
 
 
 def abi_version() -> int:

@@ -41,13 +41,15 @@ class NormLinearStack(Buffers):
 
     def __init__(self, layers: int, width: int, eps: float = 1e-5, hist_len: int = 16,
                  algo: int = ALGO_MAX, margin: int = 0, stream_dtype=torch.bfloat16,
-                 device="cuda", mma_bwd: int = MMA_EXACT):
+                 device="cuda", mma_bwd: int = MMA_EXACT, mma_decode: int = MMA_EXACT):
         if layers < 1 or width < 32 or width % 32:
             raise ValueError(f"layers {layers} must be positive, width {width} a multiple of 32")
         if stream_dtype not in (torch.bfloat16, torch.float32):
             raise TypeError("the residual stream is bf16 or fp32")
         self.layers, self.width, self.eps = layers, width, eps
-        self.algo, self.margin, self.mma_bwd = algo, margin, mma_bwd
+        self.algo, self.margin = algo, margin
+        # datapaths of the backward products, and of decode()'s with MXFP8 activations
+        self.mma_bwd, self.mma_decode = mma_bwd, mma_decode
         self.stream_dtype = stream_dtype
         super().__init__(device)
         f32 = dict(dtype=torch.float32, device=self.device)
@@ -208,7 +210,8 @@ class NormLinearStack(Buffers):
             fp8ds_rmsnorm_mx(x, self.gamma[i], self.eps, fmt, q, qs, residual, h, stream=stream)
             x = self._buf("sx", (T, C), bf, stream)
             fp8ds_gemm_mxfp4(T, C, C, q, fmt, C, qs, C // 32, self._held(f"m4t{i}", stream),
-                             C, self._held(f"m4st{i}", stream), C // 32, x, C, None, stream)
+                             C, self._held(f"m4st{i}", stream), C // 32, x, C, None, stream,
+                             self.mma_decode)
             residual = h  # in place from here on
         y = self._buf("sy", (T, C), bf, stream)
         fp8ds_rmsnorm(x, self.gamma[-1], self.eps, residual, None, y, stream=stream)

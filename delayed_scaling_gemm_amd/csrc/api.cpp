@@ -1029,11 +1029,13 @@ int fp8ds_dequant_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t rows, i
                     who);
 }
 
-int fp8ds_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t* A, fp8ds_format fa,
-                     int64_t lda, const uint8_t* scales_a, int64_t ld_scales_a, const uint8_t* B,
-                     int64_t ldb, const uint8_t* scales_b, int64_t ld_scales_b, void* C,
-                     fp8ds_dtype ct, int64_t ldc, float* amax_c, hipStream_t stream) {
-  const char* who = "fp8ds_gemm_mxfp4";
+static int gemm_mxfp4_common(const char* who, int64_t M, int64_t N, int64_t K, const uint8_t* A,
+                             fp8ds_format fa, int64_t lda, const uint8_t* scales_a,
+                             int64_t ld_scales_a, const uint8_t* B, int64_t ldb,
+                             const uint8_t* scales_b, int64_t ld_scales_b, void* C, fp8ds_dtype ct,
+                             int64_t ldc, float* amax_c, fp8ds_mma mma, hipStream_t stream) {
+  if (mma != FP8DS_MMA_EXACT && mma != FP8DS_MMA_FP8)
+    return fail(FP8DS_ERR_ENUM, "%s: bad mma %d", who, (int)mma);
   if (!valid_mx_fmt(fa)) return fail(FP8DS_ERR_ENUM, "%s: bad format %d", who, (int)fa);
   if (!valid_dtype(ct)) return fail(FP8DS_ERR_ENUM, "%s: bad output dtype", who);
   const int64_t lim = int64_t(1) << 31;
@@ -1072,9 +1074,26 @@ int fp8ds_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t* A, fp8ds_fo
     p.A = A; p.lda = lda; p.sc_a = scales_a; p.ldsa = ld_scales_a;
     p.B = B; p.ldb = ldb; p.sc_b = scales_b; p.ldsb = ld_scales_b;
     p.C = C; p.out_bf16 = ct == FP8DS_BF16; p.ldc = ldc; p.amax_c = amax_c;
-    e = fp8ds::launch_gemm_mxfp4(p, (int)fa, num_cus(), stream);
+    e = fp8ds::launch_gemm_mxfp4(p, (int)fa, mma == FP8DS_MMA_EXACT, num_cus(), stream);
   }
   return hip_status(e, who);
+}
+
+int fp8ds_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t* A, fp8ds_format fa,
+                     int64_t lda, const uint8_t* scales_a, int64_t ld_scales_a, const uint8_t* B,
+                     int64_t ldb, const uint8_t* scales_b, int64_t ld_scales_b, void* C,
+                     fp8ds_dtype ct, int64_t ldc, float* amax_c, hipStream_t stream) {
+  return gemm_mxfp4_common("fp8ds_gemm_mxfp4", M, N, K, A, fa, lda, scales_a, ld_scales_a, B, ldb,
+                           scales_b, ld_scales_b, C, ct, ldc, amax_c, FP8DS_MMA_EXACT, stream);
+}
+
+int fp8ds_gemm_mxfp4_mma(int64_t M, int64_t N, int64_t K, const uint8_t* A, fp8ds_format fa,
+                         int64_t lda, const uint8_t* scales_a, int64_t ld_scales_a,
+                         const uint8_t* B, int64_t ldb, const uint8_t* scales_b,
+                         int64_t ld_scales_b, void* C, fp8ds_dtype ct, int64_t ldc, float* amax_c,
+                         fp8ds_mma mma, hipStream_t stream) {
+  return gemm_mxfp4_common("fp8ds_gemm_mxfp4_mma", M, N, K, A, fa, lda, scales_a, ld_scales_a, B,
+                           ldb, scales_b, ld_scales_b, C, ct, ldc, amax_c, mma, stream);
 }
 
 }  // extern "C"

@@ -249,7 +249,8 @@ hipError_t launch_mxfp4_cast_transpose(const void* x, bool bf16, int64_t rows, i
 hipError_t launch_mxfp4_dequant(const uint8_t* q, const uint8_t* scales, int64_t n, void* y,
                                 bool bf16, hipStream_t stream);
 
-// C = A B^T, B in MXFP4, A of format fa (E4M3, E5M2 or E2M1 = 2) with block scales.
+// C = A B^T, B in MXFP4, A of format fa (E4M3, E5M2 or E2M1 = 2) with block scales; `exact`:
+// an FP8 A on the BF16 matrix instructions.
 struct Mxfp4Gemm {
   int64_t M, N, K;       // K a multiple of 32
   const uint8_t* A;
@@ -265,6 +266,7 @@ struct Mxfp4Gemm {
   int64_t ldc;
   float* amax_c;         // or null: combined into
 };
-hipError_t launch_gemm_mxfp4(const Mxfp4Gemm& p, int fa, int num_cus, hipStream_t stream);
+hipError_t launch_gemm_mxfp4(const Mxfp4Gemm& p, int fa, bool exact, int num_cus,
+                             hipStream_t stream);
 
 }  // namespace fp8ds

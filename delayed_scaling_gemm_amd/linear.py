@@ -417,10 +417,12 @@ class MXFP4Linear(Buffers):
 
     tokens, in and out multiples of 32.  Serving: :meth:`quantize` keeps W's codes, then
     :meth:`forward` takes any number of tokens, its activations in MXFP4 or, with
-    ``fmt`` E4M3 or E5M2, in MXFP8."""
+    ``fmt`` E4M3 or E5M2, in MXFP8.  ``mma`` picks the datapath of a product with MXFP8
+    activations (FP32 sums, or the block-scaled FP8 instruction's)."""
 
-    def __init__(self, device="cuda"):
+    def __init__(self, device="cuda", mma: int = MMA_EXACT):
         super().__init__(device)
+        self.mma = mma
 
     def _cast(self, name, x, stream):
         r, c = x.shape
@@ -432,9 +434,9 @@ class MXFP4Linear(Buffers):
         fp8ds_cast_mxfp4(x, q, s, qt, st, stream)
         return q, s, qt, st
 
-    @staticmethod
-    def _gemm(m, n, k, a, sa, fa, b, sb, out, stream):
-        fp8ds_gemm_mxfp4(m, n, k, a, fa, k, sa, k // 32, b, k, sb, k // 32, out, n, None, stream)
+    def _gemm(self, m, n, k, a, sa, fa, b, sb, out, stream):
+        fp8ds_gemm_mxfp4(m, n, k, a, fa, k, sa, k // 32, b, k, sb, k // 32, out, n, None, stream,
+                         self.mma)
         return out
 
     def quantize(self, w, stream=None):

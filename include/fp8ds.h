@@ -689,9 +689,12 @@ int fp8ds_dequant_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t rows, i
 /*
  * fp8ds_gemm_mxfp4 -- C = A B^T with B [N x K] in MXFP4 and A [M x K] in MXFP4 or MXFP8:
  *   C[i][j] = convert_ct( sum_k X_a(i, k/32) a(i,k) X_b(j, k/32) b(j,k) )
- * on gfx950's block-scaled matrix instruction, with FP32 accumulation (across a group of
- * products of an FP8 A the summation precision of FP8DS_MMA_FP8).  A NaN block makes
- * every output that it touches NaN.
+ * with exact products and FP32 sums.  MXFP4 x MXFP4 runs on gfx950's block-scaled matrix
+ * instruction.  An FP8 A, whose products that instruction adds in fewer bits, is by default
+ * widened with B to BF16 times the block scales, as fp8ds_gemm_mx widens its operands: exact
+ * where the scaled values are normal BF16 numbers (or zero), i.e. for scale codes from 10 (A
+ * E4M3) or 17 (E5M2) up to 246 or 239, and to 252 of B.  A NaN block makes every output that it
+ * touches NaN.
  *   A, fa      E2M1 (two per byte), E4M3 or E5M2; rows lda ELEMENTS apart.
  *   scales_a   [M x ld_scales_a] E8M0 codes; scales_b [N x ld_scales_b].
  *   B          E2M1; rows ldb ELEMENTS apart.
@@ -703,6 +706,18 @@ int fp8ds_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t* A, fp8ds_fo
                      int64_t lda, const uint8_t* scales_a, int64_t ld_scales_a, const uint8_t* B,
                      int64_t ldb, const uint8_t* scales_b, int64_t ld_scales_b, void* C,
                      fp8ds_dtype ct, int64_t ldc, float* amax_c, hipStream_t stream);
+
+/*
+ * fp8ds_gemm_mxfp4_mma -- fp8ds_gemm_mxfp4 with the datapath of an FP8 A named:
+ * FP8DS_MMA_EXACT (what fp8ds_gemm_mxfp4 takes), or FP8DS_MMA_FP8: the block-scaled FP8
+ * instruction at up to twice the rate, with its summation precision (see fp8ds_mma).  An
+ * MXFP4 A takes the same path for both.
+ */
+int fp8ds_gemm_mxfp4_mma(int64_t M, int64_t N, int64_t K, const uint8_t* A, fp8ds_format fa,
+                         int64_t lda, const uint8_t* scales_a, int64_t ld_scales_a,
+                         const uint8_t* B, int64_t ldb, const uint8_t* scales_b,
+                         int64_t ld_scales_b, void* C, fp8ds_dtype ct, int64_t ldc, float* amax_c,
+                         fp8ds_mma mma, hipStream_t stream);
 
 #ifdef __cplusplus
 }
