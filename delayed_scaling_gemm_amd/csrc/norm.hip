@@ -430,14 +430,15 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd_kernel(NormArg
   if constexpr (MODE == kQTensor) commit(amax, sat, p.amax, p.sat, red);
 }
 
-// Rows longer than a workgroup's registers hold: one workgroup per row passes over
-// it two or three times (sum of squares; row amax; output).  h is taken back from
-// p.h where it is stored, since p.h may be the residual's own buffer.
+// Rows longer than a workgroup's registers hold, and rows without a whole group of 8: one
+// workgroup per row, from row0 on, passes over it two or three times (sum of squares; row
+// amax; output).  h is taken back from p.h where it is stored, since p.h may be the
+// residual's own buffer.
 template <bool XBF, bool HBF, int MODE>
-__global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormArgs p) {
+__global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormArgs p, int64_t row0) {
   __shared__ uint32_t red[2 * 16];
   const int t = threadIdx.x;
-  const int64_t row = blockIdx.x, C = p.cols;
+  const int64_t row = row0 + blockIdx.x, C = p.cols;
   const int64_t ox = row * p.ldx, orr = row * p.ldr, oh = row * p.ldh;
   auto fresh = [&](int64_t c) {
     float v = load1<XBF>(p.x, ox + c);
@@ -767,9 +768,17 @@ static hipError_t launch_fwd(const NormArgs& a, RowShape sh, int num_cus, hipStr
   FP8DS_NORM_CASE(1024, 2)
   FP8DS_NORM_CASE(1024, 4)
 #undef FP8DS_NORM_CASE
-  hipLaunchKernelGGL((norm_fwd_long_kernel<XBF, HBF, MODE>), dim3((unsigned)a.rows), dim3(1024), 0,
-                     stream, a);
-  return hipGetLastError();
+  // A grid holds fewer than 2^32 threads; of a larger one HIP drops the excess without an error.
+  // (Workgroups that go on to further rows instead: 4096 x 40000 981 us, a row each 656.)
+  constexpr int64_t kSlice = 1 << 21;
+  for (int64_t r0 = 0; r0 < a.rows; r0 += kSlice) {
+    const int64_t n = a.rows - r0 < kSlice ? a.rows - r0 : kSlice;
+    hipLaunchKernelGGL((norm_fwd_long_kernel<XBF, HBF, MODE>), dim3((unsigned)n), dim3(1024), 0,
+                       stream, a, r0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <bool XBF, bool HBF>
