@@ -701,12 +701,13 @@ __global__ __launch_bounds__(1024) void norm_bwd_long_kernel(NormBwdArgs p) {
 }
 
 // dgamma[c] = sum of `parts` partial rows: 32 columns x 16 shares of the rows per
-// workgroup, joined in LDS in a fixed order.
+// workgroup, joined in LDS in a fixed order; columns from c0 on.
 __global__ __launch_bounds__(512) void norm_dgamma_kernel(const float* __restrict__ work, int parts,
-                                                          int64_t C, float* __restrict__ dgamma) {
+                                                          int64_t C, float* __restrict__ dgamma,
+                                                          int64_t c0) {
   __shared__ float part[16][33];
   const int cl = threadIdx.x & 31, sh = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + cl;
+  const int64_t c = c0 + (int64_t)blockIdx.x * 32 + cl;
   float v = 0.0f;
   if (c < C) {
 #pragma unroll 4
@@ -858,9 +859,15 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
                 : launch_bwd<false, false, false>(a, sh, parts, stream);
   }
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((a.cols + 31) / 32)), dim3(512), 0, stream,
-                     a.work, parts, a.cols, a.dgamma);
-  return hipGetLastError();
+  constexpr int64_t kSlice = 1 << 27;  // columns; 2^31 threads, of fewer than 2^32 in a grid
+  for (int64_t c0 = 0; c0 < a.cols; c0 += kSlice) {
+    const int64_t n = a.cols - c0 < kSlice ? a.cols - c0 : kSlice;
+    hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((n + 31) / 32)), dim3(512), 0, stream,
+                       a.work, parts, a.cols, a.dgamma, c0);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace fp8ds

@@ -79,3 +79,16 @@ def test_many_long_rows():
         dsg.fp8ds_rmsnorm_mx(xc[a:a + 100], gamma[:c32], EPS, dsg.E4M3, q1[a:a + 100], sc1[a:a + 100])
     torch.cuda.synchronize()
     assert torch.equal(q, q1) and torch.equal(sc, sc1)
+
+
+def test_backward_of_a_row_of_2_28_columns():
+    """dgamma's join takes 32 columns a workgroup of 512: 2^32 threads and more."""
+    cols = (1 << 28) + 40
+    g = torch.Generator(device=DEV).manual_seed(4)
+    h, dy = rand(g, 1, cols).to(BF), rand(g, 1, cols).to(BF)
+    gamma, r = torch.ones(cols, dtype=BF, device=DEV), torch.full((1,), 0.5, device=DEV)
+    dx, dg = torch.empty_like(h), torch.full((cols,), 7.0, device=DEV)
+    ws = torch.empty(dsg.fp8ds_rmsnorm_bwd_workspace(1, cols), dtype=U8, device=DEV)
+    dsg.fp8ds_rmsnorm_bwd(dy, h, r, gamma, dx, dg, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(dg, (dy.float() * (h.float() * 0.5))[0])
