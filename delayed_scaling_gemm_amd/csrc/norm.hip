@@ -11,7 +11,8 @@
 // and from the fp32 y, without a rounding to 16 bits in between, the operand of the
 // next product: FP8 with a given (delayed) per-tensor scale, FP8 with a scale per
 // row, or blocks of 32 with E8M0 scales (FP8 or FP4 elements).  Sums are fp32: each
-// lane adds at most 64 squares in order, lanes are joined as a tree.
+// lane adds at most 32 squares in order, lanes are joined as a tree.  Rows longer than the
+// registers hold are added in 64 bits by a lane, joined in fp32.
 // Backward, with xhat = h r and g = dy gamma:
 //   dx = r (g - xhat sum(g xhat) / C) + dres,   dgamma = sum over rows of dy xhat
 // (d r / d h_j = -r^3 h_j / C gives the middle term; dres is the gradient that
@@ -448,13 +449,13 @@ __global__ __launch_bounds__(1024) void norm_fwd_long_kernel(NormArgs p, int64_t
     }
     return v;
   };
-  float ss = 0.0f;
+  double mine = 0.0;  // cols / 1024 squares, too many for fp32 beyond 65536 columns
   for (int64_t c = t; c < C; c += 1024) {
     const float v = fresh(c);
-    ss += v * v;
+    mine = fma((double)v, (double)v, mine);
     if (p.h) store1<HBF>(p.h, oh + c, v);
   }
-  ss = row_sum<1024>(ss, reinterpret_cast<float*>(red));
+  const float ss = row_sum<1024>((float)mine, reinterpret_cast<float*>(red));
   const float rstd = norm_rstd(ss, C, p.eps);
   if (p.rstd && t == 0) p.rstd[row] = rstd;
   auto value = [&](int64_t c) {
@@ -676,14 +677,14 @@ __global__ __launch_bounds__(1024) void norm_bwd_long_kernel(NormBwdArgs p) {
   uint32_t amax = 0, sat = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const float rstd = p.rstd[row];
-    float dot = 0.0f;
+    double dot = 0.0;
     for (int64_t c = t; c < C; c += 1024) {
       const float xh = load1<HBF>(p.h, row * p.ldh + c) * rstd;
       const float dy = load1<XBF>(p.dy, row * p.lddy + c);
-      dot += dy * gamma1(p.gamma, p.gamma_bf16, c) * xh;
+      dot += (double)(dy * gamma1(p.gamma, p.gamma_bf16, c) * xh);
       out[c] = dy * xh + (row == (int64_t)blockIdx.x ? 0.0f : out[c]);
     }
-    const float mean = row_sum<1024>(dot, reinterpret_cast<float*>(red)) / (float)C;
+    const float mean = row_sum<1024>((float)dot, reinterpret_cast<float*>(red)) / (float)C;
     for (int64_t c = t; c < C; c += 1024) {
       const float xh = load1<HBF>(p.h, row * p.ldh + c) * rstd;
       const float g = load1<XBF>(p.dy, row * p.lddy + c) * gamma1(p.gamma, p.gamma_bf16, c);

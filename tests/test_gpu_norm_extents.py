@@ -1,8 +1,10 @@
 """RMSNorm at extents where a grid or a chain of additions would pass its limit.
 
-Tolerances with u = 2^-24: a lane adds at most one square here, lanes are joined by 6 + 16 fp32
-additions, so sums are off by at most 24 u, r by half of that and 3 u for the division, root
-and reciprocal (17 u with 2 to spare), y by 2 u more."""
+Tolerances with u = 2^-24: sums of squares over a row of any length are added in 64 bits by a
+lane and joined by 6 + 16 fp32 additions, so they are off by at most 24 u, r by half of that and
+3 u for the division, root and reciprocal (17 u with 2 to spare), y by 2 u more.  The dot product
+of the backward pass: 3 u in each term, 24 u in the sum, 2 u in the mean, and 5 u in what is made
+of it: 34 u of the absolute terms."""
 
 import pytest
 
@@ -92,3 +94,27 @@ def test_backward_of_a_row_of_2_28_columns():
     dsg.fp8ds_rmsnorm_bwd(dy, h, r, gamma, dx, dg, ws)
     torch.cuda.synchronize()
     assert torch.equal(dg, (dy.float() * (h.float() * 0.5))[0])
+
+
+def test_sums_over_very_long_rows():
+    """Equal elements: rounded one after the other their squares would drift."""
+    rows, cols = 3, 1 << 22
+    x = torch.tensor([1.1, 0.3, 0.007], device=DEV)[:, None].expand(rows, cols).contiguous()
+    gamma, r = torch.ones(cols, device=DEV), torch.empty(rows, device=DEV)
+    y = torch.empty_like(x)
+    dsg.fp8ds_rmsnorm(x, gamma, EPS, y=y, rstd=r)
+    want = 1.0 / torch.sqrt(x.double().square().mean(1) + EPS)
+    torch.cuda.synchronize()
+    assert bool(((r.double() - want).abs() <= 17 * U * want).all())
+    g = torch.Generator(device=DEV).manual_seed(3)
+    dy = 1.0 + 0.1 * rand(g, rows, cols)
+    dx, dg = torch.empty_like(x), torch.empty(cols, device=DEV)
+    ws = torch.empty(dsg.fp8ds_rmsnorm_bwd_workspace(rows, cols), dtype=U8, device=DEV)
+    dsg.fp8ds_rmsnorm_bwd(dy, x, r, gamma, dx, dg, ws)
+    torch.cuda.synchronize()
+    rd = r.double()[:, None]
+    xh = x.double() * rd
+    mean = (dy.double() * xh).mean(1, keepdim=True)
+    ex = rd * (dy.double() - xh * mean)
+    terms = rd * (dy.double().abs() + xh.abs() * (dy.double() * xh).abs().mean(1, keepdim=True))
+    assert bool(((dx.double() - ex).abs() <= 34 * U * terms).all())
