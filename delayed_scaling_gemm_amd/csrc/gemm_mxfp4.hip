@@ -755,10 +755,23 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void gemm_mxfp4_tile_kernel(Mxfp4G
 
 template <int FA, bool EXACT, int MT, int NT, int KW>
 static hipError_t launch_direct(const Mxfp4Gemm& p, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.N + 16 * NT - 1) / (16 * NT)),
-                  (unsigned)((p.M + 16 * MT - 1) / (16 * MT)));
-  hipLaunchKernelGGL((gemm_mxfp4_direct_kernel<FA, EXACT, MT, NT, KW>), grid, dim3(64 * KW), 0, stream, p);
-  return hipGetLastError();
+  // A grid holds fewer than 2^32 threads along x; of a larger one HIP drops the excess without
+  // an error.  2^27 columns are at most 2^27 / 16 workgroups of 512 (KW = 8) threads.
+  constexpr int64_t kSlice = 1 << 27;
+  for (int64_t n0 = 0; n0 < p.N; n0 += kSlice) {
+    Mxfp4Gemm s = p;
+    s.N = p.N - n0 < kSlice ? p.N - n0 : kSlice;
+    s.B = p.B + n0 * (p.ldb / 2);
+    s.sc_b = p.sc_b + n0 * p.ldsb;
+    s.C = static_cast<char*>(p.C) + n0 * (p.out_bf16 ? 2 : 4);
+    const dim3 grid((unsigned)((s.N + 16 * NT - 1) / (16 * NT)),
+                    (unsigned)((s.M + 16 * MT - 1) / (16 * MT)));
+    hipLaunchKernelGGL((gemm_mxfp4_direct_kernel<FA, EXACT, MT, NT, KW>), grid, dim3(64 * KW), 0,
+                       stream, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int FA, bool EXACT, int BM, int BN, int GM, int GN, bool WIDE>
