@@ -1004,7 +1004,8 @@ int fp8ds_cast_mxfp4(const void* x, fp8ds_dtype xt, int64_t rows, int64_t cols, 
   if (rows % 32 != 0)
     return fail(FP8DS_ERR_SHAPE, "%s: a transposed copy needs rows in multiples of 32 (got %lld)",
                 who, (long long)rows);
-  if ((rows + 127) / 128 > 65535 || (cols + 127) / 128 > (int64_t(1) << 31) - 1)
+  // (256 threads a tile; of a grid of 2^32 threads and more HIP drops the excess without an error)
+  if ((rows + 127) / 128 > 65535 || (cols + 127) / 128 >= (int64_t(1) << 24))
     return fail(FP8DS_ERR_SHAPE, "%s: too many tiles for a transposed copy", who);
   return hip_status(fp8ds::launch_mxfp4_cast_transpose(x, xt == FP8DS_BF16, rows, cols, q, scales,
                                                        q_t, scales_t, stream),

@@ -674,7 +674,8 @@ int fp8ds_adamw_clip(float* w, const void* g, fp8ds_dtype gt, float* m, float* v
  *   q          device [rows x cols / 2] bytes, 16-byte aligned: element 2 i in the low half.
  *   scales     device [rows x cols / 32].
  *   q_t, scales_t  device or both NULL: the transpose [cols x rows / 2], [cols x rows / 32],
- *              blocked along its own rows, from the same read; rows a multiple of 32.
+ *              blocked along its own rows, from the same read; rows a multiple of 32, at
+ *              most 128 * 65535, cols at most 2^31 - 128 (FP8DS_ERR_SHAPE otherwise).
  */
 int fp8ds_cast_mxfp4(const void* x, fp8ds_dtype xt, int64_t rows, int64_t cols, uint8_t* q,
                      uint8_t* scales, uint8_t* q_t, uint8_t* scales_t, hipStream_t stream);
