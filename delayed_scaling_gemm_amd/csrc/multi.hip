@@ -215,9 +215,10 @@ __device__ __forceinline__ void clip_quads(const void* g, void* o, int64_t b, in
     put(o, DBF, i, elem(g, SBF, i) * c);
 }
 
-__global__ __launch_bounds__(256) void grad_clip_kernel(TensorTable tb, const float* coef) {
+__global__ __launch_bounds__(256) void grad_clip_kernel(TensorTable tb, const float* coef,
+                                                        uint32_t chunk0) {
   const float c = *coef;
-  const uint32_t chunk = blockIdx.x;
+  const uint32_t chunk = chunk0 + blockIdx.x;
   const int t = find_tensor(tb, chunk);
   const void* g = tb.src[t];
   void* o = tb.dst[t];
@@ -263,9 +264,15 @@ hipError_t launch_grad_norm_join(const double* parts, int n, float grad_scale, f
 
 hipError_t launch_grad_clip(const TensorTable& tb, const float* coef, hipStream_t stream) {
   const uint32_t chunks = tb.start[tb.count];
-  if (chunks == 0) return hipSuccess;
-  hipLaunchKernelGGL(grad_clip_kernel, dim3(chunks), dim3(256), 0, stream, tb, coef);
-  return hipGetLastError();
+  // (a grid holds fewer than 2^32 threads; of a larger one HIP drops the excess without an error)
+  constexpr uint32_t kSlice = 1u << 20;
+  for (uint32_t c0 = 0; c0 < chunks; c0 += kSlice) {
+    hipLaunchKernelGGL(grad_clip_kernel, dim3(chunks - c0 < kSlice ? chunks - c0 : kSlice),
+                       dim3(256), 0, stream, tb, coef, c0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace fp8ds
