@@ -131,7 +131,9 @@ int fp8ds_amax(const void* x, fp8ds_dtype xt, int64_t n, float* amax, hipStream_
  *   x          device, rows*cols elements of `xt`, row-major, contiguous, 16-byte aligned.
  *   rows,cols  >= 0.
  *   fmt        target format.
- *   scale      device, 1 float: the delayed scale of this step (read once).
+ *   scale      device, 1 float: the delayed scale of this step (read once).  Finite and
+ *              not 0, as fp8ds_scale_update makes it: NaN products that another scale
+ *              makes of inputs other than NaN may be coded as +-max.
  *   q          device, rows*cols bytes, row-major, 16-byte aligned.
  *   q_t        device or NULL: if non-NULL also receives the transposed copy,
  *              [cols x rows] row-major (q_t[c*rows + r] == q[r*cols + c]), for GEMM
