@@ -80,35 +80,36 @@ class NormLinearStack(Buffers):
         return (self.scale[i:i + 1], self.scale_used[i:i + 1],
                 self._amax[self.steps & 1, i:i + 1])
 
-    def _h(self, i, tokens, stream):
-        return self._buf(f"h{i}", (tokens, self.width), self.stream_dtype, stream)
+    def _h(self, i, tokens):
+        return self._buf(f"h{i}", (tokens, self.width), self.stream_dtype)
 
     def forward(self, x, stream=None):
         """``x`` [tokens, width] BF16 (or of the stream's type) -> y [tokens, width] BF16."""
         T, C, u8, bf = x.shape[0], self.width, torch.uint8, torch.bfloat16
         if x.dim() != 2 or x.shape[1] != C:
             raise ValueError(f"x is {tuple(x.shape)}, the stack [tokens, {C}]")
-        rstd = self._buf("rstd", (self.layers + 1, T), torch.float32, stream)
+        self._use(stream)
+        rstd = self._buf("rstd", (self.layers + 1, T), torch.float32)
         mma = MMA_FP8 if C >= FP8_FWD_MIN_K else MMA_EXACT
         residual = None
         for i in range(self.layers):
             s, su, am = self._state(X, i)
-            xq = self._buf(f"xq{i}", (T, C), u8, stream)
-            h = self._h(i, T, stream)
+            xq = self._buf(f"xq{i}", (T, C), u8)
+            h = self._h(i, T)
             fp8ds_rmsnorm(x, self.gamma[i], self.eps, residual, h, None, rstd[i], E4M3, s, xq, su,
                           am, stream=stream)
             s, su, am = self._state(W, i)
-            wq = self._buf(f"wq{i}", (C, C), u8, stream)
-            wqt = self._buf(f"wqt{i}", (C, C), u8, stream)
+            wq = self._buf(f"wq{i}", (C, C), u8)
+            wqt = self._buf(f"wqt{i}", (C, C), u8)
             if not self._prepared:
                 fp8ds_cast_acc(self.w[i], E4M3, s, wq, wqt, su, am, stream=stream)
             # free again: the norm has put the last one into h
-            x = self._buf("x", (T, C), bf, stream)
+            x = self._buf("x", (T, C), bf)
             fp8ds_gemm(OP_N, OP_T, T, C, C, xq, E4M3, C, self._state(X, i)[1], wqt, E4M3, C, su, x,
                        C, None, stream, mma=mma)
             residual = h
-        y = self._buf("y", (T, C), bf, stream)
-        fp8ds_rmsnorm(x, self.gamma[-1], self.eps, residual, self._h(self.layers, T, stream), y,
+        y = self._buf("y", (T, C), bf)
+        fp8ds_rmsnorm(x, self.gamma[-1], self.eps, residual, self._h(self.layers, T), y,
                       rstd[-1], stream=stream)
         self._prepared, self._pending = False, True
         return y
@@ -117,31 +118,32 @@ class NormLinearStack(Buffers):
         """``dy`` [tokens, width] (BF16) -> the gradient of x, of the stream's type; the weights'
         are in :meth:`grads`.  Ends the step: the scales move on."""
         T, C, u8, f32 = dy.shape[0], self.width, torch.uint8, torch.float32
-        rstd = self._held("rstd", stream)
+        rstd = self._bufs.get("rstd")
         if not self._pending or tuple(dy.shape) != (rstd.shape[1], C):
             raise RuntimeError("backward() needs a forward() of this shape before it")
-        ws = self._buf("ws", (max(16, fp8ds_rmsnorm_bwd_workspace(T, C)),), u8, stream)
-        dq = self._buf("dq", (T, C), u8, stream)
+        self._use(stream)
+        ws = self._buf("ws", (max(16, fp8ds_rmsnorm_bwd_workspace(T, C)),), u8)
+        dq = self._buf("dq", (T, C), u8)
         dres = None
         for i in range(self.layers, -1, -1):
-            h = self._h(i, T, stream)
+            h = self._h(i, T)
             # in place: the stream's gradient
-            dh = self._buf("dh", (T, C), self.stream_dtype, stream)
+            dh = self._buf("dh", (T, C), self.stream_dtype)
             cast = {}
             if i > 0:  # the operand of the Linear whose output h_i took in
                 s, su, am = self._state(DY, i - 1)
                 cast = dict(fmt=E5M2, scale=s, q=dq, scale_used=su, amax=am)
             fp8ds_rmsnorm_bwd(dy, h, rstd[i], self.gamma[i], dh,
-                              self._buf(f"dg{i}", (C,), f32, stream), ws, dres, stream=stream,
+                              self._buf(f"dg{i}", (C,), f32), ws, dres, stream=stream,
                               **cast)
             if i == 0:
                 break
             j = i - 1
-            dy = self._buf("dx", (T, C), torch.bfloat16, stream)
-            fp8ds_gemm(OP_N, OP_T, T, C, C, dq, E5M2, C, su, self._held(f"wq{j}", stream), E4M3, C,
+            dy = self._buf("dx", (T, C), torch.bfloat16)
+            fp8ds_gemm(OP_N, OP_T, T, C, C, dq, E5M2, C, su, self._bufs[f"wq{j}"], E4M3, C,
                        self._state(W, j)[1], dy, C, None, stream, mma=self.mma_bwd)
-            dw = self._buf(f"dw{j}", (C, C), torch.bfloat16, stream)
-            fp8ds_gemm(OP_T, OP_N, C, C, T, self._held(f"xq{j}", stream), E4M3, C,
+            dw = self._buf(f"dw{j}", (C, C), torch.bfloat16)
+            fp8ds_gemm(OP_T, OP_N, C, C, T, self._bufs[f"xq{j}"], E4M3, C,
                        self._state(X, j)[1], dq, E5M2, C, su, dw, C, None, stream,
                        mma=self.mma_bwd)
             dres = dh
@@ -152,11 +154,10 @@ class NormLinearStack(Buffers):
         self._pending, self._fresh = False, True
         return dh
 
-    def grads(self, stream=None):
-        """The last backward's gradients, for a use on ``stream``: every dW (BF16 [in, out]), then
-        every dgamma (FP32)."""
-        return ([self._held(f"dw{i}", stream) for i in range(self.layers)]
-                + [self._held(f"dg{i}", stream) for i in range(self.layers + 1)])
+    def grads(self):
+        """The last backward's gradients: every dW (BF16 [in, out]), then every dgamma (FP32)."""
+        return ([self._bufs[f"dw{i}"] for i in range(self.layers)]
+                + [self._bufs[f"dg{i}"] for i in range(self.layers + 1)])
 
     def optimizer_step(self, lr, max_norm, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0,
                        grad_scale=1.0, stream=None):
@@ -169,16 +170,17 @@ class NormLinearStack(Buffers):
         if self._pending or not self._fresh:
             raise RuntimeError("optimizer_step() comes once after each backward(), before the next "
                                "forward()")
-        C, u8, g = self.width, torch.uint8, self.grads(stream)
-        ws = self._buf("norm_ws", (fp8ds_grad_norm_workspace(),), u8, stream)
+        self._use(stream)
+        C, u8, g = self.width, torch.uint8, self.grads()
+        ws = self._buf("norm_ws", (fp8ds_grad_norm_workspace(),), u8)
         fp8ds_grad_norm(g, max_norm, self.norm, self.coef, ws, grad_scale, stream)
         for i, p in enumerate(self.w + self.gamma):
             m, v = self.moments[i]
             cast, decay = {}, 0.0
             if i < self.layers:
                 s, su, am = self._state(W, i)
-                cast = dict(fmt=E4M3, scale=s, q=self._buf(f"wq{i}", (C, C), u8, stream),
-                            q_t=self._buf(f"wqt{i}", (C, C), u8, stream), scale_used=su, amax=am)
+                cast = dict(fmt=E4M3, scale=s, q=self._buf(f"wq{i}", (C, C), u8),
+                            q_t=self._buf(f"wqt{i}", (C, C), u8), scale_used=su, amax=am)
                 decay = weight_decay
             fp8ds_adamw(p, g[i], m, v, lr, beta1, beta2, eps, decay, self.steps,
                         grad_scale=grad_scale, grad_amax=self.norm, stream=stream,
@@ -187,13 +189,14 @@ class NormLinearStack(Buffers):
 
     def quantize(self, stream=None):
         """Write the weights' MXFP4 codes for :meth:`decode`."""
+        self._use(stream)
         C, u8 = self.width, torch.uint8
         for i, w in enumerate(self.w):
             # the product reads W^T blocked along in: the cast's transposed copy
-            fp8ds_cast_mxfp4(w, self._buf("m4", (C, C // 2), u8, stream),
-                             self._buf("m4s", (C, C // 32), u8, stream),
-                             self._buf(f"m4t{i}", (C, C // 2), u8, stream),
-                             self._buf(f"m4st{i}", (C, C // 32), u8, stream), stream)
+            fp8ds_cast_mxfp4(w, self._buf("m4", (C, C // 2), u8),
+                             self._buf("m4s", (C, C // 32), u8),
+                             self._buf(f"m4t{i}", (C, C // 2), u8),
+                             self._buf(f"m4st{i}", (C, C // 32), u8), stream)
 
     def decode(self, x, fmt=E4M3, stream=None):
         """:meth:`forward` with the weights of the last :meth:`quantize` and the activations in
@@ -203,16 +206,17 @@ class NormLinearStack(Buffers):
         T, C, u8, bf = x.shape[0], self.width, torch.uint8, torch.bfloat16
         if x.dim() != 2 or x.shape[1] != C:
             raise ValueError(f"x is {tuple(x.shape)}, the stack [tokens, {C}]")
-        q = self._buf("sq", (T, C // 2 if fmt == E2M1 else C), u8, stream)
-        qs = self._buf("sqs", (T, C // 32), u8, stream)
-        h, residual = self._buf("sh", (T, C), self.stream_dtype, stream), None
+        self._use(stream)
+        q = self._buf("sq", (T, C // 2 if fmt == E2M1 else C), u8)
+        qs = self._buf("sqs", (T, C // 32), u8)
+        h, residual = self._buf("sh", (T, C), self.stream_dtype), None
         for i in range(self.layers):
             fp8ds_rmsnorm_mx(x, self.gamma[i], self.eps, fmt, q, qs, residual, h, stream=stream)
-            x = self._buf("sx", (T, C), bf, stream)
-            fp8ds_gemm_mxfp4(T, C, C, q, fmt, C, qs, C // 32, self._held(f"m4t{i}", stream),
-                             C, self._held(f"m4st{i}", stream), C // 32, x, C, None, stream,
+            x = self._buf("sx", (T, C), bf)
+            fp8ds_gemm_mxfp4(T, C, C, q, fmt, C, qs, C // 32, self._bufs[f"m4t{i}"],
+                             C, self._bufs[f"m4st{i}"], C // 32, x, C, None, stream,
                              self.mma_decode)
             residual = h  # in place from here on
-        y = self._buf("sy", (T, C), bf, stream)
+        y = self._buf("sy", (T, C), bf)
         fp8ds_rmsnorm(x, self.gamma[-1], self.eps, residual, None, y, stream=stream)
         return y

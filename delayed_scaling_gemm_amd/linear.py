@@ -199,11 +199,12 @@ class DelayedScalingLinear(Buffers):
         M, K = x.shape
         K2, N = w.shape
         assert K == K2, "x is [M, in] and w is [in, out]"
+        self._use(stream)
         u8 = torch.uint8
-        xq = self._buf("xq", (M, K), u8, stream)
-        wq = self._buf("wq", (K, N), u8, stream)
-        wqt = self._buf("wqt", (N, K), u8, stream)
-        y = self._buf("y", (M, N), torch.bfloat16, stream)
+        xq = self._buf("xq", (M, K), u8)
+        wq = self._buf("wq", (K, N), u8)
+        wqt = self._buf("wqt", (N, K), u8)
+        y = self._buf("y", (M, N), torch.bfloat16)
         slot = self._slot
         s, su, am = self.scale, self.scale_used, self._amax_of(slot)
         amax_y = self._acc[slot, 3:4].view(torch.float32)
@@ -225,9 +226,9 @@ class DelayedScalingLinear(Buffers):
         n_upd = 2
         if dy is not None:
             assert tuple(dy.shape) == (M, N)
-            dyq = self._buf("dyq", (M, N), u8, stream)
-            dx = self._buf("dx", (M, K), torch.bfloat16, stream)
-            dw = self._buf("dw", (K, N), torch.bfloat16, stream)
+            dyq = self._buf("dyq", (M, N), u8)
+            dx = self._buf("dx", (M, K), torch.bfloat16)
+            dw = self._buf("dw", (K, N), torch.bfloat16)
             self._cast(DY, dy, dyq, None, stream)
             # dX[M, K] = dYq[M, N] . Wq^T   (Wq stored [K, N] = [N' x K'] -> op T)
             fp8ds_gemm(OP_N, OP_T, M, K, N, dyq, self.fmts[DY], N, su[DY:DY + 1], wq, self.fmts[W],
@@ -261,14 +262,15 @@ class DelayedScalingLinear(Buffers):
         ``grad_coef`` (device scalar of :func:`fp8ds_grad_norm`) clips the gradient;
         with ``grad_norm``, the norm of the same call, it is that norm's finiteness and
         not this dW's that decides, so that one bad tensor skips every layer's step."""
-        dw = self._held("dw", stream)
+        dw = self._bufs.get("dw")
         if dw is None or tuple(dw.shape) != tuple(w.shape):
             raise RuntimeError("adamw_step needs the dW of a preceding fwd+bwd step of this shape")
         if w.dtype != torch.float32:
             raise TypeError("the master weights must be fp32")
+        self._use(stream)
         K, N = w.shape
-        wq = self._buf("wq", (K, N), torch.uint8, stream)
-        wqt = self._buf("wqt", (N, K), torch.uint8, stream)
+        wq = self._buf("wq", (K, N), torch.uint8)
+        wqt = self._buf("wqt", (N, K), torch.uint8)
         # the new weights' amax and saturation go into the next step's set
         s, su = self.scale, self.scale_used
         am, sat = self._amax_of(self._slot), self._sat_of(self._slot)
@@ -331,9 +333,10 @@ class BatchedDelayedScalingLinear(Buffers):
         B, M, K = x.shape
         B2, K2, N = w.shape
         assert B == B2 == self.batch and K == K2
-        xq = self._buf("xq", (B, M, K), torch.uint8, stream)
-        wq = self._buf("wq", (B, K, N), torch.uint8, stream)
-        y = self._buf("y", (B, M, N), torch.bfloat16, stream)
+        self._use(stream)
+        xq = self._buf("xq", (B, M, K), torch.uint8)
+        wq = self._buf("wq", (B, K, N), torch.uint8)
+        y = self._buf("y", (B, M, N), torch.bfloat16)
         s, su, am, sat = self.scale, self.scale_used, self.amax, self.sat
         if self.takes_fused(x, w):
             fp8ds_linear_batched(x, w, self.fmt, self.fmt, self.history, self.cursor, self.algo,
@@ -372,10 +375,10 @@ class MXLinear(Buffers):
     def _cast(self, t, name, x, stream):
         r, c = x.shape
         u8 = torch.uint8
-        q = self._buf(name + "q", (r, c), u8, stream)
-        s = self._buf(name + "s", (r, c // 32), u8, stream)
-        qt = self._buf(name + "qt", (c, r), u8, stream)
-        st = self._buf(name + "st", (c, r // 32), u8, stream)
+        q = self._buf(name + "q", (r, c), u8)
+        s = self._buf(name + "s", (r, c // 32), u8)
+        qt = self._buf(name + "qt", (c, r), u8)
+        st = self._buf(name + "st", (c, r // 32), u8)
         fp8ds_cast_mx(x, self.fmts[t], q, s, qt, st, stream)
         return q, s, qt, st
 
@@ -389,15 +392,16 @@ class MXLinear(Buffers):
         M, K = x.shape
         N = w.shape[1]
         bf = torch.bfloat16
+        self._use(stream)
         xq, xs, xqt, xst = self._cast(X, "x", x, stream)
         wq, ws, wqt, wst = self._cast(W, "w", w, stream)
-        y = self._buf("y", (M, N), bf, stream)
+        y = self._buf("y", (M, N), bf)
         self._gemm(M, N, K, xq, xs, self.fmts[X], wqt, wst, self.fmts[W], y, stream, self.amax_y)
         out = {"y": y, "xq": xq, "xs": xs, "xqt": xqt, "xst": xst, "wq": wq, "ws": ws,
                "wqt": wqt, "wst": wst}
         if dy is not None:
             dyq, dys, dyqt, dyst = self._cast(DY, "dy", dy, stream)
-            dx, dw = self._buf("dx", (M, K), bf, stream), self._buf("dw", (K, N), bf, stream)
+            dx, dw = self._buf("dx", (M, K), bf), self._buf("dw", (K, N), bf)
             self._gemm(M, K, N, dyq, dys, self.fmts[DY], wq, ws, self.fmts[W], dx, stream)
             self._gemm(K, N, M, xqt, xst, self.fmts[X], dyqt, dyst, self.fmts[DY], dw, stream)
             out.update(dx=dx, dw=dw, dyq=dyq, dys=dys, dyqt=dyqt, dyst=dyst)
@@ -427,10 +431,10 @@ class MXFP4Linear(Buffers):
     def _cast(self, name, x, stream):
         r, c = x.shape
         u8 = torch.uint8
-        q = self._buf(name + "q", (r, c // 2), u8, stream)
-        s = self._buf(name + "s", (r, c // 32), u8, stream)
-        qt = self._buf(name + "qt", (c, r // 2), u8, stream)
-        st = self._buf(name + "st", (c, r // 32), u8, stream)
+        q = self._buf(name + "q", (r, c // 2), u8)
+        s = self._buf(name + "s", (r, c // 32), u8)
+        qt = self._buf(name + "qt", (c, r // 2), u8)
+        st = self._buf(name + "st", (c, r // 32), u8)
         fp8ds_cast_mxfp4(x, q, s, qt, st, stream)
         return q, s, qt, st
 
@@ -441,42 +445,44 @@ class MXFP4Linear(Buffers):
 
     def quantize(self, w, stream=None):
         """Keep the MXFP4 codes of ``w`` [in, out] for :meth:`forward`."""
+        self._use(stream)
         self._cast("w", w, stream)
         self.shape = tuple(w.shape)
 
     def forward(self, x, fmt=E2M1, stream=None):
         """y [tokens, out] BF16 of ``x`` [tokens, in] with the weights of :meth:`quantize`
         (of the last :meth:`step` where that came later)."""
-        wqt, wst = self._held("wqt", stream), self._held("wst", stream)
-        if wqt is None:
+        if "wqt" not in self._bufs:
             raise RuntimeError("forward() needs the weights of a preceding quantize()")
         K, N = self.shape
         M = x.shape[0]
         if x.shape[1] != K:
             raise ValueError(f"x has {x.shape[1]} features, the weights {K}")
-        xq = self._buf("fq", (M, K // 2 if fmt == E2M1 else K), torch.uint8, stream)
-        xs = self._buf("fs", (M, K // 32), torch.uint8, stream)
+        self._use(stream)
+        xq = self._buf("fq", (M, K // 2 if fmt == E2M1 else K), torch.uint8)
+        xs = self._buf("fs", (M, K // 32), torch.uint8)
         if fmt == E2M1:
             fp8ds_cast_mxfp4(x, xq, xs, stream=stream)
         else:
             fp8ds_cast_mx(x, fmt, xq, xs, stream=stream)
-        return self._gemm(M, N, K, xq, xs, fmt, wqt, wst,
-                          self._buf("fy", (M, N), torch.bfloat16, stream), stream)
+        return self._gemm(M, N, K, xq, xs, fmt, self._bufs["wqt"], self._bufs["wst"],
+                          self._buf("fy", (M, N), torch.bfloat16), stream)
 
     def step(self, x, w, dy=None, stream=None):
         """x [M, K], w [K, N] (and dy [M, N]), BF16 or FP32 on the device.  Returns the BF16
         outputs y (and dx, dw) and the MXFP4 copies of the inputs."""
         (M, K), N = x.shape, w.shape[1]
         bf = torch.bfloat16
+        self._use(stream)
         xq, xs, xqt, xst = self._cast("x", x, stream)
         wq, ws, wqt, wst = self._cast("w", w, stream)
         self.shape = (K, N)
-        y = self._gemm(M, N, K, xq, xs, E2M1, wqt, wst, self._buf("y", (M, N), bf, stream), stream)
+        y = self._gemm(M, N, K, xq, xs, E2M1, wqt, wst, self._buf("y", (M, N), bf), stream)
         out = {"y": y, "xq": xq, "xs": xs, "xqt": xqt, "xst": xst, "wq": wq, "ws": ws,
                "wqt": wqt, "wst": wst}
         if dy is not None:
             dyq, dys, dyqt, dyst = self._cast("dy", dy, stream)
-            dx, dw = self._buf("dx", (M, K), bf, stream), self._buf("dw", (K, N), bf, stream)
+            dx, dw = self._buf("dx", (M, K), bf), self._buf("dw", (K, N), bf)
             self._gemm(M, K, N, dyq, dys, E2M1, wq, ws, dx, stream)
             self._gemm(K, N, M, xqt, xst, E2M1, dyqt, dyst, dw, stream)
             out.update(dx=dx, dw=dw, dyq=dyq, dys=dys, dyqt=dyqt, dyst=dyst)
