@@ -20,7 +20,8 @@ MXFP4, fp8ds_rmsnorm_mx writes the activations in blocks of 32 (E2M1, E4M3 or E5
 fp8ds_gemm_mxfp4 multiplies them.  No calibration, any number of tokens.
 
 Weights are stored [in, out].  Everything stays on one stream, without a host
-synchronisation.
+synchronisation.  A decode can be captured into a graph; the training calls alternate amax sets
+and count steps on the host, so a graph of one would repeat that step's.
 """
 
 from __future__ import annotations
@@ -103,8 +104,7 @@ class NormLinearStack(Buffers):
             wqt = self._buf(f"wqt{i}", (C, C), u8)
             if not self._prepared:
                 fp8ds_cast_acc(self.w[i], E4M3, s, wq, wqt, su, am, stream=stream)
-            # free again: the norm has put the last one into h
-            x = self._buf("x", (T, C), bf)
+            x = self._buf("x", (T, C), bf)  # free again: the norm has put the last one into h
             fp8ds_gemm(OP_N, OP_T, T, C, C, xq, E4M3, C, self._state(X, i)[1], wqt, E4M3, C, su, x,
                        C, None, stream, mma=mma)
             residual = h
@@ -127,15 +127,13 @@ class NormLinearStack(Buffers):
         dres = None
         for i in range(self.layers, -1, -1):
             h = self._h(i, T)
-            # in place: the stream's gradient
-            dh = self._buf("dh", (T, C), self.stream_dtype)
+            dh = self._buf("dh", (T, C), self.stream_dtype)  # in place: the stream's gradient
             cast = {}
             if i > 0:  # the operand of the Linear whose output h_i took in
                 s, su, am = self._state(DY, i - 1)
                 cast = dict(fmt=E5M2, scale=s, q=dq, scale_used=su, amax=am)
-            fp8ds_rmsnorm_bwd(dy, h, rstd[i], self.gamma[i], dh,
-                              self._buf(f"dg{i}", (C,), f32), ws, dres, stream=stream,
-                              **cast)
+            fp8ds_rmsnorm_bwd(dy, h, rstd[i], self.gamma[i], dh, self._buf(f"dg{i}", (C,), f32), ws,
+                              dres, stream=stream, **cast)
             if i == 0:
                 break
             j = i - 1

@@ -122,8 +122,8 @@ struct RowPtr {
 // rows the product is the reading of B, (1/2 + 1/32) byte per weight.  Measured: 1 token x
 // 14336 x 4096 8.4 us, 3.7 TB/s of B; with B from HBM each time and an FP8 A 10.6 us on the
 // FP8 datapath and 11.5 on the exact one, whose conversions (8 to 16 for one to four matrix
-// instructions) come on top.  What is over the copy's 6.1 us is the launch, the first loads' latency and
-// the join: with 4 waves a K of 4096 is two spans for each.
+// instructions) come on top.  What is over the copy's 6.1 us is the launch, the first loads'
+// latency and the join: with 4 waves a K of 4096 is two spans for each.
 template <int FA, bool EXACT, int MT, int NT, int KW>
 __global__ __launch_bounds__(64 * KW) void gemm_mxfp4_direct_kernel(Mxfp4Gemm p) {
   constexpr int BM = 16 * MT, BN = 16 * NT;
@@ -241,13 +241,16 @@ __global__ __launch_bounds__(64 * KW) void gemm_mxfp4_direct_kernel(Mxfp4Gemm p)
 // 4096 x 4096 x 16384.  Two buffers for FP8 x FP4: 416 us instead of 395 at
 // 8192 x 14336 x 4096.
 //
-// Measured with random codes (FP4 x FP4, M x N x K): 4096 x 4096 x 16384 130 us = 4.2 PFLOP/s,
-// 8192 x 14336 x 4096 254 us = 3.8, 16384 x 4096 x 4096 168 us = 3.3; FP8 x FP4
-// 8192 x 14336 x 4096 359 us = 2.7 on the FP8 datapath, 692 us = 1.4 on the exact one, whose
+// Measured with random codes (FP4 x FP4, M x N x K): 4096 x 4096 x 16384 123 us = 4.5 PFLOP/s,
+// 8192 x 14336 x 4096 239 us = 4.0, 16384 x 4096 x 4096 143 us = 3.8; FP8 x FP4
+// 8192 x 14336 x 4096 348 us = 2.8 on the FP8 datapath, 675 us = 1.4 on the exact one, whose
 // BF16 instructions have half the FP8 rate and share their issue with 24 conversions for 8 of
-// them.  The instruction alone, fed from registers with random
-// codes, reaches 6.6 (4.2 for FP8 x FP8): the chip lowers its clock under it.  The matrix
-// unit is busy 65, 56 and 47% of the time.  What holds it up: LDS, of whose time a step of
+// them.  These are times in a loop that has run for some 200 launches; before that power
+// control lowers the clock for a while, and the same calls take up to a fifth longer.  The
+// comparisons in this file are of loops of 24 to 60 launches, both sides alike.  The instruction
+// alone, fed from registers with random codes, reaches 6.6 (4.2 for FP8 x FP8).  The matrix
+// unit is busy 65, 47 and 56% of the time (4096 x 4096 x 16384, 16384 x 4096 x 4096,
+// 8192 x 14336 x 4096).  What holds it up: LDS, of whose time a step of
 // MFMAs (512 cycles of a SIMD) takes 384 for fragment reads and 128 for the next stage's
 // arrival; and at K = 4096 the start and end of each tile, 5 to 9 us a round of tiles, of
 // which the stores of C are 1.5 to 3.5.  Waves of 128 x 128 outputs (4 a workgroup) read

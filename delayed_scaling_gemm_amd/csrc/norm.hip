@@ -30,8 +30,12 @@
 // of 7 B per element (a copy of 1 GiB runs at 5.1); backward with FP8 output 119 us, 5.1 TB/s
 // of 9 B, and 6.6 us for the join of dgamma's partials.  Traffic is the algorithm's within
 // 1% (backward 3%, the partials).  1531 x 1023 with an FP32 stream and a scale per row, whose rows
-// start at odd addresses: 9.0 us, 1.9 TB/s, two rounds of latency.  One row of 4096: 3.5 us,
-// the launch and a chain of two loads, a reduction and a store.
+// start at odd addresses: 8.4 us, 2.1 TB/s, one round of 383 workgroups and so one chain of
+// load, two reductions and store.  At 1024 columns that is 5.7 us; unaligned rows cost 0.6,
+// and the last 7 elements 2.0: they are loaded one by one, after the rest and after one another
+// for x, the residual and gamma (the backward pass does so for its four operands), and
+// stored so too.  One row of 4096: 3.5 us, the launch and a chain of two loads, a reduction
+// and a store.
 
 #include <type_traits>
 
