@@ -113,27 +113,36 @@ __global__ void current_scale_kernel(const float* __restrict__ amax, float fmax,
 
 // ------------------------------------------------------------------ host launchers
 
+template <bool BF16, int FMT>
+static hipError_t launch_rowwise_t(const void* x, int64_t rows, int64_t cols, int margin, uint8_t* q,
+                                   float* scale, float* scale_inv, float* amax,
+                                   hipStream_t stream) {
+  // a grid holds fewer than 2^32 threads; of a larger one HIP drops a part without an error
+  constexpr int64_t kSlice = 1 << 23;
+  for (int64_t r = 0; r < rows; r += kSlice) {
+    const int64_t n = rows - r < kSlice ? rows - r : kSlice;
+    hipLaunchKernelGGL((rowwise_cast_kernel<BF16, FMT>), dim3((unsigned)n), dim3(256), 0, stream,
+                       static_cast<const char*>(x) + r * cols * (BF16 ? 2 : 4), cols, margin,
+                       q + r * cols, scale + r, scale_inv ? scale_inv + r : nullptr,
+                       amax ? amax + r : nullptr);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 hipError_t launch_rowwise_cast(const void* x, bool bf16, int64_t rows, int64_t cols, int fmt,
                                int margin, uint8_t* q, float* scale, float* scale_inv,
                                float* amax, hipStream_t stream) {
-  if (rows <= 0) return hipSuccess;
-  const dim3 grid((unsigned)rows);
-  if (bf16) {
-    if (fmt == kE4M3)
-      hipLaunchKernelGGL((rowwise_cast_kernel<true, kE4M3>), grid, dim3(256), 0, stream, x, cols,
-                         margin, q, scale, scale_inv, amax);
-    else
-      hipLaunchKernelGGL((rowwise_cast_kernel<true, kE5M2>), grid, dim3(256), 0, stream, x, cols,
-                         margin, q, scale, scale_inv, amax);
-  } else {
-    if (fmt == kE4M3)
-      hipLaunchKernelGGL((rowwise_cast_kernel<false, kE4M3>), grid, dim3(256), 0, stream, x, cols,
-                         margin, q, scale, scale_inv, amax);
-    else
-      hipLaunchKernelGGL((rowwise_cast_kernel<false, kE5M2>), grid, dim3(256), 0, stream, x, cols,
-                         margin, q, scale, scale_inv, amax);
-  }
-  return hipGetLastError();
+  if (bf16)
+    return fmt == kE4M3 ? launch_rowwise_t<true, kE4M3>(x, rows, cols, margin, q, scale, scale_inv,
+                                                        amax, stream)
+                        : launch_rowwise_t<true, kE5M2>(x, rows, cols, margin, q, scale, scale_inv,
+                                                        amax, stream);
+  return fmt == kE4M3 ? launch_rowwise_t<false, kE4M3>(x, rows, cols, margin, q, scale, scale_inv,
+                                                       amax, stream)
+                      : launch_rowwise_t<false, kE5M2>(x, rows, cols, margin, q, scale, scale_inv,
+                                                       amax, stream);
 }
 
 hipError_t launch_current_scale(const float* amax, int fmt, int margin, float* scale,
