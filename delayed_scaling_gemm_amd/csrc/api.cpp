@@ -59,6 +59,11 @@ int num_cus() {
 bool valid_fmt(int f) { return f == FP8DS_E4M3 || f == FP8DS_E5M2; }
 bool valid_mx_fmt(int f) { return valid_fmt(f) || f == FP8DS_E2M1; }
 bool valid_dtype(int t) { return t == FP8DS_F32 || t == FP8DS_BF16; }
+// A transposing cast's tiles of 128 x 128, of 256 threads each, columns along x: of a grid of 2^32
+// threads and more HIP drops a part without an error.
+bool too_many_tiles(int64_t rows, int64_t cols) {
+  return (rows + 127) / 128 > 65535 || (cols + 127) / 128 >= (int64_t(1) << 24);
+}
 
 }  // namespace
 
@@ -113,9 +118,9 @@ static int cast_common(const char* who, const void* x, fp8ds_dtype xt, int64_t r
     if (!aligned16(x) || !aligned16(q) || (q_t && !aligned16(q_t)))
       return fail(FP8DS_ERR_ALIGN, "%s: x, q and q_t must be 16-byte aligned", who);
   }
-  if (q_t && (rows + 127) / 128 > 65535)
-    return fail(FP8DS_ERR_SHAPE, "%s: a transposed copy supports at most %d rows", who,
-                65535 * 128);
+  if (q_t && too_many_tiles(rows, cols))
+    return fail(FP8DS_ERR_SHAPE, "%s: a transposed copy supports at most %d rows and 2^31 - 128 "
+                "columns", who, 65535 * 128);
   hipError_t e = hipSuccess;
   if (!acc)  // with health counts, sat_count is counts[0] and the four others follow it
     e = fp8ds::launch_prologue(1, scale, scale_used, amax, sat_count, stream,
@@ -432,9 +437,9 @@ static int adamw_common(const char* who, float* w, const void* g, fp8ds_dtype gt
         (q_t && !aligned16(q_t)))
       return fail(FP8DS_ERR_ALIGN, "%s: w, g, m, v, q and q_t must be 16-byte aligned", who);
   }
-  if (q_t && (rows + 127) / 128 > 65535)
-    return fail(FP8DS_ERR_SHAPE, "%s: a transposed copy supports at most %d rows", who,
-                65535 * 128);
+  if (q_t && too_many_tiles(rows, cols))
+    return fail(FP8DS_ERR_SHAPE, "%s: a transposed copy supports at most %d rows and 2^31 - 128 "
+                "columns", who, 65535 * 128);
   // Per-step constants: float64 from the fp32 hyperparameters, one rounding to fp32.
   const double lr_d = lr, wd_d = weight_decay, b1 = beta1, b2 = beta2;
   fp8ds::AdamWConsts c;
@@ -525,9 +530,9 @@ int fp8ds_cast_current(const void* x, fp8ds_dtype xt, int64_t rows, int64_t cols
     if (!aligned16(x) || !aligned16(q) || (q_t && !aligned16(q_t)))
       return fail(FP8DS_ERR_ALIGN, "%s: x, q and q_t must be 16-byte aligned", who);
   }
-  if (q_t && (rows + 127) / 128 > 65535)
-    return fail(FP8DS_ERR_SHAPE, "%s: a transposed copy supports at most %d rows", who,
-                65535 * 128);
+  if (q_t && too_many_tiles(rows, cols))
+    return fail(FP8DS_ERR_SHAPE, "%s: a transposed copy supports at most %d rows and 2^31 - 128 "
+                "columns", who, 65535 * 128);
   // amax pass, scale from it, then the cast with that scale
   hipError_t e = fp8ds::launch_prologue(1, nullptr, nullptr, amax, sat_count, stream);
   if (e == hipSuccess && n > 0)
@@ -1004,8 +1009,7 @@ int fp8ds_cast_mxfp4(const void* x, fp8ds_dtype xt, int64_t rows, int64_t cols, 
   if (rows % 32 != 0)
     return fail(FP8DS_ERR_SHAPE, "%s: a transposed copy needs rows in multiples of 32 (got %lld)",
                 who, (long long)rows);
-  // (256 threads a tile; of a grid of 2^32 threads and more HIP drops the excess without an error)
-  if ((rows + 127) / 128 > 65535 || (cols + 127) / 128 >= (int64_t(1) << 24))
+  if (too_many_tiles(rows, cols))
     return fail(FP8DS_ERR_SHAPE, "%s: too many tiles for a transposed copy", who);
   return hip_status(fp8ds::launch_mxfp4_cast_transpose(x, xt == FP8DS_BF16, rows, cols, q, scales,
                                                        q_t, scales_t, stream),

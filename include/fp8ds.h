@@ -138,7 +138,7 @@ int fp8ds_amax(const void* x, fp8ds_dtype xt, int64_t n, float* amax, hipStream_
  *   q_t        device or NULL: if non-NULL also receives the transposed copy,
  *              [cols x rows] row-major (q_t[c*rows + r] == q[r*cols + c]), for GEMM
  *              operands the caller wants K-contiguous.  16-byte aligned; rows at
- *              most 65535 * 128 (else FP8DS_ERR_SHAPE).
+ *              most 65535 * 128, cols at most 2^31 - 128 (else FP8DS_ERR_SHAPE).
  *   scale_used device or NULL: receives a copy of *scale -- the snapshot the FP8
  *              bytes were made with.  GEMMs must be given this snapshot, because
  *              fp8ds_scale_update overwrites *scale for the next step.
@@ -394,7 +394,7 @@ int fp8ds_linear_batched(int64_t batch, int64_t M, int64_t N, int64_t K, fp8ds_d
  *   q          device, rows*cols bytes (required with scale when rows*cols > 0): the
  *              FP8 copy of the new weights.
  *   q_t        device or NULL: the transposed copy [cols x rows]; rows at most
- *              65535 * 128.
+ *              65535 * 128 (cols at most 2^31 - 128).
  *   scale_used, amax, sat_count  device or NULL: as fp8ds_cast (written also when
  *              rows*cols == 0).
  * Out-of-range scalars return FP8DS_ERR_VALUE.
