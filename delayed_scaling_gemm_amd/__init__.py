@@ -28,6 +28,7 @@ F32, BF16 = 0, 1
 ALGO_MAX, ALGO_MOST_RECENT = 0, 1
 OP_N, OP_T = 0, 1
 MMA_EXACT, MMA_FP8 = 0, 1
+ACT_SILU, ACT_GELU = 0, 1
 
 FMT_MAX = {E4M3: 448.0, E5M2: 57344.0}
 
@@ -126,6 +127,27 @@ def _declare(lib):
     lib.fp8ds_gemm_mxfp4.argtypes = gemm4 + [vp]
     lib.fp8ds_gemm_mxfp4_mma.restype = i32
     lib.fp8ds_gemm_mxfp4_mma.argtypes = gemm4 + [i32, vp]
+    gated = [i64, i64, i64, vp, i32, i64, vp, vp, i32, i64, vp, i32, vp, i64, vp, i32, i64, i32, vp,
+             vp, i64, vp, vp, vp, i32, vp]
+    lib.fp8ds_gated_gemm.restype = i32
+    lib.fp8ds_gated_gemm.argtypes = gated
+    lib.fp8ds_gated_gemm_bwd.restype = i32
+    lib.fp8ds_gated_gemm_bwd.argtypes = gated
+    around = [vp, i32, i64, vp, i32, f, vp, i32, vp, f, vp, i64, i32, vp, i32, i64, i64, f, vp, i64, vp,
+              i32, i64, vp, vp, i32]
+    lib.fp8ds_rmsnorm_sandwich.restype = i32
+    lib.fp8ds_rmsnorm_sandwich.argtypes = around + [vp, vp, i64, vp, vp, vp, vp]
+    lib.fp8ds_rmsnorm_sandwich_rowwise.restype = i32
+    lib.fp8ds_rmsnorm_sandwich_rowwise.argtypes = around + [i32, vp, i64, vp, vp, vp, vp]
+    lib.fp8ds_rmsnorm_sandwich_mx.restype = i32
+    lib.fp8ds_rmsnorm_sandwich_mx.argtypes = around + [vp, i64, vp, i64, vp]
+    lib.fp8ds_rmsnorm_sandwich_bwd_workspace.restype = i64
+    lib.fp8ds_rmsnorm_sandwich_bwd_workspace.argtypes = [i64, i64]
+    lib.fp8ds_rmsnorm_sandwich_bwd.restype = i32
+    lib.fp8ds_rmsnorm_sandwich_bwd.argtypes = [vp, i32, i64, vp, i32, i64, vp, vp, i32, vp, i64, vp,
+                                               vp, i32, vp, i32, vp, f, vp, i64, i64, i64, vp, i64,
+                                               vp, i64, vp, vp, vp, vp, vp, i64, i32, vp, vp, i64,
+                                               vp, vp, vp, vp]
     return lib
 
 
@@ -899,6 +921,171 @@ def fp8ds_gemm_mxfp4(M, N, K, a, fa, lda, scales_a, ld_scales_a, b, ldb, scales_
         _call("fp8ds_gemm_mxfp4", *args, _stream(stream))
     else:
         _call("fp8ds_gemm_mxfp4_mma", *args, mma, _stream(stream))
+
+
+def _gated(name, x, fx, scale_x, w, fw, scale_w, act, gu, y, yname, halves, fmt, scale, q, scale_used,
+           amax, sat_count, stream, mma):
+    import torch
+
+    u8, f32, high = (torch.uint8,), (torch.float32,), _high()
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError(f"operands of shapes {tuple(x.shape)} and {tuple(w.shape)}: both 2-D, "
+                         "contracted over their columns")
+    M, K = x.shape
+    F, odd = divmod(w.shape[0], 3 - halves)  # the forward's weights hold gate and up
+    if odd:
+        raise ValueError(f"w: {w.shape[0]} rows, expected the gate's and the up projection's")
+    xp, ldx = _rows2d(x, "x", u8, M, K)
+    wp, ldw = _rows2d(w, "w", u8, w.shape[0], K)
+    gp, ldg = (None, 2 * F) if gu is None else _rows2d(gu, "gu", (torch.bfloat16,), M, 2 * F)
+    yp, ldy, yt = None, halves * F, BF16
+    if y is not None:
+        yp, ldy = _rows2d(y, yname, high, M, halves * F)
+        yt = high[y.dtype]
+    qp, ldq = (None, halves * F) if q is None else _rows2d(q, "q", u8, M, halves * F)
+    if w.shape[0] == 1:
+        ldw = (K + 15) // 16 * 16  # one row has no distance to the next
+    _call(name, M, F, K, xp, fx, ldx, _vec(scale_x, "scale_x", f32, 1), wp, fw, ldw,
+          _vec(scale_w, "scale_w", f32, 1), act, gp, ldg, yp, yt, ldy, fmt,
+          _vec(scale, "scale", f32, 1), qp, ldq, _vec(scale_used, "scale_used", f32, 1),
+          _vec(amax, "amax", f32, 1), _vec(sat_count, "sat_count", (torch.int64,), 1), mma,
+          _stream(stream))
+
+
+def fp8ds_gated_gemm(x, fx, scale_x, w, fw, scale_w, act, gu=None, y=None, fmt=E4M3, scale=None, q=None,
+                     scale_used=None, amax=None, sat_count=None, stream=None, mma=MMA_EXACT):
+    """Gate and up products of a feed-forward block with the activation: a = act(g) u from the FP8
+    codes ``x`` [M, K] and ``w`` [2F, K] (the gate's rows, then the up projection's; rows at 16
+    bytes), into ``y`` [M, F] (bf16 or fp32) and / or, with the per-tensor ``scale``, its FP8 copy
+    ``q``; ``gu`` (bf16 [M, 2F]) keeps g and u for the backward pass.  ``amax`` and ``sat_count``
+    are combined into (as :func:`fp8ds_cast_acc`)."""
+    _gated("fp8ds_gated_gemm", x, fx, scale_x, w, fw, scale_w, act, gu, y, "y", 1, fmt, scale, q,
+           scale_used, amax, sat_count, stream, mma)
+
+
+def fp8ds_gated_gemm_bwd(dy, fdy, scale_dy, w, fw, scale_w, act, gu, dgu=None, fmt=E5M2, scale=None,
+                         q=None, scale_used=None, amax=None, sat_count=None, stream=None,
+                         mma=MMA_EXACT):
+    """Backward of :func:`fp8ds_gated_gemm` through the down projection: from the codes ``dy``
+    [M, H] and ``w`` [F, H] (the down projection as stored) and the kept ``gu``, the gradients of
+    g and u into ``dgu`` [M, 2F] (bf16 or fp32) and / or, with ``scale``, its FP8 copy ``q``."""
+    _gated("fp8ds_gated_gemm_bwd", dy, fdy, scale_dy, w, fw, scale_w, act, gu, dgu, "dgu", 2, fmt,
+           scale, q, scale_used, amax, sat_count, stream, mma)
+
+
+def _sandwich_args(x, post_gamma, post_eps, residual, gamma, eps, h, alpha, gate, row_gate, y, post_rstd,
+                   rstd, fmt):
+    import torch
+
+    high, f32 = _high(), (torch.float32,)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [rows, cols]")
+    rows, cols = x.shape
+    xp, ldx = _rows2d(x, "x", high, rows, cols)
+    rp, ldr = _rows2d(residual, "residual", high, rows, cols)
+    hp, ldh = _rows2d(h, "h", (residual.dtype,), rows, cols)
+    yp, ldy, yt = None, cols, BF16
+    if y is not None:
+        yp, ldy = _rows2d(y, "y", high, rows, cols)
+        yt = high[y.dtype]
+    return rows, cols, (xp, high[x.dtype], ldx, _vec(post_gamma, "post_gamma", high, cols),
+                        high[post_gamma.dtype], float(post_eps), _vec(gate, "gate", high, cols),
+                        F32 if gate is None else high[gate.dtype], _vec(row_gate, "row_gate", f32, rows),
+                        float(alpha), rp, ldr, high[residual.dtype], _vec(gamma, "gamma", high, cols),
+                        high[gamma.dtype], rows, cols, float(eps), hp, ldh, yp, yt, ldy,
+                        _vec(post_rstd, "post_rstd", f32, rows), _vec(rstd, "rstd", f32, rows), fmt)
+
+
+def fp8ds_rmsnorm_sandwich(x, post_gamma, post_eps, residual, gamma, eps, h, alpha=1.0, gate=None,
+                           row_gate=None, y=None, post_rstd=None, rstd=None, fmt=E4M3, scale=None,
+                           q=None, scale_used=None, amax=None, sat_count=None, stream=None):
+    """The norms around a residual addition: ``h`` = ``residual`` + alpha gate row_gate
+    RMSNorm(``x``; post_gamma), then RMSNorm(h; gamma) into ``y`` and / or, with the per-tensor
+    ``scale``, its FP8 copy ``q`` (as :func:`fp8ds_rmsnorm`).  ``gate`` [cols], ``row_gate`` fp32
+    [rows].  Rows may be strided; ``h`` may be ``residual`` itself."""
+    import torch
+
+    rows, cols, args = _sandwich_args(x, post_gamma, post_eps, residual, gamma, eps, h, alpha, gate,
+                                      row_gate, y, post_rstd, rstd, fmt)
+    f32 = (torch.float32,)
+    qp, ldq = (None, cols) if q is None else _rows2d(q, "q", (torch.uint8,), rows, cols)
+    _call("fp8ds_rmsnorm_sandwich", *args, _vec(scale, "scale", f32, 1), qp, ldq,
+          _vec(scale_used, "scale_used", f32, 1), _vec(amax, "amax", f32, 1),
+          _vec(sat_count, "sat_count", (torch.int64,), 1), _stream(stream))
+
+
+def fp8ds_rmsnorm_sandwich_rowwise(x, post_gamma, post_eps, residual, gamma, eps, h, fmt, margin, q,
+                                   scale, scale_inv=None, amax=None, alpha=1.0, gate=None,
+                                   row_gate=None, y=None, post_rstd=None, rstd=None, stream=None):
+    """:func:`fp8ds_rmsnorm_sandwich` with a scale per row (``scale``, ``scale_inv``, ``amax``
+    [rows])."""
+    import torch
+
+    rows, cols, args = _sandwich_args(x, post_gamma, post_eps, residual, gamma, eps, h, alpha, gate,
+                                      row_gate, y, post_rstd, rstd, fmt)
+    f32 = (torch.float32,)
+    qp, ldq = _rows2d(q, "q", (torch.uint8,), rows, cols)
+    _call("fp8ds_rmsnorm_sandwich_rowwise", *args, int(margin), qp, ldq,
+          _vec(scale, "scale", f32, rows), _vec(scale_inv, "scale_inv", f32, rows),
+          _vec(amax, "amax", f32, rows), _stream(stream))
+
+
+def fp8ds_rmsnorm_sandwich_mx(x, post_gamma, post_eps, residual, gamma, eps, h, fmt, q, scales,
+                              alpha=1.0, gate=None, row_gate=None, y=None, post_rstd=None, rstd=None,
+                              stream=None):
+    """:func:`fp8ds_rmsnorm_sandwich` with E8M0 scales of blocks of 32 (``q`` and ``scales`` as
+    :func:`fp8ds_rmsnorm_mx`)."""
+    import torch
+
+    rows, cols, args = _sandwich_args(x, post_gamma, post_eps, residual, gamma, eps, h, alpha, gate,
+                                      row_gate, y, post_rstd, rstd, fmt)
+    u8 = (torch.uint8,)
+    qp, ldq = _rows2d(q, "q", u8, rows, cols // 2 if fmt == E2M1 else cols)
+    sp, lds = _rows2d(scales, "scales", u8, rows, cols // 32)
+    _call("fp8ds_rmsnorm_sandwich_mx", *args, qp, ldq, sp, lds, _stream(stream))
+
+
+def fp8ds_rmsnorm_sandwich_bwd_workspace(rows, cols) -> int:
+    """Bytes of workspace that :func:`fp8ds_rmsnorm_sandwich_bwd` needs for this shape."""
+    n = lib().fp8ds_rmsnorm_sandwich_bwd_workspace(rows, cols)
+    if n < 0:
+        _check(int(n))
+    return n
+
+
+def fp8ds_rmsnorm_sandwich_bwd(dy, h, rstd, gamma, x, post_rstd, post_gamma, dh, dgamma, dpost_gamma,
+                               workspace, alpha=1.0, gate=None, row_gate=None, dgate=None,
+                               drow_gate=None, dres=None, dx=None, fmt=E5M2, scale=None, q=None,
+                               scale_used=None, amax=None, sat_count=None, stream=None):
+    """Backward of :func:`fp8ds_rmsnorm_sandwich` from the stored ``h``, ``rstd``, ``x`` and
+    ``post_rstd``: ``dh`` (``+ dres``), the gradient of residual; that of x into ``dx`` and / or, with
+    ``scale``, its FP8 copy ``q``; the parameters' in fp32 (``dgate`` [cols], ``drow_gate``
+    [rows]).  ``workspace``: uint8, :func:`fp8ds_rmsnorm_sandwich_bwd_workspace` bytes."""
+    import torch
+
+    high, f32 = _high(), (torch.float32,)
+    if h.dim() != 2:
+        raise ValueError("h must be 2-D [rows, cols]")
+    rows, cols = h.shape
+    hp, ldh = _rows2d(h, "h", high, rows, cols)
+    xp, ldx = _rows2d(x, "x", high, rows, cols)
+    yp, lddy = _rows2d(dy, "dy", (x.dtype,), rows, cols)
+    rp, lddr = (None, cols) if dres is None else _rows2d(dres, "dres", (h.dtype,), rows, cols)
+    dhp, lddh = _rows2d(dh, "dh", (h.dtype,), rows, cols)
+    dxp, lddx = (None, cols) if dx is None else _rows2d(dx, "dx", (x.dtype,), rows, cols)
+    qp, ldq = (None, cols) if q is None else _rows2d(q, "q", (torch.uint8,), rows, cols)
+    wp = _vec(workspace, "workspace", (torch.uint8,), 0)
+    _call("fp8ds_rmsnorm_sandwich_bwd", yp, high[x.dtype], lddy, hp, high[h.dtype], ldh,
+          _vec(rstd, "rstd", f32, rows), _vec(gamma, "gamma", high, cols), high[gamma.dtype], xp, ldx,
+          _vec(post_rstd, "post_rstd", f32, rows), _vec(post_gamma, "post_gamma", high, cols),
+          high[post_gamma.dtype], _vec(gate, "gate", high, cols),
+          F32 if gate is None else high[gate.dtype], _vec(row_gate, "row_gate", f32, rows),
+          float(alpha), rp, lddr, rows, cols, dhp, lddh, dxp, lddx,
+          _vec(dgamma, "dgamma", f32, cols), _vec(dpost_gamma, "dpost_gamma", f32, cols),
+          _vec(dgate, "dgate", f32, cols), _vec(drow_gate, "drow_gate", f32, rows), wp,
+          0 if workspace is None else workspace.numel(), fmt, _vec(scale, "scale", f32, 1), qp, ldq,
+          _vec(scale_used, "scale_used", f32, 1), _vec(amax, "amax", f32, 1),
+          _vec(sat_count, "sat_count", (torch.int64,), 1), _stream(stream))
 
 
 def abi_version() -> int:

@@ -1101,4 +1101,299 @@ int fp8ds_gemm_mxfp4_mma(int64_t M, int64_t N, int64_t K, const uint8_t* A, fp8d
                            ldb, scales_b, ld_scales_b, C, ct, ldc, amax_c, mma, stream);
 }
 
+// ------------------------------------------------------------------ gated feed-forward
+
+// `bwd`: gu is read (required) and y, q hold both halves of the gradient.
+static int gated_common(const char* who, bool bwd, int64_t M, int64_t F, int64_t K, const uint8_t* A,
+                        fp8ds_format fa, int64_t lda, const float* scale_a, const uint8_t* B,
+                        fp8ds_format fb, int64_t ldb, const float* scale_b, fp8ds_act act, void* gu,
+                        int64_t ldgu, void* y, fp8ds_dtype yt, int64_t ldy, fp8ds_format fmt,
+                        const float* scale, uint8_t* q, int64_t ldq, float* scale_used, float* amax,
+                        uint64_t* sat_count, fp8ds_mma mma, hipStream_t stream) {
+  if (mma != FP8DS_MMA_EXACT && mma != FP8DS_MMA_FP8)
+    return fail(FP8DS_ERR_ENUM, "%s: bad mma %d", who, (int)mma);
+  if (!valid_fmt(fa) || !valid_fmt(fb) || !valid_fmt(fmt))
+    return fail(FP8DS_ERR_ENUM, "%s: bad format", who);
+  if (act != FP8DS_ACT_SILU && act != FP8DS_ACT_GELU)
+    return fail(FP8DS_ERR_ENUM, "%s: bad activation %d", who, (int)act);
+  if (!valid_dtype(yt)) return fail(FP8DS_ERR_ENUM, "%s: bad output dtype %d", who, (int)yt);
+  if (fb != FP8DS_E4M3 || (!bwd && fa != FP8DS_E4M3))
+    return fail(FP8DS_ERR_UNSUPPORTED, "%s: weights%s are E4M3", who, bwd ? "" : " and X");
+  // (128 x 64 outputs of a workgroup, fewer than 2^32 threads in a grid)
+  if (M < 0 || F < 0 || K < 0 || M >= (int64_t(1) << 31) || F >= (int64_t(1) << 30) ||
+      K >= (int64_t(1) << 31) || ((M + 127) / 128) * ((F + 63) / 64) >= (int64_t(1) << 23))
+    return fail(FP8DS_ERR_SHAPE, "%s: bad M/F/K %lld/%lld/%lld", who, (long long)M, (long long)F,
+                (long long)K);
+  const int64_t wide = bwd ? 2 * F : F, wrows = bwd ? F : 2 * F;
+  if (lda < K || ldb < K || (gu && ldgu < 2 * F) || (y && ldy < wide) || (q && ldq < wide) ||
+      lda > kMaxElems / (M + 1) || ldb > kMaxElems / (wrows + 1) || ldgu > kMaxElems / (M + 1) ||
+      ldy > kMaxElems / (M + 1) || ldq > kMaxElems / (M + 1))
+    return fail(FP8DS_ERR_SHAPE, "%s: bad leading dimension", who);
+  if (!scale != !q) return fail(FP8DS_ERR_NULL, "%s: scale and q go together", who);
+  if (!scale && (scale_used || sat_count))
+    return fail(FP8DS_ERR_NULL, "%s: scale_used and sat_count need a scale", who);
+  if (reinterpret_cast<uintptr_t>(scale_a) % 4 || reinterpret_cast<uintptr_t>(scale_b) % 4 ||
+      reinterpret_cast<uintptr_t>(scale) % 4 || reinterpret_cast<uintptr_t>(scale_used) % 4 ||
+      reinterpret_cast<uintptr_t>(amax) % 4 || reinterpret_cast<uintptr_t>(sat_count) % 8)
+    return fail(FP8DS_ERR_ALIGN, "%s: scalars are not aligned to their type", who);
+  if (M == 0 || F == 0) {
+    if (scale_used)
+      return hip_status(fp8ds::launch_prologue(1, scale, scale_used, nullptr, nullptr, stream), who);
+    return ok();
+  }
+  if (!scale_a || !scale_b || (K > 0 && (!A || !B)))
+    return fail(FP8DS_ERR_NULL, "%s: the operands and their scales are required", who);
+  if (bwd ? !gu : (!gu && !y && !q))
+    return fail(FP8DS_ERR_NULL, bwd ? "%s: gu is required" : "%s: no output", who);
+  if (bwd && !y && !q) return fail(FP8DS_ERR_NULL, "%s: no output", who);
+  if (K > 0 && (!aligned16(A) || !aligned16(B) || (M > 1 && lda % 16) || ldb % 16))
+    return fail(FP8DS_ERR_ALIGN, "%s: the rows of the operands must be 16-byte aligned", who);
+  const int ysz = yt == FP8DS_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(gu) % 2 || reinterpret_cast<uintptr_t>(y) % ysz)
+    return fail(FP8DS_ERR_ALIGN, "%s: gu or the output is not aligned to its elements", who);
+  fp8ds::GatedProblem p = {};
+  p.M = M; p.F = F; p.K = K;
+  p.A = A; p.lda = lda; p.scale_a = scale_a;
+  p.B = B; p.ldb = ldb; p.scale_b = scale_b;
+  p.act = (int)act;
+  p.gu = gu; p.ldgu = ldgu;
+  p.y = y; p.y_bf16 = yt == FP8DS_BF16; p.ldy = ldy;
+  p.fmt = (int)fmt; p.scale = scale; p.q = q; p.ldq = ldq;
+  p.scale_used = scale_used; p.amax = amax; p.sat = sat_count;
+  p.vec = F % 16 == 0 && (!gu || (aligned16(gu) && ldgu % 8 == 0)) &&
+          (!y || (aligned16(y) && ldy * ysz % 16 == 0)) && (!q || (aligned16(q) && ldq % 16 == 0));
+  const bool exact = mma == FP8DS_MMA_EXACT;
+  return hip_status(bwd ? fp8ds::launch_gated_bwd(p, (int)fa, exact, num_cus(), stream)
+                        : fp8ds::launch_gated_fwd(p, exact, num_cus(), stream),
+                    who);
+}
+
+int fp8ds_gated_gemm(int64_t M, int64_t F, int64_t K, const uint8_t* A, fp8ds_format fa, int64_t lda,
+                     const float* scale_a, const uint8_t* B, fp8ds_format fb, int64_t ldb,
+                     const float* scale_b, fp8ds_act act, void* gu, int64_t ldgu, void* y,
+                     fp8ds_dtype yt, int64_t ldy, fp8ds_format fmt, const float* scale, uint8_t* q,
+                     int64_t ldq, float* scale_used, float* amax, uint64_t* sat_count, fp8ds_mma mma,
+                     hipStream_t stream) {
+  return gated_common("fp8ds_gated_gemm", false, M, F, K, A, fa, lda, scale_a, B, fb, ldb, scale_b,
+                      act, gu, ldgu, y, yt, ldy, fmt, scale, q, ldq, scale_used, amax, sat_count, mma,
+                      stream);
+}
+
+int fp8ds_gated_gemm_bwd(int64_t M, int64_t F, int64_t H, const uint8_t* A, fp8ds_format fa,
+                         int64_t lda, const float* scale_a, const uint8_t* B, fp8ds_format fb,
+                         int64_t ldb, const float* scale_b, fp8ds_act act, const void* gu,
+                         int64_t ldgu, void* dgu, fp8ds_dtype dt, int64_t lddgu, fp8ds_format fmt,
+                         const float* scale, uint8_t* q, int64_t ldq, float* scale_used, float* amax,
+                         uint64_t* sat_count, fp8ds_mma mma, hipStream_t stream) {
+  return gated_common("fp8ds_gated_gemm_bwd", true, M, F, H, A, fa, lda, scale_a, B, fb, ldb, scale_b,
+                      act, const_cast<void*>(gu), ldgu, dgu, dt, lddgu, fmt, scale, q, ldq, scale_used,
+                      amax, sat_count, mma, stream);
+}
+
+// ------------------------------------------------------------------ norms around a block
+
+// What the three forward calls share.
+static int sandwich_args(const char* who, fp8ds::SandwichArgs& a, const void* x, fp8ds_dtype xt,
+                         int64_t ldx, const void* post_gamma, fp8ds_dtype pt, float post_eps,
+                         const void* gate, fp8ds_dtype gate_t, const float* row_gate, float alpha,
+                         const void* residual, int64_t ldr, fp8ds_dtype ht, const void* gamma,
+                         fp8ds_dtype gt, int64_t rows, int64_t cols, float eps, void* h, int64_t ldh,
+                         void* y, fp8ds_dtype yt, int64_t ldy, float* post_rstd, float* rstd, uint8_t* q,
+                         int64_t ldq, int64_t qcols) {
+  if (!valid_dtype(pt) || !valid_dtype(gate_t)) return fail(FP8DS_ERR_ENUM, "%s: bad dtype", who);
+  if (!(std::isfinite(post_eps) && post_eps >= 0.0f) || !std::isfinite(alpha))
+    return fail(FP8DS_ERR_VALUE, "%s: bad post_eps or alpha", who);
+  if (int e = norm_args(who, a, x, xt, ldx, residual, ldr, ht, gamma, gt, rows, cols, eps, h, ldh, y, yt,
+                        ldy, rstd, q, ldq, qcols))
+    return e;
+  if (rows > 0 && cols > 0) {
+    if (!post_gamma || !residual || !h)
+      return fail(FP8DS_ERR_NULL, "%s: post_gamma, residual and h are required", who);
+    if (reinterpret_cast<uintptr_t>(post_gamma) % (pt == FP8DS_BF16 ? 2 : 4) ||
+        reinterpret_cast<uintptr_t>(gate) % (gate_t == FP8DS_BF16 ? 2 : 4))
+      return fail(FP8DS_ERR_ALIGN, "%s: post_gamma or gate is not aligned to its elements", who);
+    if (!aligned16(post_gamma) || !aligned16(gate)) a.vec = false;
+  }
+  if (reinterpret_cast<uintptr_t>(post_rstd) % 4 || reinterpret_cast<uintptr_t>(row_gate) % 4)
+    return fail(FP8DS_ERR_ALIGN, "%s: post_rstd and row_gate are fp32", who);
+  a.post_gamma = post_gamma; a.post_gamma_bf16 = pt == FP8DS_BF16; a.post_eps = post_eps;
+  a.gate = gate; a.gate_bf16 = gate_t == FP8DS_BF16;
+  a.row_gate = row_gate; a.alpha = alpha; a.post_rstd = post_rstd;
+  return FP8DS_OK;
+}
+
+int fp8ds_rmsnorm_sandwich(const void* x, fp8ds_dtype xt, int64_t ldx, const void* post_gamma,
+                           fp8ds_dtype pt, float post_eps, const void* gate, fp8ds_dtype gate_t,
+                           const float* row_gate, float alpha, const void* residual, int64_t ldr,
+                           fp8ds_dtype ht, const void* gamma, fp8ds_dtype gt, int64_t rows,
+                           int64_t cols, float eps, void* h, int64_t ldh, void* y, fp8ds_dtype yt,
+                           int64_t ldy, float* post_rstd, float* rstd, fp8ds_format fmt,
+                           const float* scale, uint8_t* q, int64_t ldq, float* scale_used, float* amax,
+                           uint64_t* sat_count, hipStream_t stream) {
+  const char* who = "fp8ds_rmsnorm_sandwich";
+  fp8ds::SandwichArgs a = {};
+  const bool cast = scale != nullptr;
+  if (cast && !valid_fmt(fmt)) return fail(FP8DS_ERR_ENUM, "%s: bad format %d", who, (int)fmt);
+  if (!cast && (q || scale_used || amax || sat_count))
+    return fail(FP8DS_ERR_NULL, "%s: q, scale_used, amax and sat_count need scale", who);
+  if (int e = sandwich_args(who, a, x, xt, ldx, post_gamma, pt, post_eps, gate, gate_t, row_gate, alpha,
+                            residual, ldr, ht, gamma, gt, rows, cols, eps, h, ldh, y, yt, ldy, post_rstd,
+                            rstd, q, ldq, cols))
+    return e;
+  if (cast && rows > 0 && cols > 0 && !q) return fail(FP8DS_ERR_NULL, "%s: q is null", who);
+  if (rows == 0 || cols == 0)
+    return scale_used ? hip_status(fp8ds::launch_prologue(1, scale, scale_used, nullptr, nullptr,
+                                                          stream), who)
+                      : ok();
+  a.mode = cast ? 1 : 0;
+  a.fmt = (int)fmt;
+  a.scale_in = scale; a.scale_used = scale_used; a.amax = amax; a.sat = sat_count;
+  return hip_status(fp8ds::launch_sandwich_fwd(a, num_cus(), stream), who);
+}
+
+int fp8ds_rmsnorm_sandwich_rowwise(const void* x, fp8ds_dtype xt, int64_t ldx, const void* post_gamma,
+                                   fp8ds_dtype pt, float post_eps, const void* gate,
+                                   fp8ds_dtype gate_t, const float* row_gate, float alpha,
+                                   const void* residual, int64_t ldr, fp8ds_dtype ht,
+                                   const void* gamma, fp8ds_dtype gt, int64_t rows, int64_t cols,
+                                   float eps, void* h, int64_t ldh, void* y, fp8ds_dtype yt,
+                                   int64_t ldy, float* post_rstd, float* rstd, fp8ds_format fmt,
+                                   int margin, uint8_t* q, int64_t ldq, float* scale, float* scale_inv,
+                                   float* amax, hipStream_t stream) {
+  const char* who = "fp8ds_rmsnorm_sandwich_rowwise";
+  fp8ds::SandwichArgs a = {};
+  if (!valid_fmt(fmt)) return fail(FP8DS_ERR_ENUM, "%s: bad format %d", who, (int)fmt);
+  if (margin < -126 || margin > 126)
+    return fail(FP8DS_ERR_SHAPE, "%s: margin %d not in [-126, 126]", who, margin);
+  if (int e = sandwich_args(who, a, x, xt, ldx, post_gamma, pt, post_eps, gate, gate_t, row_gate, alpha,
+                            residual, ldr, ht, gamma, gt, rows, cols, eps, h, ldh, y, yt, ldy, post_rstd,
+                            rstd, q, ldq, cols))
+    return e;
+  if (rows == 0 || cols == 0) return ok();
+  if (!q || !scale) return fail(FP8DS_ERR_NULL, "%s: q and scale are required", who);
+  a.mode = 2;
+  a.fmt = (int)fmt; a.margin = margin;
+  a.scale_out = scale; a.scale_inv = scale_inv; a.amax = amax;
+  return hip_status(fp8ds::launch_sandwich_fwd(a, num_cus(), stream), who);
+}
+
+int fp8ds_rmsnorm_sandwich_mx(const void* x, fp8ds_dtype xt, int64_t ldx, const void* post_gamma,
+                              fp8ds_dtype pt, float post_eps, const void* gate, fp8ds_dtype gate_t,
+                              const float* row_gate, float alpha, const void* residual, int64_t ldr,
+                              fp8ds_dtype ht, const void* gamma, fp8ds_dtype gt, int64_t rows,
+                              int64_t cols, float eps, void* h, int64_t ldh, void* y, fp8ds_dtype yt,
+                              int64_t ldy, float* post_rstd, float* rstd, fp8ds_format fmt, uint8_t* q,
+                              int64_t ldq, uint8_t* scales, int64_t ld_scales, hipStream_t stream) {
+  const char* who = "fp8ds_rmsnorm_sandwich_mx";
+  fp8ds::SandwichArgs a = {};
+  if (!valid_mx_fmt(fmt)) return fail(FP8DS_ERR_ENUM, "%s: bad format %d", who, (int)fmt);
+  if (cols > 0 && cols % 32 != 0)
+    return fail(FP8DS_ERR_SHAPE, "%s: the row length %lld is not a multiple of the block (32)", who,
+                (long long)cols);
+  if (int e = sandwich_args(who, a, x, xt, ldx, post_gamma, pt, post_eps, gate, gate_t, row_gate, alpha,
+                            residual, ldr, ht, gamma, gt, rows, cols, eps, h, ldh, y, yt, ldy, post_rstd,
+                            rstd, q, ldq, fmt == FP8DS_E2M1 ? cols / 2 : cols))
+    return e;
+  if (rows == 0 || cols == 0) return ok();
+  if (!q || !scales) return fail(FP8DS_ERR_NULL, "%s: q and scales are required", who);
+  if (ld_scales < cols / 32 || ld_scales > kMaxElems / rows)
+    return fail(FP8DS_ERR_SHAPE, "%s: ld_scales %lld for %lld blocks a row", who,
+                (long long)ld_scales, (long long)(cols / 32));
+  if (!a.vec)
+    return fail(FP8DS_ERR_ALIGN, "%s: the rows of x, residual, h and y and the parameters must be "
+                "16-byte aligned, the rows of q 8-byte", who);
+  a.mode = 3;
+  a.fmt = (int)fmt;
+  a.mx_scales = scales; a.ldms = ld_scales;
+  return hip_status(fp8ds::launch_sandwich_fwd(a, num_cus(), stream), who);
+}
+
+int64_t fp8ds_rmsnorm_sandwich_bwd_workspace(int64_t rows, int64_t cols) {
+  if (check_norm_shape("fp8ds_rmsnorm_sandwich_bwd_workspace", rows, cols)) return FP8DS_ERR_SHAPE;
+  ok();
+  return rows == 0 ? 0
+                   : 2 * (int64_t)fp8ds::sandwich_bwd_parts(rows, cols) * cols * (int64_t)sizeof(float);
+}
+
+int fp8ds_rmsnorm_sandwich_bwd(const void* dy, fp8ds_dtype xt, int64_t lddy, const void* h,
+                               fp8ds_dtype ht, int64_t ldh, const float* rstd, const void* gamma,
+                               fp8ds_dtype gt, const void* x, int64_t ldx, const float* post_rstd,
+                               const void* post_gamma, fp8ds_dtype pt, const void* gate,
+                               fp8ds_dtype gate_t, const float* row_gate, float alpha,
+                               const void* dres, int64_t lddr, int64_t rows, int64_t cols, void* dh,
+                               int64_t lddh, void* dx, int64_t lddx, float* dgamma, float* dpost_gamma,
+                               float* dgate, float* drow_gate, void* workspace,
+                               int64_t workspace_bytes, fp8ds_format fmt, const float* scale, uint8_t* q,
+                               int64_t ldq, float* scale_used, float* amax, uint64_t* sat_count,
+                               hipStream_t stream) {
+  const char* who = "fp8ds_rmsnorm_sandwich_bwd";
+  fp8ds::SandwichBwdArgs a = {};
+  if (!valid_dtype(xt) || !valid_dtype(ht) || !valid_dtype(gt) || !valid_dtype(pt) ||
+      !valid_dtype(gate_t))
+    return fail(FP8DS_ERR_ENUM, "%s: bad dtype", who);
+  if (xt == FP8DS_F32 && ht == FP8DS_BF16)
+    return fail(FP8DS_ERR_UNSUPPORTED, "%s: an FP32 x with a BF16 residual stream", who);
+  if (!std::isfinite(alpha)) return fail(FP8DS_ERR_VALUE, "%s: bad alpha", who);
+  const bool cast = scale != nullptr;
+  if (cast && !valid_fmt(fmt)) return fail(FP8DS_ERR_ENUM, "%s: bad format %d", who, (int)fmt);
+  if (!cast && (q || scale_used || amax || sat_count))
+    return fail(FP8DS_ERR_NULL, "%s: q, scale_used, amax and sat_count need scale", who);
+  if (int e = check_norm_shape(who, rows, cols)) return e;
+  if (cols == 0)
+    return scale_used ? hip_status(fp8ds::launch_prologue(1, scale, scale_used, nullptr, nullptr,
+                                                          stream), who)
+                      : ok();
+  if (!dgamma || !dpost_gamma)
+    return fail(FP8DS_ERR_NULL, "%s: dgamma and dpost_gamma are required", who);
+  if (dgate && !gate) return fail(FP8DS_ERR_NULL, "%s: dgate without a gate", who);
+  if (drow_gate && !row_gate) return fail(FP8DS_ERR_NULL, "%s: drow_gate without a row_gate", who);
+  const float* f32[] = {dgamma, dpost_gamma, dgate, drow_gate, rstd, post_rstd, row_gate};
+  for (const float* v : f32)
+    if (reinterpret_cast<uintptr_t>(v) % 4)
+      return fail(FP8DS_ERR_ALIGN, "%s: an fp32 vector is not aligned to its elements", who);
+  // (also read when there are no rows: the column sums' factors)
+  if (!post_gamma) return fail(FP8DS_ERR_NULL, "%s: post_gamma is required", who);
+  if (reinterpret_cast<uintptr_t>(post_gamma) % (pt == FP8DS_BF16 ? 2 : 4) ||
+      reinterpret_cast<uintptr_t>(gate) % (gate_t == FP8DS_BF16 ? 2 : 4) ||
+      reinterpret_cast<uintptr_t>(gamma) % (gt == FP8DS_BF16 ? 2 : 4))
+    return fail(FP8DS_ERR_ALIGN, "%s: a parameter is not aligned to its elements", who);
+  if (rows > 0) {
+    if (!dy || !h || !rstd || !gamma || !x || !post_rstd || !dh)
+      return fail(FP8DS_ERR_NULL, "%s: dy, h, rstd, gamma, x, post_rstd and dh are required", who);
+    if (cast && !q) return fail(FP8DS_ERR_NULL, "%s: q is null", who);
+    const int hs = ht == FP8DS_BF16 ? 2 : 4, xs = xt == FP8DS_BF16 ? 2 : 4;
+    const RowsArg m[] = {{"dy", dy, lddy, xs}, {"h", h, ldh, hs}, {"x", x, ldx, xs},
+                         {"dres", dres, lddr, hs}, {"dh", dh, lddh, hs}, {"dx", dx, lddx, xs},
+                         {"q", q, ldq, 1}};
+    if (int e = check_rows(who, m, 7, rows, cols, &a.vec)) return e;
+    if (!aligned16(gamma) || !aligned16(post_gamma) || !aligned16(gate)) a.vec = false;
+    const int64_t need = fp8ds_rmsnorm_sandwich_bwd_workspace(rows, cols);
+    if (!workspace || workspace_bytes < need)
+      return fail(workspace ? FP8DS_ERR_SHAPE : FP8DS_ERR_NULL, "%s: workspace of %lld bytes, %lld "
+                  "needed", who, (long long)(workspace ? workspace_bytes : 0), (long long)need);
+    if (!aligned16(workspace))
+      return fail(FP8DS_ERR_ALIGN, "%s: workspace not 16-byte aligned", who);
+  }
+  a.dy = dy; a.x_bf16 = xt == FP8DS_BF16; a.lddy = lddy;
+  a.h = h; a.h_bf16 = ht == FP8DS_BF16; a.ldh = ldh;
+  a.x = x; a.ldx = ldx;
+  a.dres = dres; a.lddr = lddr;
+  a.rstd = rstd; a.post_rstd = post_rstd;
+  a.gamma = gamma; a.gamma_bf16 = gt == FP8DS_BF16;
+  a.post_gamma = post_gamma; a.post_gamma_bf16 = pt == FP8DS_BF16;
+  a.gate = gate; a.gate_bf16 = gate_t == FP8DS_BF16;
+  a.row_gate = row_gate; a.alpha = alpha;
+  a.rows = rows; a.cols = cols;
+  a.dh = dh; a.lddh = lddh; a.dx = dx; a.lddx = lddx;
+  a.dgamma = dgamma; a.dpost_gamma = dpost_gamma; a.dgate = dgate; a.drow_gate = drow_gate;
+  a.work = static_cast<float*>(workspace);
+  a.fmt = (int)fmt; a.scale_in = scale; a.q = q; a.ldq = ldq;
+  a.scale_used = scale_used; a.amax = amax; a.sat = sat_count;
+  hipError_t e = hipSuccess;
+  if (rows == 0 && scale_used)
+    e = fp8ds::launch_prologue(1, scale, scale_used, nullptr, nullptr, stream);
+  if (e == hipSuccess) e = fp8ds::launch_sandwich_bwd(a, stream);
+  return hip_status(e, who);
+}
+
 }  // extern "C"

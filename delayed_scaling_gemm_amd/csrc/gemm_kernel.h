@@ -49,7 +49,7 @@
 
 #include <type_traits>
 
-#include "device_common.h"
+#include "cast_common.h"
 #include "launch.h"
 
 namespace fp8ds {
@@ -58,9 +58,6 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
 constexpr int kRowBytes = 128;  // bytes per LDS tile row (both datapaths)
 
 struct GemmArgs {
@@ -82,6 +79,35 @@ struct GemmArgs {
   const uint8_t* sc_a;  // MX: E8M0 scale of each 32-element block of a row of A [M][ldsa]
   const uint8_t* sc_b;  // MX: the same for B [N][ldsb]
   int64_t ldsa, ldsb;
+};
+
+// What a kernel does with its tile: the dequantised product; a gated feed-forward block's
+// activation and product of two column halves; or the backward pass of that (gated.h).
+constexpr int kEpiPlain = 0, kEpiGate = 1, kEpiGateBwd = 2;
+// N is the block's inner width F; B of kEpiGate is [2F x K], rows F .. 2F the second half.
+struct GatedArgs : GemmArgs {
+  int act;
+  uint16_t* gu;         // [M][ldgu] BF16, halves F apart: out or null (forward), in (backward)
+  int64_t ldgu;
+  void* y;              // or null: [M][ldy] the unquantised result (backward: halves F apart)
+  int64_t ldy;
+  int y_f32;
+  uint8_t* q;           // or null: its FP8 codes [M][ldq]
+  int64_t ldq;
+  int fmt;
+  const float* scale;   // with q
+  float* scale_used;    // or null
+  uint32_t* amax;       // or null: combined into
+  unsigned long long* sat;  // or null: added to
+  int vec;              // the rows of gu, y and q are 16-byte aligned, F a multiple of 16
+};
+template <int EPI>
+struct EpiArgs {
+  using type = GatedArgs;
+};
+template <>
+struct EpiArgs<kEpiPlain> {
+  using type = GemmArgs;
 };
 
 __device__ __forceinline__ int swz(int r) { return (r ^ (r >> 4)) & 7; }
@@ -154,7 +180,14 @@ __device__ __forceinline__ float e8m0_to_f32(uint32_t code) {
 // KC: K-contiguous source, rows [row0, row0 + ROWS) of a [rows x K] byte matrix
 // (leading dimension ld); one stage covers KB bytes of K starting at k0.  Each
 // lane moves 16-byte chunks; bytes past K read as zero.
-template <int ROWS, int NT, int KB>
+// HALF > 0: the tile's rows are runs of HALF taken in turn from row0 on and from `up` rows
+// further on (the gate's and the up projection's columns of one wave lie next to each other).
+template <int HALF>
+__device__ __forceinline__ int64_t half_row(int r, int64_t up) {
+  if constexpr (HALF == 0) return r;
+  else return (r / (2 * HALF)) * HALF + r % HALF + ((r / HALF) & 1 ? up : 0);
+}
+template <int ROWS, int NT, int KB, int HALF = 0>
 struct LoaderKC {
   static constexpr int kPerRow = KB / 16;  // source chunks per row per stage
   static constexpr int kChunks = ROWS * kPerRow / NT;
@@ -162,12 +195,13 @@ struct LoaderKC {
   u32x4 v[kChunks];
 
   __device__ __forceinline__ void load(const uint8_t* __restrict__ src, int64_t ld, int64_t row0,
-                                       int64_t rows, int64_t k0, int64_t K, int tid) {
+                                       int64_t rows, int64_t k0, int64_t K, int tid,
+                                       int64_t up = 0) {
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       const int q = tid + NT * i;
       const int r = q / kPerRow, c = q % kPerRow;
-      const int64_t gr = row0 + r;
+      const int64_t gr = row0 + half_row<HALF>(r, up);
       const int64_t gk = k0 + c * 16;
       u32x4 val = {0u, 0u, 0u, 0u};
       if (gr < rows && gk < K) {
@@ -268,14 +302,14 @@ struct LoaderMN {
   }
 };
 
-template <bool KC, int ROWS, int NT, int KB>
+template <bool KC, int ROWS, int NT, int KB, int HALF = 0>
 struct LoaderSel;
-template <int ROWS, int NT, int KB>
-struct LoaderSel<true, ROWS, NT, KB> {
-  using type = LoaderKC<ROWS, NT, KB>;
+template <int ROWS, int NT, int KB, int HALF>
+struct LoaderSel<true, ROWS, NT, KB, HALF> {
+  using type = LoaderKC<ROWS, NT, KB, HALF>;
 };
 template <int ROWS, int NT, int KB>
-struct LoaderSel<false, ROWS, NT, KB> {
+struct LoaderSel<false, ROWS, NT, KB, 0> {
   using type = LoaderMN<ROWS, NT, KB>;
 };
 
@@ -312,8 +346,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t byte_rsrc(const uint8_t* base,
 // stage K): no per-load address arithmetic beyond one XOR and one add, and rows
 // past the matrix read as zeros (they only feed outputs that are never stored).
 // Requires every offset of the operand below 2^31 (checked by the caller).
-template <int ROWS, int NT>
+template <int ROWS, int NT, int HALF = 0>
 struct LoaderKCDirect {
+  static_assert(HALF % 8 == 0, "a segment of 8 rows lies in one run");
   static constexpr int kSegs = ROWS / 8;
   static constexpr int kWaves = NT / 64;
   static constexpr int kPerWave = kSegs / kWaves;
@@ -323,11 +358,13 @@ struct LoaderKCDirect {
   int w;         // wave index (scalar)
   int lane_row;  // (lane / 8) * ld
   int colx;      // ((lane % 8) ^ (lane / 8)) * 16
+  int up;        // HALF: distance of the second run's rows
 
   // rows [row0, rows) of a [rows x K] byte matrix with leading dimension ld
   __device__ __forceinline__ LoaderKCDirect(const uint8_t* src, int64_t ld_, int64_t row0,
-                                            int64_t rows, int64_t K, int tid) {
+                                            int64_t rows, int64_t K, int tid, int64_t up_ = 0) {
     ld = (int)ld_;
+    up = (int)up_;
     w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lane = tid & 63, rr = lane >> 3, pc = lane & 7;
     lane_row = rr * ld;
@@ -346,7 +383,7 @@ struct LoaderKCDirect {
       if (i < lo || i >= hi) continue;
       const int seg = w * kPerWave + i;
       const int voff = lane_row + (colx ^ (((seg >> 1) & 7) << 4));
-      const int soff = seg * 8 * ld + (int)k0;
+      const int soff = (int)half_row<HALF>(seg * 8, up) * ld + (int)k0;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rsrc, (void __attribute__((address_space(3)))*)(lds + seg * 1024), 16, voff, soff, 0, 0);
     }
@@ -418,14 +455,14 @@ struct LoaderMNDirect {
   }
 };
 
-template <bool KC, int ROWS, int NT>
+template <bool KC, int ROWS, int NT, int HALF = 0>
 struct DirectSel;
-template <int ROWS, int NT>
-struct DirectSel<true, ROWS, NT> {
-  using type = LoaderKCDirect<ROWS, NT>;
+template <int ROWS, int NT, int HALF>
+struct DirectSel<true, ROWS, NT, HALF> {
+  using type = LoaderKCDirect<ROWS, NT, HALF>;
 };
 template <int ROWS, int NT>
-struct DirectSel<false, ROWS, NT> {
+struct DirectSel<false, ROWS, NT, 0> {
   using type = LoaderMNDirect<ROWS, NT>;
 };
 
@@ -660,6 +697,10 @@ __device__ __forceinline__ int epilogue_barriers(const GemmArgs& p, int64_t m0, 
   return (!p.out_f32 && full ? 2 : 0) + (p.amax_c ? 1 : 0);
 }
 
+}  // namespace fp8ds
+#include "gated.h"
+namespace fp8ds {
+
 // ------------------------------------------------------------------ the kernel
 //
 // Both datapaths stage FP8 tiles of 128 K values per LDS row.  Lane l works on
@@ -686,8 +727,9 @@ __device__ __forceinline__ int epilogue_barriers(const GemmArgs& p, int64_t m0, 
 // grids of 128 x 128 tiles that give each CU one tile or less: twice the waves
 // per CU, without partial results in memory.
 template <int BM, int BN, bool A_KC, bool B_KC, int FA, int FB, bool EXACT, bool DIRECT,
-          bool VS = false, bool MX = false, int KS = 1>
-__global__ __launch_bounds__(256 * KS, 1) void gemm_kernel(GemmArgs p) {
+          bool VS = false, bool MX = false, int KS = 1, int EPI = kEpiPlain>
+__global__ __launch_bounds__(256 * KS, 1) void gemm_kernel(typename EpiArgs<EPI>::type p) {
+  static_assert(EPI == kEpiPlain || (A_KC && B_KC && !VS && !MX), "gated blocks: NT products");
   static_assert(!MX || (DIRECT && A_KC && B_KC && !VS),
                 "MX blocks run along K: both operands K-contiguous, direct loads");
   static_assert(KS == 1 || (KS == 2 && DIRECT && !MX && BM == 128 && BN == 128),
@@ -696,6 +738,9 @@ __global__ __launch_bounds__(256 * KS, 1) void gemm_kernel(GemmArgs p) {
   constexpr int WTM = BM / 2, WTN = BN / 2;
   constexpr int FM = WTM / 32, FN = WTN / 32;
   constexpr int KB = 128;  // K values per stage
+  // kEpiGate: half of the tile's columns are the gate's, half the up projection's
+  constexpr int HALF = EPI == kEpiGate ? WTN / 2 : 0;
+  constexpr int BNO = EPI == kEpiGate ? BN / 2 : BN;  // output columns of a tile
   __shared__ __attribute__((aligned(16))) uint8_t lds_a_g[KS][2][BM * kRowBytes];
   __shared__ __attribute__((aligned(16))) uint8_t lds_b_g[KS][2][BN * kRowBytes];
   __shared__ uint32_t red[4];
@@ -711,13 +756,19 @@ __global__ __launch_bounds__(256 * KS, 1) void gemm_kernel(GemmArgs p) {
 
   int tm, tn;
   tile_coords(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
-  const int64_t M = p.M, N = p.N, K = p.K;
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BNO;
+  const int64_t M = p.M, K = p.K;
+  const int64_t N = EPI == kEpiGate ? 2 * p.N : p.N;  // rows of B
+  const int64_t up = EPI == kEpiGate ? p.N : 0;
   const uint8_t* A = p.A + bz * p.stride_a;
   const uint8_t* B = p.B + bz * p.stride_b;
 
   typename LoaderSel<A_KC, BM, NT, KB>::type la;
-  typename LoaderSel<B_KC, BN, NT, KB>::type lb;
+  typename LoaderSel<B_KC, BN, NT, KB, HALF>::type lb;
+  auto load_b = [&](int64_t k0) {
+    if constexpr (HALF > 0) lb.load(B, p.ldb, n0, N, k0, K, tid, up);
+    else lb.load(B, p.ldb, n0, N, k0, K, tid);
+  };
 
   v16f acc[FM][FN];
 #pragma unroll
@@ -792,9 +843,12 @@ __global__ __launch_bounds__(256 * KS, 1) void gemm_kernel(GemmArgs p) {
   constexpr int kIssuesA = direct_issues<A_KC, BM, NT>();
   constexpr int kIssuesB = direct_issues<B_KC, BN, NT>();
   using DLA = typename DirectSel<A_KC, BM, NT>::type;
-  using DLB = typename DirectSel<B_KC, BN, NT>::type;
+  using DLB = typename DirectSel<B_KC, BN, NT, HALF>::type;
   const DLA dla(DIRECT ? A : nullptr, p.lda, m0, M, K, tid);
-  const DLB dlb(DIRECT ? B : nullptr, p.ldb, n0, N, K, tid);
+  const DLB dlb = [&] {
+    if constexpr (HALF > 0) return DLB(DIRECT ? B : nullptr, p.ldb, n0, N, K, tid, up);
+    else return DLB(DIRECT ? B : nullptr, p.ldb, n0, N, K, tid);
+  }();
   auto issue_direct = [&](int kt, int buf, int lo = 0, int hi = 1 << 20) {
     if constexpr (DIRECT) {
       const int la = lo, ha = hi < kIssuesA ? hi : kIssuesA;
@@ -903,7 +957,7 @@ __global__ __launch_bounds__(256 * KS, 1) void gemm_kernel(GemmArgs p) {
         }
       } else {
         la.load(A, p.lda, m0, M, 0, K, tid);
-        lb.load(B, p.ldb, n0, N, 0, K, tid);
+        load_b(0);
         la.store(lds_a[0], tid);
         lb.store(lds_b[0], tid);
       }
@@ -931,7 +985,7 @@ __global__ __launch_bounds__(256 * KS, 1) void gemm_kernel(GemmArgs p) {
       if constexpr (MX) take_scales(0);  // units 0, 1 of this stage (loaded a stage ago)
       if constexpr (MORE && !DIRECT) {
         la.load(A, p.lda, m0, M, (int64_t)(kt + 1) * KB, K, tid);
-        lb.load(B, p.ldb, n0, N, (int64_t)(kt + 1) * KB, K, tid);
+        load_b((int64_t)(kt + 1) * KB);
       }
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
@@ -1075,7 +1129,7 @@ __global__ __launch_bounds__(256 * KS, 1) void gemm_kernel(GemmArgs p) {
         }
       } else {
         la.load(A, p.lda, m0, M, 0, K, tid);
-        lb.load(B, p.ldb, n0, N, 0, K, tid);
+        load_b(0);
         la.store(lds_a[0], tid);
         lb.store(lds_b[0], tid);
       }
@@ -1118,7 +1172,7 @@ __global__ __launch_bounds__(256 * KS, 1) void gemm_kernel(GemmArgs p) {
       const int cur = kt & 1;
       if constexpr (MORE && !DIRECT) {
         la.load(A, p.lda, m0, M, (int64_t)(kt + 1) * KB, K, tid);
-        lb.load(B, p.ldb, n0, N, (int64_t)(kt + 1) * KB, K, tid);
+        load_b((int64_t)(kt + 1) * KB);
       }
       if constexpr (MX) {
 #pragma unroll
@@ -1194,7 +1248,10 @@ __global__ __launch_bounds__(256 * KS, 1) void gemm_kernel(GemmArgs p) {
     __syncthreads();
     if (grp == 1) {
       // the epilogue's barriers, which group 0 reaches there
-      const int nb = epilogue_barriers<BM, BN>(p, m0, n0);
+      const int nb = [&] {
+        if constexpr (EPI == kEpiPlain) return epilogue_barriers<BM, BN>(p, m0, n0);
+        else return gated_barriers(p);
+      }();
       for (int b = 0; b < nb; ++b) __syncthreads();
       return;
     }
@@ -1209,9 +1266,12 @@ __global__ __launch_bounds__(256 * KS, 1) void gemm_kernel(GemmArgs p) {
           for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] = acc[i][j][4 * q + e] + o[e];
         }
   }
-  epilogue<BM, BN, FM, FN, WTM, WTN, VS>(p, acc, m0, n0, wm, wn, tid, bz, d, red,
-                                        reinterpret_cast<uint8_t*>(lds_a),
-                                        reinterpret_cast<uint8_t*>(lds_b));
+  uint8_t *st0 = reinterpret_cast<uint8_t*>(lds_a), *st1 = reinterpret_cast<uint8_t*>(lds_b);
+  if constexpr (EPI == kEpiPlain)
+    epilogue<BM, BN, FM, FN, WTM, WTN, VS>(p, acc, m0, n0, wm, wn, tid, bz, d, red, st0, st1);
+  else
+    gated_epilogue<EPI == kEpiGateBwd, BM, BNO, FM, FN, WTM, WTN>(p, acc, m0, n0, wm, wn, tid, d,
+                                                                  red, st0, st1);
 }
 
 // ------------------------------------------------------------------ dispatch

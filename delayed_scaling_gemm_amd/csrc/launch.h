@@ -218,6 +218,56 @@ struct NormBwdArgs {
 int norm_bwd_parts(int64_t rows, int64_t cols);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream);
 
+// The norms around a gated residual addition (sandwich.hip).  NormArgs hold x, res (required), h
+// (required), the second norm and its cast.
+struct SandwichArgs : NormArgs {
+  const void* post_gamma;  // [cols]
+  bool post_gamma_bf16;
+  float post_eps;
+  const void* gate;        // or null: [cols]
+  bool gate_bf16;
+  const float* row_gate;   // or null: [rows]
+  float alpha;
+  float* post_rstd;        // or null: [rows]
+};
+hipError_t launch_sandwich_fwd(const SandwichArgs& a, int num_cus, hipStream_t stream);
+
+struct SandwichBwdArgs {
+  const void* dy;          // [rows][lddy]
+  bool x_bf16;             // type of dy, x and dx
+  const void* h;           // [rows][ldh]
+  bool h_bf16;             // type of h, dres and dh
+  const void* x;           // [rows][ldx]
+  const void* dres;        // or null
+  const float* rstd;       // [rows]
+  const float* post_rstd;  // [rows]
+  const void* gamma;
+  bool gamma_bf16;
+  const void* post_gamma;
+  bool post_gamma_bf16;
+  const void* gate;        // or null
+  bool gate_bf16;
+  const float* row_gate;   // or null
+  float alpha;
+  int64_t rows, cols, lddy, ldh, ldx, lddr, lddh, lddx, ldq;
+  void* dh;                // [rows][lddh]
+  void* dx;                // or null: [rows][lddx]
+  float* dgamma;           // [cols]
+  float* dpost_gamma;      // [cols]
+  float* dgate;            // or null: [cols]
+  float* drow_gate;        // or null: [rows]
+  float* work;             // [2][sandwich_bwd_parts][cols]
+  int fmt;
+  const float* scale_in;   // with q
+  uint8_t* q;              // or null: [rows][ldq]
+  float* scale_used;       // or null
+  float* amax;             // or null: combined into
+  uint64_t* sat;           // or null: added to
+  bool vec;
+};
+int sandwich_bwd_parts(int64_t rows, int64_t cols);
+hipError_t launch_sandwich_bwd(const SandwichBwdArgs& a, hipStream_t stream);
+
 // Tensors of one launch of the gradient norm or the clip (kernel arguments: at most
 // 4 KB).  start[i]: the launch's first chunk of tensor i, start[count] their number.
 constexpr int kTensors = 128;
@@ -268,5 +318,37 @@ struct Mxfp4Gemm {
 };
 hipError_t launch_gemm_mxfp4(const Mxfp4Gemm& p, int fa, bool exact, int num_cus,
                              hipStream_t stream);
+
+// Gated feed-forward products.  Forward: A = X [M x K], B = [2F x K], gate rows then up rows.
+// Backward: A = dY [M x K], B = W_down [F x K].
+struct GatedProblem {
+  int64_t M, F, K;
+  const uint8_t* A;
+  int64_t lda;
+  const float* scale_a;
+  const uint8_t* B;      // E4M3
+  int64_t ldb;
+  const float* scale_b;
+  int act;               // 0 SiLU, 1 GELU (tanh form)
+  void* gu;              // [M][ldgu] BF16: out or null (forward), in (backward)
+  int64_t ldgu;
+  void* y;               // or null: [M][ldy]
+  bool y_bf16;
+  int64_t ldy;
+  int fmt;
+  const float* scale;    // with q
+  uint8_t* q;            // or null: [M][ldq]
+  int64_t ldq;
+  float* scale_used;     // or null
+  float* amax;           // or null: combined into
+  uint64_t* sat;         // or null: added to
+  bool vec;              // rows of gu, y and q at 16 bytes, F a multiple of 16
+};
+// Forward for at most kGatedFewRows rows (exact datapath).
+constexpr int64_t kGatedFewRows = 32;
+hipError_t launch_gated_few(const GatedProblem& p, hipStream_t stream);
+hipError_t launch_gated_fwd(const GatedProblem& p, bool exact, int num_cus, hipStream_t stream);
+hipError_t launch_gated_bwd(const GatedProblem& p, int fa, bool exact, int num_cus,
+                            hipStream_t stream);
 
 }  // namespace fp8ds

@@ -722,6 +722,135 @@ int fp8ds_gemm_mxfp4_mma(int64_t M, int64_t N, int64_t K, const uint8_t* A, fp8d
                          int64_t ld_scales_b, void* C, fp8ds_dtype ct, int64_t ldc, float* amax_c,
                          fp8ds_mma mma, hipStream_t stream);
 
+/* Activations of a gated feed-forward block: SiLU g / (1 + e^-g), GELU in its tanh form
+ * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2. */
+typedef enum { FP8DS_ACT_SILU = 0, FP8DS_ACT_GELU = 1 } fp8ds_act;
+
+/*
+ * fp8ds_gated_gemm -- gate and up projections of a feed-forward block, its activation and their
+ * product in one kernel:
+ *   g[i][j] = d sum_k a(i,k) b(j,k),  u[i][j] = d sum_k a(i,k) b(F+j,k),  d as fp8ds_gemm's
+ *   y[i][j] = act(g[i][j]) u[i][j]                    fp32, from the fp32 sums
+ * with y stored in 16 or 32 bits and / or cast to FP8 as fp8ds_cast_acc casts (q = encode(y *
+ * (*scale)); amax, of |y|, and sat_count are COMBINED INTO): the operand of the down projection.
+ *   A          device [M x K] codes, rows lda apart.   fa  E4M3.
+ *   B          device [2F x K] codes, rows ldb apart: the gate's rows, then the up projection's
+ *              (for weights stored [K x 2F] the transposed copy of their cast).   fb  E4M3.
+ *   scale_a/b  device, 1 float each: the scale snapshots of the operands.
+ *   gu         device or NULL: [M x 2F] BF16, rows ldgu apart: g, then u (for the backward pass).
+ *   y          device or NULL: [M x F] of yt, rows ldy apart.
+ *   scale      device or NULL (then q, scale_used and sat_count must be NULL): the delayed scale.
+ *   q          device [M x F] codes of fmt, rows ldq apart.
+ *   amax       device or NULL: of y, with or without a scale.
+ *   mma        as fp8ds_gemm; up to 32 rows run exact either way.
+ *   M, F, K    >= 0, any size (ceil(M/128) ceil(F/64) < 2^23).  Rows of A and B 16-byte aligned; gu
+ *              and y aligned to their elements (fastest with rows at 16 bytes, F a multiple of 16).
+ * At least one of gu, y and q.  Outputs must not overlap each other or the operands.  M or F of 0:
+ * nothing but *scale_used is written.  Up to 32 rows read every weight once.
+ */
+int fp8ds_gated_gemm(int64_t M, int64_t F, int64_t K, const uint8_t* A, fp8ds_format fa, int64_t lda,
+                     const float* scale_a, const uint8_t* B, fp8ds_format fb, int64_t ldb,
+                     const float* scale_b, fp8ds_act act, void* gu, int64_t ldgu, void* y,
+                     fp8ds_dtype yt, int64_t ldy, fp8ds_format fmt, const float* scale, uint8_t* q,
+                     int64_t ldq, float* scale_used, float* amax, uint64_t* sat_count, fp8ds_mma mma,
+                     hipStream_t stream);
+
+/*
+ * fp8ds_gated_gemm_bwd -- backward of the block through the down projection and the activation:
+ *   da[i][j] = d sum_h a(i,h) b(j,h)
+ *   dg = da u act'(g),   du = da act(g)               fp32, from the stored g and u
+ *   A          device [M x H] codes of dY, E5M2 or E4M3.
+ *   B          device [F x H] codes of the down projection as stored ([in, out]), E4M3.
+ *   gu         device [M x 2F] BF16: what fp8ds_gated_gemm stored.
+ *   dgu        device or NULL: [M x 2F] of dt, rows lddgu apart: dg, then du.
+ *   q          device or NULL: the same in FP8 (E5M2 as a rule), rows ldq apart, with scale,
+ *              scale_used, amax and sat_count as fp8ds_gated_gemm.  One scale for both halves, so
+ *              dX = [dg du] W^T and dW = X^T [dg du] are single fp8ds_gemm calls.
+ * Other arguments, sizes and alignment as fp8ds_gated_gemm.  At least one of dgu and q; neither may
+ * overlap gu.
+ */
+int fp8ds_gated_gemm_bwd(int64_t M, int64_t F, int64_t H, const uint8_t* A, fp8ds_format fa,
+                         int64_t lda, const float* scale_a, const uint8_t* B, fp8ds_format fb,
+                         int64_t ldb, const float* scale_b, fp8ds_act act, const void* gu,
+                         int64_t ldgu, void* dgu, fp8ds_dtype dt, int64_t lddgu, fp8ds_format fmt,
+                         const float* scale, uint8_t* q, int64_t ldq, float* scale_used, float* amax,
+                         uint64_t* sat_count, fp8ds_mma mma, hipStream_t stream);
+
+/*
+ * The norms around a residual addition: the branch's output x is normalised, gated and added, the
+ * new stream is normalised for the next block, and that is cast.  Per row
+ *   r1 = 1 / sqrt(sum_c x[c]^2 / cols + post_eps)
+ *   h[c] = residual[c] + t (x[c] r1) (alpha gate[c] post_gamma[c])    rounded to ht
+ *   r2 = 1 / sqrt(sum_c h[c]^2 / cols + eps),   y[c] = (h[c] r2) gamma[c]
+ * with everything in fp32, and y cast as fp8ds_rmsnorm, _rowwise and _mx cast theirs.
+ *   x, residual, h, y, gamma, eps, rstd (r2) and the cast's arguments: as those calls; residual and
+ *              h are required here.  h may be residual itself.
+ *   post_gamma device [cols] of pt.          post_eps  finite, >= 0.
+ *   gate       device or NULL: [cols] of gate_t, a factor per channel.
+ *   row_gate   device or NULL: [rows], t, a factor per token (1 without it).
+ *   alpha      finite: the residual scale.
+ *   post_rstd  device or NULL: [rows], r1 (for the backward pass).
+ * fp8ds_rmsnorm_sandwich_mx needs post_gamma and gate 16-byte aligned too.
+ */
+int fp8ds_rmsnorm_sandwich(const void* x, fp8ds_dtype xt, int64_t ldx, const void* post_gamma,
+                           fp8ds_dtype pt, float post_eps, const void* gate, fp8ds_dtype gate_t,
+                           const float* row_gate, float alpha, const void* residual, int64_t ldr,
+                           fp8ds_dtype ht, const void* gamma, fp8ds_dtype gt, int64_t rows,
+                           int64_t cols, float eps, void* h, int64_t ldh, void* y, fp8ds_dtype yt,
+                           int64_t ldy, float* post_rstd, float* rstd, fp8ds_format fmt,
+                           const float* scale, uint8_t* q, int64_t ldq, float* scale_used, float* amax,
+                           uint64_t* sat_count, hipStream_t stream);
+int fp8ds_rmsnorm_sandwich_rowwise(const void* x, fp8ds_dtype xt, int64_t ldx, const void* post_gamma,
+                                   fp8ds_dtype pt, float post_eps, const void* gate,
+                                   fp8ds_dtype gate_t, const float* row_gate, float alpha,
+                                   const void* residual, int64_t ldr, fp8ds_dtype ht,
+                                   const void* gamma, fp8ds_dtype gt, int64_t rows, int64_t cols,
+                                   float eps, void* h, int64_t ldh, void* y, fp8ds_dtype yt,
+                                   int64_t ldy, float* post_rstd, float* rstd, fp8ds_format fmt,
+                                   int margin, uint8_t* q, int64_t ldq, float* scale, float* scale_inv,
+                                   float* amax, hipStream_t stream);
+int fp8ds_rmsnorm_sandwich_mx(const void* x, fp8ds_dtype xt, int64_t ldx, const void* post_gamma,
+                              fp8ds_dtype pt, float post_eps, const void* gate, fp8ds_dtype gate_t,
+                              const float* row_gate, float alpha, const void* residual, int64_t ldr,
+                              fp8ds_dtype ht, const void* gamma, fp8ds_dtype gt, int64_t rows,
+                              int64_t cols, float eps, void* h, int64_t ldh, void* y, fp8ds_dtype yt,
+                              int64_t ldy, float* post_rstd, float* rstd, fp8ds_format fmt, uint8_t* q,
+                              int64_t ldq, uint8_t* scales, int64_t ld_scales, hipStream_t stream);
+
+/*
+ * fp8ds_rmsnorm_sandwich_bwd -- backward of those.  With xh2 = h r2, g2 = dy gamma, xh1 = x r1,
+ * k = alpha gate post_gamma, per row
+ *   dh = r2 (g2 - xh2 (sum_c g2 xh2) / cols) + dres        the gradient of residual
+ *   g1 = t k dh,   dx = r1 (g1 - xh1 (sum_c g1 xh1) / cols)     from the fp32 dh
+ *   drow_gate = sum_c k dh xh1
+ * and over the rows, with S = sum alpha t dh xh1:
+ *   dgamma = sum dy xh2,   dpost_gamma = gate S,   dgate = post_gamma S
+ *   dy         device [rows x cols] of xt.      h   device [rows x cols] of ht: what was stored.
+ *   x          device [rows x cols] of xt.      rstd, post_rstd  device [rows]: what was stored.
+ *   dres       device or NULL: [rows x cols] of ht, the gradient that reaches h from above.
+ *   dh         device [rows x cols] of ht.  May be dres (same leading dimension).
+ *   dx         device or NULL: [rows x cols] of xt.  May be dy (same leading dimension).
+ *   dgamma, dpost_gamma  device [cols] fp32.    dgate  device or NULL: [cols] fp32.
+ *   drow_gate  device or NULL: [rows] fp32.
+ *   workspace  device, at least fp8ds_rmsnorm_sandwich_bwd_workspace(rows, cols) bytes, 16-byte
+ *              aligned; its contents need no preparation and do not matter afterwards.
+ *   scale      device or NULL: with it dx, in fp32, is also cast to FP8 (fmt, q, ldq, scale_used,
+ *              amax, sat_count as fp8ds_rmsnorm_bwd).
+ * (xt, ht) as fp8ds_rmsnorm.  Sums are fp32, in an order fixed by the shape.
+ */
+int64_t fp8ds_rmsnorm_sandwich_bwd_workspace(int64_t rows, int64_t cols);
+int fp8ds_rmsnorm_sandwich_bwd(const void* dy, fp8ds_dtype xt, int64_t lddy, const void* h,
+                               fp8ds_dtype ht, int64_t ldh, const float* rstd, const void* gamma,
+                               fp8ds_dtype gt, const void* x, int64_t ldx, const float* post_rstd,
+                               const void* post_gamma, fp8ds_dtype pt, const void* gate,
+                               fp8ds_dtype gate_t, const float* row_gate, float alpha,
+                               const void* dres, int64_t lddr, int64_t rows, int64_t cols, void* dh,
+                               int64_t lddh, void* dx, int64_t lddx, float* dgamma, float* dpost_gamma,
+                               float* dgate, float* drow_gate, void* workspace,
+                               int64_t workspace_bytes, fp8ds_format fmt, const float* scale, uint8_t* q,
+                               int64_t ldq, float* scale_used, float* amax, uint64_t* sat_count,
+                               hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
