@@ -10,7 +10,9 @@ Functions keep the C names: ``fp8ds_amax``, ``fp8ds_cast``, ``fp8ds_cast_health`
 ``fp8ds_cast_batched``, ``fp8ds_scale_update``, ``fp8ds_gemm``, ``fp8ds_gemm_batched``,
 ``fp8ds_linear_batched``, ``fp8ds_adamw``; around the Linear ``fp8ds_rmsnorm`` (``_rowwise``,
 ``_mx``, ``_bwd``), ``fp8ds_grad_norm``, ``fp8ds_grad_clip``, ``fp8ds_cast_mxfp4``,
-``fp8ds_dequant_mxfp4``, ``fp8ds_gemm_mxfp4`` (``_mma``).
+``fp8ds_dequant_mxfp4``, ``fp8ds_gemm_mxfp4`` (``_mma``); the feed-forward block
+``fp8ds_gated_gemm`` (``_bwd``), ``fp8ds_rmsnorm_sandwich`` (``_rowwise``, ``_mx``, ``_bwd``); Muon
+``fp8ds_muon_direction``, ``fp8ds_muon_apply``.
 """
 
 from __future__ import annotations
@@ -148,6 +150,14 @@ def _declare(lib):
                                                vp, i32, vp, i32, vp, f, vp, i64, i64, i64, vp, i64,
                                                vp, i64, vp, vp, vp, vp, vp, i64, i32, vp, vp, i64,
                                                vp, vp, vp, vp]
+    lib.fp8ds_muon_workspace.restype = i64
+    lib.fp8ds_muon_workspace.argtypes = [i64, i64]
+    lib.fp8ds_muon_direction.restype = i32
+    lib.fp8ds_muon_direction.argtypes = [vp, i32, vp, i64, i64, f, i32, f, vp, vp, i32, vp, f, vp, i32,
+                                         vp, i64, vp]
+    lib.fp8ds_muon_apply.restype = i32
+    lib.fp8ds_muon_apply.argtypes = [vp, vp, i32, i64, i64, f, f, f, vp, i32, vp, vp, vp, vp, vp, vp,
+                                     vp]
     return lib
 
 
@@ -1084,6 +1094,60 @@ def fp8ds_rmsnorm_sandwich_bwd(dy, h, rstd, gamma, x, post_rstd, post_gamma, dh,
           _vec(dgamma, "dgamma", f32, cols), _vec(dpost_gamma, "dpost_gamma", f32, cols),
           _vec(dgate, "dgate", f32, cols), _vec(drow_gate, "drow_gate", f32, rows), wp,
           0 if workspace is None else workspace.numel(), fmt, _vec(scale, "scale", f32, 1), qp, ldq,
+          _vec(scale_used, "scale_used", f32, 1), _vec(amax, "amax", f32, 1),
+          _vec(sat_count, "sat_count", (torch.int64,), 1), _stream(stream))
+
+
+def fp8ds_muon_workspace(rows, cols) -> int:
+    """Bytes of workspace that :func:`fp8ds_muon_direction` needs for this shape."""
+    n = lib().fp8ds_muon_workspace(rows, cols)
+    if n < 0:
+        _check(int(n))
+    return n
+
+
+def fp8ds_muon_direction(g, o, workspace, momentum=None, mu=0.95, nesterov=True, steps=5, coefs=None,
+                         eps=1e-7, grad_scale=1.0, grad_coef=None, grad_amax=None, stream=None):
+    """Muon's direction ``o`` [rows, cols] (bf16 or fp32) of the gradient ``g`` (bf16 or fp32): the
+    ``momentum`` (fp32, in place) takes it in, and ``steps`` Newton-Schulz steps with ``coefs``
+    (``steps`` triples; None: the usual quintic) orthogonalise the update.  ``grad_coef`` and
+    ``grad_amax`` as :func:`fp8ds_adamw`.  ``workspace``: uint8, :func:`fp8ds_muon_workspace`
+    bytes."""
+    import torch
+
+    high, f32 = _high(), (torch.float32,)
+    if g.dim() != 2 or g.shape != o.shape or (momentum is not None and momentum.shape != g.shape):
+        raise ValueError("g, o and momentum must be 2-D [rows, cols] of one shape")
+    rows, cols = g.shape
+    n, cp = rows * cols, None
+    if coefs is not None:
+        flat = [float(c) for triple in coefs for c in triple]
+        if len(flat) != 3 * steps:
+            raise ValueError(f"coefs: {len(flat)} numbers for {steps} steps of three")
+        cp = _host_array("f", flat)
+    _call("fp8ds_muon_direction", _vec(g, "g", high, n), high[g.dtype],
+          _vec(momentum, "momentum", f32, n), rows, cols, float(mu), int(bool(nesterov)),
+          float(grad_scale), _vec(grad_coef, "grad_coef", f32, 1),
+          _vec(grad_amax, "grad_amax", f32, 1), int(steps), cp, float(eps), _vec(o, "o", high, n),
+          high[o.dtype], _vec(workspace, "workspace", (torch.uint8,), 0),
+          0 if workspace is None else workspace.numel(), _stream(stream))
+
+
+def fp8ds_muon_apply(w, o, lr, weight_decay=0.0, adjust=1.0, fmt=E4M3, scale=None, q=None, q_t=None,
+                     scale_used=None, amax=None, sat_count=None, grad_amax=None, stream=None):
+    """``w`` (fp32 [rows, cols], in place) = (1 - lr weight_decay) w - lr adjust ``o``; with ``scale``
+    also the FP8 copy of the new weights (``q``, ``q_t``), ``amax`` and ``sat_count`` combined
+    into.  ``grad_amax``: a non-finite value leaves w alone."""
+    import torch
+
+    f32, u8, high = (torch.float32,), (torch.uint8,), _high()
+    if w.dim() != 2 or w.shape != o.shape:
+        raise ValueError("w and o must be 2-D [rows, cols] of one shape")
+    rows, cols = w.shape
+    n = rows * cols
+    _call("fp8ds_muon_apply", _vec(w, "w", f32, n), _vec(o, "o", high, n), high[o.dtype], rows, cols,
+          float(lr), float(weight_decay), float(adjust), _vec(grad_amax, "grad_amax", f32, 1), fmt,
+          _vec(scale, "scale", f32, 1), _vec(q, "q", u8, n), _vec(q_t, "q_t", u8, n),
           _vec(scale_used, "scale_used", f32, 1), _vec(amax, "amax", f32, 1),
           _vec(sat_count, "sat_count", (torch.int64,), 1), _stream(stream))
 

@@ -59,7 +59,12 @@ __device__ __forceinline__ bool adamw_skip(const AdamWLaunch& p) {
 // place the quads of consecutive lanes next to each other, so every load and
 // store instruction of a wave covers one contiguous run (1 KB of fp32).
 // Skipped steps only read w.
-template <bool GBF16>
+// APPLY: the step of a given direction instead (Muon's): w = decay w - step_size g.
+__device__ __forceinline__ float apply_elem(float w, float g, const AdamWConsts& c) {
+#pragma clang fp contract(off)
+  return c.decay * w - c.step_size * g;
+}
+template <bool GBF16, bool APPLY = false>
 __device__ __forceinline__ void adamw_quads(const AdamWLaunch& p, const int64_t (&off)[4],
                                             bool skip, uint32_t (&wb)[16]) {
   u32x4 wv[4];
@@ -74,8 +79,10 @@ __device__ __forceinline__ void adamw_quads(const AdamWLaunch& p, const int64_t 
   u32x4 mv[4], vv[4], gv[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    mv[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.m + off[k]));
-    vv[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.v + off[k]));
+    if constexpr (!APPLY) {
+      mv[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.m + off[k]));
+      vv[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.v + off[k]));
+    }
     if constexpr (GBF16) {
       const u32x2 h = __builtin_nontemporal_load(
           reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p.g) + off[k]));
@@ -87,6 +94,12 @@ __device__ __forceinline__ void adamw_quads(const AdamWLaunch& p, const int64_t 
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
+    if constexpr (APPLY) {
+      const float w = apply_elem(__uint_as_float(wv[i >> 2][i & 3]), __uint_as_float(gv[i >> 2][i & 3]), p.c);
+      wb[i] = __float_as_uint(w);
+      wv[i >> 2][i & 3] = wb[i];
+      continue;
+    }
     float m = __uint_as_float(mv[i >> 2][i & 3]);
     float v = __uint_as_float(vv[i >> 2][i & 3]);
     const float w = adamw_elem(__uint_as_float(wv[i >> 2][i & 3]),
@@ -99,18 +112,25 @@ __device__ __forceinline__ void adamw_quads(const AdamWLaunch& p, const int64_t 
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     __builtin_nontemporal_store(wv[k], reinterpret_cast<u32x4*>(p.w + off[k]));
-    __builtin_nontemporal_store(mv[k], reinterpret_cast<u32x4*>(p.m + off[k]));
-    __builtin_nontemporal_store(vv[k], reinterpret_cast<u32x4*>(p.v + off[k]));
+    if constexpr (!APPLY) {
+      __builtin_nontemporal_store(mv[k], reinterpret_cast<u32x4*>(p.m + off[k]));
+      __builtin_nontemporal_store(vv[k], reinterpret_cast<u32x4*>(p.v + off[k]));
+    }
   }
 }
 
 // One element (ragged tails and unaligned tiles); returns the new weight.
-template <bool GBF16>
+template <bool GBF16, bool APPLY = false>
 __device__ __forceinline__ float adamw1(const AdamWLaunch& p, int64_t i, bool skip) {
   const float w = p.w[i];
   if (skip) return w;
   const float g = GBF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.g)[i] << 16)
                         : static_cast<const float*>(p.g)[i];
+  if constexpr (APPLY) {
+    const float wn = apply_elem(w, g, p.c);
+    p.w[i] = wn;
+    return wn;
+  }
   float m = p.m[i], v = p.v[i];
   const float wn = adamw_elem(w, g, m, v, p.c);
   p.w[i] = wn;
@@ -132,9 +152,12 @@ __device__ __forceinline__ uint32_t cast1(float w, float s, uint32_t& amax, uint
 // threads owns 4096 consecutive elements; thread t takes the quads at
 // 4t + 1024k, k = 0..3.  The last, partial workgroup goes element by element.
 // CAST = false is the plain fused AdamW step.
-template <bool GBF16, int FMT, bool CAST>
+template <bool GBF16, int FMT, bool CAST, bool APPLY = false>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamWLaunch p) {
   __shared__ uint32_t red[2 * 4];
+  if constexpr (APPLY && CAST) {
+    if (p.scale_used && blockIdx.x == 0 && threadIdx.x == 0) *p.scale_used = *p.scale;
+  }
   if (p.grad_coef) p.c.grad_scale *= *p.grad_coef;  // before g: g' = g * fl32(scale * coef)
   const int64_t n = p.rows * p.cols;
   const bool skip = adamw_skip(p);
@@ -145,7 +168,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamWLaunch p) {
   if ((int64_t)(blockIdx.x + 1) * 4096 <= n) {
     const int64_t off[4] = {base, base + 1024, base + 2048, base + 3072};
     uint32_t wb[16];
-    adamw_quads<GBF16>(p, off, skip, wb);
+    adamw_quads<GBF16, APPLY>(p, off, skip, wb);
     if constexpr (CAST) {
       const u32x4 codes = cast16_f32<FMT, false>(wb, s, amax, sat, p.sat != nullptr);
 #pragma unroll
@@ -157,7 +180,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamWLaunch p) {
       for (int j = 0; j < 4; ++j) {
         const int64_t i = base + 1024 * k + j;
         if (i < n) {
-          const float w = adamw1<GBF16>(p, i, skip);
+          const float w = adamw1<GBF16, APPLY>(p, i, skip);
           if constexpr (CAST) p.q[i] = (uint8_t)cast1<FMT>(w, s, amax, sat);
         }
       }
@@ -171,11 +194,14 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamWLaunch p) {
 
 // Transposing kernel: a 128 x 128 tile of the [rows x cols] weights per
 // workgroup; q and q_t as the standalone transposing cast writes them.
-template <bool GBF16, int FMT>
+template <bool GBF16, int FMT, bool APPLY = false>
 __global__ __launch_bounds__(256) void adamw_transpose_kernel(AdamWLaunch p) {
   constexpr int T = 128;
   __shared__ __attribute__((aligned(16))) uint8_t tile[T * T];
   __shared__ uint32_t red[2 * 4];
+  if constexpr (APPLY) {
+    if (p.scale_used && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.scale_used = *p.scale;
+  }
   if (p.grad_coef) p.c.grad_scale *= *p.grad_coef;
   const bool skip = adamw_skip(p);
   const float s = p.scale[0];
@@ -199,7 +225,7 @@ __global__ __launch_bounds__(256) void adamw_transpose_kernel(AdamWLaunch p) {
         off[k] = (r0 + rr[k]) * cols + c0 + cc[k];
       }
       uint32_t wb[16];
-      adamw_quads<GBF16>(p, off, skip, wb);
+      adamw_quads<GBF16, APPLY>(p, off, skip, wb);
       const u32x4 codes = cast16_f32<FMT, false>(wb, s, amax, sat, p.sat != nullptr);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -218,7 +244,7 @@ __global__ __launch_bounds__(256) void adamw_transpose_kernel(AdamWLaunch p) {
       const int64_t c = c0 + tc + i;
       uint32_t code = 0;
       if (r < rows && c < cols) {
-        const float w = adamw1<GBF16>(p, r * cols + c, skip);
+        const float w = adamw1<GBF16, APPLY>(p, r * cols + c, skip);
         code = cast1<FMT>(w, s, amax, sat);
         p.q[r * cols + c] = (uint8_t)code;
       }
@@ -243,18 +269,18 @@ __global__ __launch_bounds__(256) void adamw_transpose_kernel(AdamWLaunch p) {
 
 // ------------------------------------------------------------------ host launcher
 
-template <bool GBF16, int FMT>
+template <bool GBF16, int FMT, bool APPLY = false>
 static hipError_t launch_adamw_t(const AdamWLaunch& a, hipStream_t stream) {
   if (a.qt) {
     const dim3 grid((unsigned)((a.cols + 127) / 128), (unsigned)((a.rows + 127) / 128));
-    hipLaunchKernelGGL((adamw_transpose_kernel<GBF16, FMT>), grid, dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((adamw_transpose_kernel<GBF16, FMT, APPLY>), grid, dim3(256), 0, stream, a);
   } else {
     const int64_t pieces = (a.rows * a.cols + 15) / 16;
     const dim3 grid((unsigned)((pieces + 255) / 256));
     if (a.q)
-      hipLaunchKernelGGL((adamw_kernel<GBF16, FMT, true>), grid, dim3(256), 0, stream, a);
+      hipLaunchKernelGGL((adamw_kernel<GBF16, FMT, true, APPLY>), grid, dim3(256), 0, stream, a);
     else
-      hipLaunchKernelGGL((adamw_kernel<GBF16, FMT, false>), grid, dim3(256), 0, stream, a);
+      hipLaunchKernelGGL((adamw_kernel<GBF16, FMT, false, APPLY>), grid, dim3(256), 0, stream, a);
   }
   return hipGetLastError();
 }
@@ -266,6 +292,14 @@ hipError_t launch_adamw(const AdamWLaunch& a, hipStream_t stream) {
                           : launch_adamw_t<true, kE5M2>(a, stream);
   return a.fmt == kE4M3 ? launch_adamw_t<false, kE4M3>(a, stream)
                         : launch_adamw_t<false, kE5M2>(a, stream);
+}
+
+hipError_t launch_muon_apply(const AdamWLaunch& a, hipStream_t stream) {
+  if (a.g_bf16)
+    return a.fmt == kE4M3 ? launch_adamw_t<true, kE4M3, true>(a, stream)
+                          : launch_adamw_t<true, kE5M2, true>(a, stream);
+  return a.fmt == kE4M3 ? launch_adamw_t<false, kE4M3, true>(a, stream)
+                        : launch_adamw_t<false, kE5M2, true>(a, stream);
 }
 
 }  // namespace fp8ds

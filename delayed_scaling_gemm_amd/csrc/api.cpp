@@ -1396,4 +1396,103 @@ int fp8ds_rmsnorm_sandwich_bwd(const void* dy, fp8ds_dtype xt, int64_t lddy, con
   return hip_status(e, who);
 }
 
+// ------------------------------------------------------------------ Muon
+
+static int check_muon_shape(const char* who, int64_t rows, int64_t cols) {
+  const int64_t side = int64_t(1) << 19;  // byte offsets within a tile of pair rows stay below 2^30
+  if (rows < 0 || cols < 0 || rows > side || cols > side || rows * cols > (int64_t(1) << 34))
+    return fail(FP8DS_ERR_SHAPE, "%s: bad shape %lld x %lld", who, (long long)rows, (long long)cols);
+  return FP8DS_OK;
+}
+
+int64_t fp8ds_muon_workspace(int64_t rows, int64_t cols) {
+  if (check_muon_shape("fp8ds_muon_workspace", rows, cols)) return FP8DS_ERR_SHAPE;
+  ok();
+  return fp8ds::muon_workspace(rows, cols);
+}
+
+int fp8ds_muon_direction(const void* g, fp8ds_dtype gt, float* momentum, int64_t rows, int64_t cols,
+                         float mu, int nesterov, float grad_scale, const float* grad_coef,
+                         const float* grad_amax, int steps, const float* coefs, float eps, void* o,
+                         fp8ds_dtype ot, void* workspace, int64_t workspace_bytes,
+                         hipStream_t stream) {
+  const char* who = "fp8ds_muon_direction";
+  if (!valid_dtype(gt) || !valid_dtype(ot)) return fail(FP8DS_ERR_ENUM, "%s: bad dtype", who);
+  if (int e = check_muon_shape(who, rows, cols)) return e;
+  if (!(mu >= 0.0f && mu < 1.0f) || !(std::isfinite(grad_scale) && grad_scale > 0.0f) ||
+      !(std::isfinite(eps) && eps > 0.0f) || steps < 1 || steps > FP8DS_MUON_MAX_STEPS)
+    return fail(FP8DS_ERR_VALUE, "%s: need 0 <= mu < 1, finite grad_scale > 0, finite eps > 0 and 1 to "
+                "%d steps", who, FP8DS_MUON_MAX_STEPS);
+  float c[3 * FP8DS_MUON_MAX_STEPS];
+  static const float kUsual[3] = {3.4445f, -4.7750f, 2.0315f};
+  for (int i = 0; i < 3 * steps; ++i) {
+    c[i] = coefs ? coefs[i] : kUsual[i % 3];
+    if (!std::isfinite(c[i])) return fail(FP8DS_ERR_VALUE, "%s: coefs[%d] is not finite", who, i);
+  }
+  if (reinterpret_cast<uintptr_t>(grad_coef) % 4 || reinterpret_cast<uintptr_t>(grad_amax) % 4)
+    return fail(FP8DS_ERR_ALIGN, "%s: grad_coef and grad_amax are fp32", who);
+  if (rows == 0 || cols == 0) return ok();
+  if (!g || !o) return fail(FP8DS_ERR_NULL, "%s: g and o are required", who);
+  if (!aligned16(g) || !aligned16(momentum) || !aligned16(o))
+    return fail(FP8DS_ERR_ALIGN, "%s: g, momentum and o must be 16-byte aligned", who);
+  const int64_t need = fp8ds::muon_workspace(rows, cols);
+  if (!workspace || workspace_bytes < need)
+    return fail(workspace ? FP8DS_ERR_SHAPE : FP8DS_ERR_NULL, "%s: workspace of %lld bytes, %lld "
+                "needed", who, (long long)(workspace ? workspace_bytes : 0), (long long)need);
+  if (!aligned16(workspace))
+    return fail(FP8DS_ERR_ALIGN, "%s: workspace not 16-byte aligned", who);
+  fp8ds::MuonLaunch q = {};
+  q.g = g; q.g_bf16 = gt == FP8DS_BF16;
+  q.momentum = momentum;
+  q.rows = rows; q.cols = cols;
+  q.mu = mu; q.nesterov = nesterov != 0;
+  q.grad_scale = grad_scale; q.grad_coef = grad_coef; q.grad_amax = grad_amax;
+  q.steps = steps; q.coefs = c; q.eps = eps;
+  q.o = o; q.o_bf16 = ot == FP8DS_BF16;
+  q.workspace = workspace;
+  return hip_status(fp8ds::launch_muon_direction(q, stream), who);
+}
+
+int fp8ds_muon_apply(float* w, const void* o, fp8ds_dtype ot, int64_t rows, int64_t cols, float lr,
+                     float weight_decay, float adjust, const float* grad_amax, fp8ds_format fmt,
+                     const float* scale, uint8_t* q, uint8_t* q_t, float* scale_used, float* amax,
+                     uint64_t* sat_count, hipStream_t stream) {
+#pragma clang fp contract(off)
+  const char* who = "fp8ds_muon_apply";
+  if (!valid_dtype(ot)) return fail(FP8DS_ERR_ENUM, "%s: bad dtype %d", who, (int)ot);
+  if (rows < 0 || cols < 0 || (cols > 0 && rows > kMaxElems / cols))
+    return fail(FP8DS_ERR_SHAPE, "%s: bad shape %lld x %lld", who, (long long)rows, (long long)cols);
+  if (!(std::isfinite(lr) && std::isfinite(weight_decay) && std::isfinite(adjust)))
+    return fail(FP8DS_ERR_VALUE, "%s: lr, weight_decay and adjust must be finite", who);
+  const bool cast = scale != nullptr;
+  if (cast && !valid_fmt(fmt)) return fail(FP8DS_ERR_ENUM, "%s: bad format %d", who, (int)fmt);
+  if (!cast && (q || q_t || scale_used || amax || sat_count))
+    return fail(FP8DS_ERR_NULL, "%s: q, q_t, scale_used, amax and sat_count need scale", who);
+  if (reinterpret_cast<uintptr_t>(grad_amax) % 4 || reinterpret_cast<uintptr_t>(scale) % 4 ||
+      reinterpret_cast<uintptr_t>(scale_used) % 4 || reinterpret_cast<uintptr_t>(amax) % 4 ||
+      reinterpret_cast<uintptr_t>(sat_count) % 8)
+    return fail(FP8DS_ERR_ALIGN, "%s: scalars are not aligned to their type", who);
+  const int64_t n = rows * cols;
+  if (n == 0)
+    return scale_used ? hip_status(fp8ds::launch_prologue(1, scale, scale_used, nullptr, nullptr,
+                                                          stream), who)
+                      : ok();
+  if (!w || !o) return fail(FP8DS_ERR_NULL, "%s: w and o are required", who);
+  if (cast && !q) return fail(FP8DS_ERR_NULL, "%s: q is null", who);
+  if (!aligned16(w) || !aligned16(o) || !aligned16(q) || !aligned16(q_t))
+    return fail(FP8DS_ERR_ALIGN, "%s: w, o, q and q_t must be 16-byte aligned", who);
+  if (q_t && too_many_tiles(rows, cols))
+    return fail(FP8DS_ERR_SHAPE, "%s: a transposed copy supports at most %d rows and 2^31 - 128 "
+                "columns", who, 65535 * 128);
+  if (n > (int64_t(1) << 35))  // 4096 elements a workgroup, fewer than 2^32 threads in a grid
+    return fail(FP8DS_ERR_SHAPE, "%s: more than 2^35 elements", who);
+  fp8ds::AdamWConsts c = {};
+  c.decay = (float)(1.0 - (double)lr * (double)weight_decay);
+  c.step_size = (float)((double)lr * (double)adjust);
+  c.grad_scale = 1.0f;
+  fp8ds::AdamWLaunch a{w, o, ot == FP8DS_BF16, nullptr, nullptr, rows, cols, c, grad_amax, (int)fmt,
+                       scale, q, q_t, amax, sat_count, nullptr, scale_used};
+  return hip_status(fp8ds::launch_muon_apply(a, stream), who);
+}
+
 }  // extern "C"

@@ -63,8 +63,33 @@ struct AdamWLaunch {
   float* amax;             // or null; reset by launch_prologue
   uint64_t* sat;           // or null; reset by launch_prologue
   const float* grad_coef = nullptr;  // or null: device factor that multiplies c.grad_scale
+  float* scale_used = nullptr;       // launch_muon_apply: or null
 };
 hipError_t launch_adamw(const AdamWLaunch& a, hipStream_t stream);
+// w = c.decay w - c.step_size g and the cast of the new weights; amax and sat are combined into,
+// scale_used is written; m and v are not used.
+hipError_t launch_muon_apply(const AdamWLaunch& a, hipStream_t stream);
+
+// Muon's direction: momentum, then Newton-Schulz steps on the normalised update.
+struct MuonLaunch {
+  const void* g;           // [rows][cols], contiguous, 16-byte aligned
+  bool g_bf16;
+  float* momentum;         // or null
+  int64_t rows, cols;
+  float mu;
+  bool nesterov;
+  float grad_scale;
+  const float* grad_coef;  // or null
+  const float* grad_amax;  // or null: a non-finite value skips the update
+  int steps;
+  const float* coefs;      // host [steps][3]
+  float eps;
+  void* o;                 // [rows][cols], contiguous, 16-byte aligned
+  bool o_bf16;
+  void* workspace;         // muon_workspace bytes
+};
+int64_t muon_workspace(int64_t rows, int64_t cols);
+hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream);
 
 // Current scaling with one scale per row of a [rows x cols] matrix: q, scale[rows],
 // scale_inv[rows] (or null), amax[rows] (or null).

@@ -851,6 +851,59 @@ int fp8ds_rmsnorm_sandwich_bwd(const void* dy, fp8ds_dtype xt, int64_t lddy, con
                                int64_t ldq, float* scale_used, float* amax, uint64_t* sat_count,
                                hipStream_t stream);
 
+/*
+ * fp8ds_muon_direction -- Muon's update of one matrix: momentum, then Newton-Schulz steps that bring
+ * the update's singular values near 1.
+ *   g' = g * fl32(grad_scale * (*grad_coef)),   m = mu m + g'
+ *   U = g' + mu m (nesterov) or m;  U = g' without a momentum
+ *   X = U / (|U|_F + eps)                 the norm in 64 bits
+ *   per step, with its own a, b, c:  A = X X^T,  X = a X + (b A + c A A) X
+ *   o = X                                 (on the transpose where rows > cols)
+ * m and U: each operation one fp32 rounding.  The products take their operands as pairs of BF16 (16
+ * significant bits), three products of each, with fp32 sums: o is within about 1e-4 (relative, of
+ * the whole matrix) of the iteration in 64 bits, also where few directions dominate g.
+ *   g          device [rows x cols] of gt, contiguous.
+ *   momentum   device or NULL: [rows x cols] fp32, contiguous, updated in place (zeros before the
+ *              first step).
+ *   rows,cols  0 .. 2^19 each, 2^34 elements at most.    mu  in [0, 1).
+ *   grad_scale finite, > 0.    grad_coef  device or NULL: a further factor (fp8ds_grad_norm's coef).
+ *   grad_amax  device or NULL: if it holds an infinity or NaN (fp8ds_grad_norm's norm), momentum and o
+ *              are left as they are.
+ *   steps      1 .. FP8DS_MUON_MAX_STEPS (5 as a rule).
+ *   coefs      HOST [steps][3] or NULL: a, b, c of each step, finite; NULL: 3.4445, -4.7750, 2.0315.
+ *   eps        finite, > 0 (1e-7 as a rule).  A zero U gives a zero o.
+ *   o          device [rows x cols] of ot, contiguous; must not overlap the others.
+ *   workspace  device, at least fp8ds_muon_workspace(rows, cols) bytes; its contents need no
+ *              preparation and do not matter afterwards.  About 12 bytes for each element and 8 for
+ *              each of min(rows, cols)^2.
+ * g, momentum, o and workspace 16-byte aligned.  No atomics: the same inputs give the same bits.
+ */
+#define FP8DS_MUON_MAX_STEPS 16
+int64_t fp8ds_muon_workspace(int64_t rows, int64_t cols);
+int fp8ds_muon_direction(const void* g, fp8ds_dtype gt, float* momentum, int64_t rows, int64_t cols,
+                         float mu, int nesterov, float grad_scale, const float* grad_coef,
+                         const float* grad_amax, int steps, const float* coefs, float eps, void* o,
+                         fp8ds_dtype ot, void* workspace, int64_t workspace_bytes,
+                         hipStream_t stream);
+
+/*
+ * fp8ds_muon_apply -- the weights' step along a direction, and the FP8 copy of the new weights:
+ *   w = decay w - step o,   decay = 1 - lr weight_decay,  step = lr adjust
+ * each operation one fp32 rounding, decay and step in float64 and rounded once.  adjust is the
+ * update's size for lr 1, e.g. 0.2 sqrt(max(rows, cols)) for updates of AdamW's size.  With a scale
+ * the new weights are cast as fp8ds_adamw casts them, except that amax and sat_count are COMBINED
+ * INTO, as fp8ds_cast_acc does.
+ *   w          device [rows x cols] fp32, updated in place.     o  device [rows x cols] of ot.
+ *   lr, weight_decay, adjust  finite.
+ *   grad_amax  device or NULL: if not finite, w stays; the FP8 copy is made all the same.
+ *   fmt, scale, q, q_t, scale_used, amax, sat_count  as fp8ds_adamw.
+ * At most 2^35 elements; w, o, q and q_t contiguous and 16-byte aligned.
+ */
+int fp8ds_muon_apply(float* w, const void* o, fp8ds_dtype ot, int64_t rows, int64_t cols, float lr,
+                     float weight_decay, float adjust, const float* grad_amax, fp8ds_format fmt,
+                     const float* scale, uint8_t* q, uint8_t* q_t, float* scale_used, float* amax,
+                     uint64_t* sat_count, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
