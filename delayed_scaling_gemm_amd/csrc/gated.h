@@ -15,26 +15,35 @@ namespace fp8ds {
 
 constexpr int kActSilu = 0, kActGelu = 1;
 
+// Both sigmoids' argument is g (k1 + k3 g^2), k3 = 0 for SiLU: no branch on the activation.  e1 and e3
+// are -k1 and -k3 over ln 2.
+struct Act {
+  float k1, k33, e1, e3;
+  __device__ __forceinline__ explicit Act(int act) {
+    constexpr float kL = 1.4426950408889634f;
+    constexpr float kG = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+    k1 = act == kActGelu ? kG : 1.0f;
+    k33 = act == kActGelu ? 3.0f * 0.044715f * kG : 0.0f;
+    e1 = act == kActGelu ? -kG * kL : -kL;
+    e3 = act == kActGelu ? -0.044715f * kG * kL : 0.0f;
+  }
+};
 struct ActValue {
   float a, d;  // act(g), act'(g)
 };
-// exp and the reciprocal are the hardware's, 1 ulp each: relative errors of a few 2^-24 (2^-24 |g|
-// where the sigmoid is small), far below the 8 or 16 bits that the result is rounded to.
+// exp2 and the reciprocal are the hardware's, 1 ulp each: relative errors of a few 2^-24 (2^-24 |g|
+// where the sigmoid is small), far below the 8 or 16 bits that the result is rounded to.  g^2 is
+// kept finite, so that k3 = 0 and a sigmoid of 0 make zeros of it; NaN stays NaN.
 template <bool GRAD>
-__device__ __forceinline__ ActValue act_value(float g, int act) {
-  float z = g, dz = 1.0f;
-  if (act == kActGelu) {
-    constexpr float k = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-    const float g2 = g * g;
-    z = k * (g + 0.044715f * g2 * g);
-    if (GRAD) dz = k * (1.0f + 0.134145f * g2);
-  }
-  const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+__device__ __forceinline__ ActValue act_value(float g, const Act& c) {
+  const float g2 = fminf(g * g, 1e37f);
+  const float e = __builtin_amdgcn_exp2f(g * __builtin_fmaf(c.e3, g2, c.e1));
+  const float p = __builtin_amdgcn_rcpf(1.0f + e);
   ActValue v;
   v.a = g * p;
-  if (GRAD) {
-    const float t = p * (1.0f - p);
-    v.d = p + (t > 0.0f ? g * t * dz : t);  // (t is 0 where g dz may be infinite; NaN stays)
+  if constexpr (GRAD) {
+    const float t = __builtin_fmaf(-p, p, p);
+    v.d = __builtin_fmaf(g * t, __builtin_fmaf(c.k33, g2, c.k1), p);
   }
   return v;
 }
@@ -98,7 +107,7 @@ __device__ __forceinline__ void gated_store8(uint8_t* p, int n, const u32x2& c) 
 }
 
 // Eight codes of v s (the converts round as the definition does inside the format's range, which the
-// clamp makes of every value but NaN; `nan`: some value of the eight is one).
+// clamp makes of every value but NaN; `nan`: some value of the eight may be one).
 __device__ __forceinline__ u32x2 gated_codes(const float (&v)[8], float s, bool e5m2, bool nan,
                                              uint32_t& sat, bool want) {
   const float top = e5m2 ? FmtTraits<kE5M2>::kMax : FmtTraits<kE4M3>::kMax;
@@ -164,7 +173,9 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& p, const v16f (&
   const bool e5m2 = p.fmt == kE5M2;
   const float s = p.q ? *p.scale : 1.0f;
   if (p.scale_used && blockIdx.x == 0 && tid == 0) *p.scale_used = s;
+  float top = 0.0f;
   uint32_t amax = 0, sat = 0;
+  const Act act(p.act);
   const bool want_sat = p.sat != nullptr;
   // two buffers of 32 rows, used in turn
   uint8_t* st = (wave < 2 ? stage0 : stage1) + (wave & 1) * (BM * kRowBytes);
@@ -239,7 +250,7 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& p, const v16f (&
           take(uc, g);
           take(WTO + uc, u);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) out[0][k] = act_value<false>(g[k], p.act).a * u[k];
+          for (int k = 0; k < 8; ++k) out[0][k] = act_value<false>(g[k], act).a * u[k];
           if (m >= M || left <= 0) continue;
           if (p.gu) {
             gated_store16<AL>(p.gu + m * p.ldgu + n, left, g);
@@ -253,22 +264,28 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& p, const v16f (&
           for (int k = 0; k < 8; ++k) {
             const float g = k & 1 ? bf16_hi(now[t][0][k >> 1]) : bf16_lo(now[t][0][k >> 1]);
             const float u = k & 1 ? bf16_hi(now[t][1][k >> 1]) : bf16_lo(now[t][1][k >> 1]);
-            const ActValue a = act_value<true>(g, p.act);
+            const ActValue a = act_value<true>(g, act);
             out[0][k] = da[k] * u * a.d;
             out[1][k] = da[k] * a.a;
           }
         }
 #pragma unroll
         for (int h = 0; h < NO; ++h) {
-          uint32_t mine = 0;
+          // the largest magnitude as a float, which passes over NaN; 0 times a value that is not
+          // finite tells of one
+          float odd = 0.0f;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             if (!AL && k >= left) out[h][k] = 0.0f;
-            mine = max(mine, __float_as_uint(out[h][k]) & 0x7FFFFFFFu);
+            odd = __builtin_fmaf(out[h][k], 0.0f, odd);
+            top = fmaxf(top, fabsf(out[h][k]));
           }
-          amax = max(amax, mine);
+          if (odd != 0.0f) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) amax = max(amax, __float_as_uint(out[h][k]) & 0x7FFFFFFFu);
+          }
           if (p.q) {
-            const u32x2 c = gated_codes(out[h], s, e5m2, mine > 0x7F800000u, sat, want_sat);
+            const u32x2 c = gated_codes(out[h], s, e5m2, odd != 0.0f, sat, want_sat);
             gated_store8<AL>(p.q + m * p.ldq + n + h * F, left, c);
           }
           if (p.y) {
@@ -286,7 +303,7 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& p, const v16f (&
   else if constexpr (BM < 256) rows(std::false_type{});
 
   if (p.amax || p.sat) {  // four waves: one word each
-    amax = wave_max_u32(amax);
+    amax = wave_max_u32(max(amax, __float_as_uint(top)));
     if (lane == 0) red[wave] = amax;
     if (p.sat && __any(sat != 0)) {
       sat = wave_sum_u32(sat);

@@ -369,9 +369,9 @@ struct GatedProblem {
   uint64_t* sat;         // or null: added to
   bool vec;              // rows of gu, y and q at 16 bytes, F a multiple of 16
 };
-// Forward for at most kGatedFewRows rows (exact datapath).
-constexpr int64_t kGatedFewRows = 32;
-hipError_t launch_gated_few(const GatedProblem& p, hipStream_t stream);
+// Forward for at most kGatedFewRows rows (exact datapath), both operands below 2^31 bytes.
+constexpr int64_t kGatedFewRows = 16;
+hipError_t launch_gated_few(const GatedProblem& p, int num_cus, hipStream_t stream);
 hipError_t launch_gated_fwd(const GatedProblem& p, bool exact, int num_cus, hipStream_t stream);
 hipError_t launch_gated_bwd(const GatedProblem& p, int fa, bool exact, int num_cus,
                             hipStream_t stream);

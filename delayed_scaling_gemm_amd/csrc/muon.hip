@@ -95,7 +95,7 @@ __device__ __forceinline__ float update1(const MuonIn& p, float g, float m) {
   return p.nesterov ? g + p.mu * m : m;
 }
 
-constexpr int kParts = 256;  // partial sums of squares, one per workgroup
+constexpr int kParts = 2048;  // partial sums of squares, one per workgroup
 
 // m, and sum U^2 in 64 bits: a share of the elements per workgroup, four at a time.
 template <bool GBF>
@@ -155,7 +155,8 @@ __global__ __launch_bounds__(256) void muon_split_kernel(MuonIn p, const double*
                                                          int64_t ldxt) {
   __shared__ float tile[64][65];
   __shared__ double red[4];
-  double sum = (int)threadIdx.x < nparts ? parts[threadIdx.x] : 0.0;
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < nparts; i += 256) sum += parts[i];
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(256) void muon_split_kernel(MuonIn p, const double*
 
 // ------------------------------------------------------------------ products
 
-constexpr int kGram = 0;   // A = P P^T, symmetric
+constexpr int kGram = 0;   // C = P Q^T where that is symmetric: X X^T, products of polynomials of one A
 constexpr int kPart = 1;   // the same over a share of K, fp32 sums for muon_join_kernel
 constexpr int kPoly = 2;   // B = a I + b A + c A A, symmetric (P is A)
 constexpr int kStep = 3;   // X = P Q^T and its transpose (P is B, Q is X^T)
@@ -485,8 +486,9 @@ int tile_for(int64_t m, int64_t n, bool sym, int most) {
 struct MuonPlan {
   bool tall;            // more rows than columns: X is the transpose
   int64_t m, n;         // padded sizes of X
-  int step_tile, sym_tile, shares;
-  int64_t parts, x, xt[2], a, b, share, total;  // offsets in the workspace, bytes
+  int step_tile, sym_tile, shares, share_stages;
+  bool grouped;         // steps in groups (launch_muon_direction)
+  int64_t parts, x, xt[2], a, t, b[3], share, total;  // offsets in the workspace, bytes
 };
 MuonPlan muon_plan(int64_t rows, int64_t cols) {
   MuonPlan p = {};
@@ -497,10 +499,13 @@ MuonPlan muon_plan(int64_t rows, int64_t cols) {
   p.m = pad(m);
   p.n = pad(n);
   p.sym_tile = tile_for(p.m, p.m, true, p.step_tile);
-  // X X^T with few tiles and a long K: shares of K of 16 stages and more, each CU one or two
+  // X X^T with few tiles and a long K: shares of K, of 16 stages and more, up to a tile per CU.
+  // (Shares that even out 136 tiles over 256 CUs, 3 or 7, were no faster at 4096 x 14336: the CUs
+  // that work run at a higher clock.)
   const int64_t st = p.m / p.sym_tile, pairs = st * (st + 1) / 2, stages = p.n / 32;
   int64_t shares = 1;
-  while (pairs * shares * 2 <= kCus && stages % (shares * 4) == 0 && stages / (shares * 2) >= 16) shares *= 2;
+  while (pairs * shares * 2 <= kCus && stages / (shares * 2) >= 16) shares *= 2;
+  p.share_stages = (int)((stages + 2 * shares - 1) / (2 * shares) * 2);  // (the last may be shorter)
   p.shares = (int)shares;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -512,8 +517,14 @@ MuonPlan muon_plan(int64_t rows, int64_t cols) {
   p.x = take(p.m * p.n * 4);
   p.xt[0] = take(p.m * p.n * 4);
   p.xt[1] = take(p.m * p.n * 4);
+  p.grouped = 2 * p.n >= 3 * p.m;
   p.a = take(p.m * p.m * 4);
-  p.b = take(p.m * p.m * 4);
+  p.b[0] = take(p.m * p.m * 4);
+  if (p.grouped) {
+    p.t = take(p.m * p.m * 4);
+    p.b[1] = take(p.m * p.m * 4);
+    p.b[2] = take(p.m * p.m * 4);
+  }
   p.share = take(p.shares > 1 ? p.shares * pairs * p.sym_tile * p.sym_tile * 4 : 0);
   p.total = at;
   return p;
@@ -549,7 +560,7 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
 
-  uint8_t *x = ws + pl.x, *a = ws + pl.a, *b = ws + pl.b;
+  uint8_t *x = ws + pl.x, *a = ws + pl.a;
   const int64_t ldx = pl.n * 4, ldxt = pl.m * 4;  // bytes of a pair row of X, of X^T, A and B
   // the matrix as it lies is X, or X's transpose
   uint8_t *as_is = pl.tall ? ws + pl.xt[0] : x, *turned = pl.tall ? x : ws + pl.xt[0];
@@ -565,10 +576,21 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
   e = hipGetLastError();
 
   const int st = (int)(pl.m / pl.sym_tile), pairs = st * (st + 1) / 2;
-  for (int k = 0; e == hipSuccess && k < q.steps; ++k) {
-    const uint8_t* xt = ws + pl.xt[k & 1];
+  // C = P Q^T over m columns, symmetric
+  auto symmetric = [&](auto mode_tag, const uint8_t* P, const uint8_t* Q, uint8_t* C, const float* abc) {
     NsArgs g = {};
-    g.P = g.Q = x; g.ld = (int)ldx; g.nk = (int)(pl.n / 32) / pl.shares;
+    g.P = P; g.Q = Q; g.ld = (int)ldxt; g.nk = (int)(pl.m / 32);
+    g.C = g.Ct = C; g.ldc = g.ldct = ldxt;
+    if (abc) { g.a = abc[0]; g.b = abc[1]; g.c = abc[2]; }
+    if (e == hipSuccess) e = launch_product<decltype(mode_tag)::value>(g, pl.sym_tile, pairs, 1, stream);
+  };
+  const std::integral_constant<int, kGram> product{};
+  const std::integral_constant<int, kPoly> poly{};
+  int turn = 0;  // of the two transposes
+  for (int k = 0; e == hipSuccess && k < q.steps; ++turn) {
+    const uint8_t* xt = ws + pl.xt[turn & 1];
+    NsArgs g = {};
+    g.P = g.Q = x; g.ld = (int)ldx; g.nk = pl.share_stages;
     g.C = g.Ct = a; g.ldc = g.ldct = ldxt;
     if (pl.shares > 1) {
       g.part = reinterpret_cast<float*>(ws + pl.share);
@@ -586,18 +608,31 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
     } else {
       e = launch_product<kGram>(g, pl.sym_tile, pairs, 1, stream);
     }
+    // A group of steps is one product with X: with B_0 of A_0 = X X^T, the next step's A_1 is
+    // B_0 A_0 B_0, and X becomes (B_1 B_0) X.  Every factor is a polynomial of A_0, so all of them
+    // are symmetric and commute.
+    const int size = !pl.grouped ? 1 : q.steps - k < (k ? 3 : 2) ? q.steps - k : (k ? 3 : 2);
+    uint8_t *const b0 = ws + pl.b[0], *const b1 = ws + pl.b[1], *const b2 = ws + pl.b[2];
+    uint8_t *last = b0, *sofar = b0;  // B of the last step, the product of all
+    symmetric(poly, a, a, b0, q.coefs + 3 * k);
+    for (int i = 1; i < size; ++i) {  // (three steps at most: b0 and then b1 are free again by then)
+      symmetric(product, last, a, ws + pl.t, nullptr);
+      symmetric(product, ws + pl.t, last, a, nullptr);
+      uint8_t *fresh = i == 1 ? b1 : b0, *joined = i == 1 ? b2 : b1;
+      symmetric(poly, a, a, fresh, q.coefs + 3 * (k + i));
+      symmetric(product, fresh, sofar, joined, nullptr);
+      last = fresh;
+      sofar = joined;
+    }
+    k += size;
     if (e != hipSuccess) return e;
-    g.P = g.Q = a; g.ld = (int)ldxt; g.nk = (int)(pl.m / 32);
-    g.C = g.Ct = b;
-    g.a = q.coefs[3 * k]; g.b = q.coefs[3 * k + 1]; g.c = q.coefs[3 * k + 2];
-    e = launch_product<kPoly>(g, pl.sym_tile, pairs, 1, stream);
-    if (e != hipSuccess) return e;
-    g.P = b; g.Q = xt;
+    g = NsArgs{};
+    g.P = sofar; g.Q = xt; g.ld = (int)ldxt; g.nk = (int)(pl.m / 32);
     g.tiles_m = (int)(pl.m / pl.step_tile); g.tiles_n = (int)(pl.n / pl.step_tile);
     const unsigned tiles = (unsigned)(g.tiles_m * g.tiles_n);
-    if (k + 1 < q.steps) {
+    if (k < q.steps) {
       g.C = x; g.ldc = ldx;
-      g.Ct = ws + pl.xt[(k + 1) & 1]; g.ldct = ldxt;
+      g.Ct = ws + pl.xt[(turn + 1) & 1]; g.ldct = ldxt;
       e = launch_product<kStep>(g, pl.step_tile, tiles, 1, stream);
     } else {
       g.o = q.o; g.o_bf16 = q.o_bf16 ? 1 : 0; g.o_t = pl.tall ? 1 : 0;

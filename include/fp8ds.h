@@ -742,11 +742,11 @@ typedef enum { FP8DS_ACT_SILU = 0, FP8DS_ACT_GELU = 1 } fp8ds_act;
  *   scale      device or NULL (then q, scale_used and sat_count must be NULL): the delayed scale.
  *   q          device [M x F] codes of fmt, rows ldq apart.
  *   amax       device or NULL: of y, with or without a scale.
- *   mma        as fp8ds_gemm; up to 32 rows run exact either way.
+ *   mma        as fp8ds_gemm; up to 16 rows run exact either way.
  *   M, F, K    >= 0, any size (ceil(M/128) ceil(F/64) < 2^23).  Rows of A and B 16-byte aligned; gu
  *              and y aligned to their elements (fastest with rows at 16 bytes, F a multiple of 16).
  * At least one of gu, y and q.  Outputs must not overlap each other or the operands.  M or F of 0:
- * nothing but *scale_used is written.  Up to 32 rows read every weight once.
+ * nothing but *scale_used is written.  Up to 16 rows read every weight once.
  */
 int fp8ds_gated_gemm(int64_t M, int64_t F, int64_t K, const uint8_t* A, fp8ds_format fa, int64_t lda,
                      const float* scale_a, const uint8_t* B, fp8ds_format fb, int64_t ldb,
