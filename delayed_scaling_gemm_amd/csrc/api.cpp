@@ -1129,9 +1129,8 @@ static int gated_common(const char* who, bool bwd, int64_t M, int64_t F, int64_t
       lda > kMaxElems / (M + 1) || ldb > kMaxElems / (wrows + 1) || ldgu > kMaxElems / (M + 1) ||
       ldy > kMaxElems / (M + 1) || ldq > kMaxElems / (M + 1))
     return fail(FP8DS_ERR_SHAPE, "%s: bad leading dimension", who);
-  if (!scale != !q) return fail(FP8DS_ERR_NULL, "%s: scale and q go together", who);
-  if (!scale && (scale_used || sat_count))
-    return fail(FP8DS_ERR_NULL, "%s: scale_used and sat_count need a scale", who);
+  if (!scale && (q || scale_used || sat_count))
+    return fail(FP8DS_ERR_NULL, "%s: q, scale_used and sat_count need a scale", who);
   if (reinterpret_cast<uintptr_t>(scale_a) % 4 || reinterpret_cast<uintptr_t>(scale_b) % 4 ||
       reinterpret_cast<uintptr_t>(scale) % 4 || reinterpret_cast<uintptr_t>(scale_used) % 4 ||
       reinterpret_cast<uintptr_t>(amax) % 4 || reinterpret_cast<uintptr_t>(sat_count) % 8)
@@ -1143,6 +1142,7 @@ static int gated_common(const char* who, bool bwd, int64_t M, int64_t F, int64_t
   }
   if (!scale_a || !scale_b || (K > 0 && (!A || !B)))
     return fail(FP8DS_ERR_NULL, "%s: the operands and their scales are required", who);
+  if (scale && !q) return fail(FP8DS_ERR_NULL, "%s: q is null", who);
   if (bwd ? !gu : (!gu && !y && !q))
     return fail(FP8DS_ERR_NULL, bwd ? "%s: gu is required" : "%s: no output", who);
   if (bwd && !y && !q) return fail(FP8DS_ERR_NULL, "%s: no output", who);

@@ -44,9 +44,11 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void gated_few_kernel(GatedArgs 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, kq = (lane >> 4) * 32;
   const int F = (int)p.N, K = (int)p.K, ldb = (int)p.ldb;
-  // (offsets below 2^31: the launcher sees to that; what is past the last row reads as zeros)
-  const __amdgpu_buffer_rsrc_t bw = byte_rsrc(p.B, (2 * p.N - 1) * p.ldb + K);
-  const __amdgpu_buffer_rsrc_t bx = byte_rsrc(p.A, (p.M - 1) * p.lda + K);
+  // (offsets below 2^31: the launcher sees to that; what is past the last row reads as zeros.  Rows
+  // start at 16 bytes, so the piece that K ends in is read whole and masked.)
+  const int64_t row = (p.K + 15) / 16 * 16;
+  const __amdgpu_buffer_rsrc_t bw = byte_rsrc(p.B, (2 * p.N - 1) * p.ldb + row);
+  const __amdgpu_buffer_rsrc_t bx = byte_rsrc(p.A, (p.M - 1) * p.lda + row);
   const int vx = r * (int)p.lda + kq;
   // K in equal chunks of a step each
   const int segs = (K + 127) / 128, chunks = segs == 0 ? 1 : (segs + NW * NS - 1) / (NW * NS);
