@@ -153,8 +153,8 @@ def _declare(lib):
     lib.fp8ds_muon_workspace.restype = i64
     lib.fp8ds_muon_workspace.argtypes = [i64, i64]
     lib.fp8ds_muon_direction.restype = i32
-    lib.fp8ds_muon_direction.argtypes = [vp, i32, vp, i64, i64, f, i32, f, vp, vp, i32, vp, f, vp, i32,
-                                         vp, i64, vp]
+    lib.fp8ds_muon_direction.argtypes = [vp, i32, i64, vp, i64, i64, f, i32, f, vp, vp, i32, vp, f, vp,
+                                         i32, i64, vp, i64, vp]
     lib.fp8ds_muon_apply.restype = i32
     lib.fp8ds_muon_apply.argtypes = [vp, vp, i32, i64, i64, f, f, f, vp, i32, vp, vp, vp, vp, vp, vp,
                                      vp]
@@ -1110,7 +1110,7 @@ def fp8ds_muon_direction(g, o, workspace, momentum=None, mu=0.95, nesterov=True,
                          eps=1e-7, grad_scale=1.0, grad_coef=None, grad_amax=None, stream=None):
     """Muon's direction ``o`` [rows, cols] (bf16 or fp32) of the gradient ``g`` (bf16 or fp32): the
     ``momentum`` (fp32, in place) takes it in, and ``steps`` Newton-Schulz steps with ``coefs``
-    (``steps`` triples; None: the usual quintic) orthogonalise the update.  ``grad_coef`` and
+    (``steps`` triples; None: the usual quintic) orthogonalise the update.  Rows of g and o may be strided.  ``grad_coef`` and
     ``grad_amax`` as :func:`fp8ds_adamw`.  ``workspace``: uint8, :func:`fp8ds_muon_workspace`
     bytes."""
     import torch
@@ -1125,11 +1125,12 @@ def fp8ds_muon_direction(g, o, workspace, momentum=None, mu=0.95, nesterov=True,
         if len(flat) != 3 * steps:
             raise ValueError(f"coefs: {len(flat)} numbers for {steps} steps of three")
         cp = _host_array("f", flat)
-    _call("fp8ds_muon_direction", _vec(g, "g", high, n), high[g.dtype],
-          _vec(momentum, "momentum", f32, n), rows, cols, float(mu), int(bool(nesterov)),
-          float(grad_scale), _vec(grad_coef, "grad_coef", f32, 1),
-          _vec(grad_amax, "grad_amax", f32, 1), int(steps), cp, float(eps), _vec(o, "o", high, n),
-          high[o.dtype], _vec(workspace, "workspace", (torch.uint8,), 0),
+    gp, ldg = _rows2d(g, "g", high, rows, cols)
+    op, ldo = _rows2d(o, "o", high, rows, cols)
+    _call("fp8ds_muon_direction", gp, high[g.dtype], ldg, _vec(momentum, "momentum", f32, n), rows, cols,
+          float(mu), int(bool(nesterov)), float(grad_scale), _vec(grad_coef, "grad_coef", f32, 1),
+          _vec(grad_amax, "grad_amax", f32, 1), int(steps), cp, float(eps), op, high[o.dtype], ldo,
+          _vec(workspace, "workspace", (torch.uint8,), 0),
           0 if workspace is None else workspace.numel(), _stream(stream))
 
 

@@ -1411,11 +1411,11 @@ int64_t fp8ds_muon_workspace(int64_t rows, int64_t cols) {
   return fp8ds::muon_workspace(rows, cols);
 }
 
-int fp8ds_muon_direction(const void* g, fp8ds_dtype gt, float* momentum, int64_t rows, int64_t cols,
-                         float mu, int nesterov, float grad_scale, const float* grad_coef,
-                         const float* grad_amax, int steps, const float* coefs, float eps, void* o,
-                         fp8ds_dtype ot, void* workspace, int64_t workspace_bytes,
-                         hipStream_t stream) {
+int fp8ds_muon_direction(const void* g, fp8ds_dtype gt, int64_t ldg, float* momentum, int64_t rows,
+                         int64_t cols, float mu, int nesterov, float grad_scale,
+                         const float* grad_coef, const float* grad_amax, int steps,
+                         const float* coefs, float eps, void* o, fp8ds_dtype ot, int64_t ldo,
+                         void* workspace, int64_t workspace_bytes, hipStream_t stream) {
   const char* who = "fp8ds_muon_direction";
   if (!valid_dtype(gt) || !valid_dtype(ot)) return fail(FP8DS_ERR_ENUM, "%s: bad dtype", who);
   if (int e = check_muon_shape(who, rows, cols)) return e;
@@ -1433,8 +1433,12 @@ int fp8ds_muon_direction(const void* g, fp8ds_dtype gt, float* momentum, int64_t
     return fail(FP8DS_ERR_ALIGN, "%s: grad_coef and grad_amax are fp32", who);
   if (rows == 0 || cols == 0) return ok();
   if (!g || !o) return fail(FP8DS_ERR_NULL, "%s: g and o are required", who);
-  if (!aligned16(g) || !aligned16(momentum) || !aligned16(o))
-    return fail(FP8DS_ERR_ALIGN, "%s: g, momentum and o must be 16-byte aligned", who);
+  if (ldg < cols || ldo < cols || ldg > kMaxElems / rows || ldo > kMaxElems / rows)
+    return fail(FP8DS_ERR_SHAPE, "%s: bad leading dimension", who);
+  if (reinterpret_cast<uintptr_t>(g) % (gt == FP8DS_BF16 ? 2 : 4) ||
+      reinterpret_cast<uintptr_t>(o) % (ot == FP8DS_BF16 ? 2 : 4) || !aligned16(momentum))
+    return fail(FP8DS_ERR_ALIGN, "%s: g and o must be aligned to their elements, momentum to 16 bytes",
+                who);
   const int64_t need = fp8ds::muon_workspace(rows, cols);
   if (!workspace || workspace_bytes < need)
     return fail(workspace ? FP8DS_ERR_SHAPE : FP8DS_ERR_NULL, "%s: workspace of %lld bytes, %lld "
@@ -1442,13 +1446,13 @@ int fp8ds_muon_direction(const void* g, fp8ds_dtype gt, float* momentum, int64_t
   if (!aligned16(workspace))
     return fail(FP8DS_ERR_ALIGN, "%s: workspace not 16-byte aligned", who);
   fp8ds::MuonLaunch q = {};
-  q.g = g; q.g_bf16 = gt == FP8DS_BF16;
+  q.g = g; q.g_bf16 = gt == FP8DS_BF16; q.ldg = ldg;
   q.momentum = momentum;
   q.rows = rows; q.cols = cols;
   q.mu = mu; q.nesterov = nesterov != 0;
   q.grad_scale = grad_scale; q.grad_coef = grad_coef; q.grad_amax = grad_amax;
   q.steps = steps; q.coefs = c; q.eps = eps;
-  q.o = o; q.o_bf16 = ot == FP8DS_BF16;
+  q.o = o; q.o_bf16 = ot == FP8DS_BF16; q.ldo = ldo;
   q.workspace = workspace;
   return hip_status(fp8ds::launch_muon_direction(q, stream), who);
 }

@@ -72,9 +72,10 @@ hipError_t launch_muon_apply(const AdamWLaunch& a, hipStream_t stream);
 
 // Muon's direction: momentum, then Newton-Schulz steps on the normalised update.
 struct MuonLaunch {
-  const void* g;           // [rows][cols], contiguous, 16-byte aligned
+  const void* g;           // [rows][ldg]
   bool g_bf16;
-  float* momentum;         // or null
+  int64_t ldg;
+  float* momentum;         // or null: [rows][cols], contiguous, 16-byte aligned
   int64_t rows, cols;
   float mu;
   bool nesterov;
@@ -84,8 +85,9 @@ struct MuonLaunch {
   int steps;
   const float* coefs;      // host [steps][3]
   float eps;
-  void* o;                 // [rows][cols], contiguous, 16-byte aligned
+  void* o;                 // [rows][ldo]
   bool o_bf16;
+  int64_t ldo;
   void* workspace;         // muon_workspace bytes
 };
 int64_t muon_workspace(int64_t rows, int64_t cols);

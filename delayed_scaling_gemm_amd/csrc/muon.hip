@@ -75,13 +75,18 @@ __device__ __forceinline__ bool skipped(const float* amax) {
 struct MuonIn {
   const void* g;
   float* m;              // or null
-  int64_t n;             // rows * cols
+  int64_t n, cols, ldg;  // elements; row length and distance of g's rows
+  int vec;               // four elements of g at a time
   float mu;
   int nesterov;
   float grad_scale;
   const float* grad_coef;  // or null
   const float* grad_amax;  // or null
 };
+// Place of element i in g.
+__device__ __forceinline__ int64_t grad_at(const MuonIn& p, int64_t i) {
+  return p.ldg == p.cols ? i : i / p.cols * p.ldg + i % p.cols;
+}
 template <bool GBF>
 __device__ __forceinline__ float grad1(const MuonIn& p, int64_t i, float s) {
   if constexpr (GBF)
@@ -116,13 +121,14 @@ __global__ __launch_bounds__(256) void muon_sum_kernel(MuonIn p, double* __restr
       sum = fma((double)u, (double)u, sum);
     };
     for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x * 4; i < p.n; i += step) {
-      if (i + 4 <= p.n) {
+      if (p.vec && i + 4 <= p.n) {
         float g[4], m[4] = {0.f, 0.f, 0.f, 0.f};
+        const int64_t at = grad_at(p, i);
         if constexpr (GBF) {
-          const u32x2 d = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p.g) + i);
+          const u32x2 d = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p.g) + at);
           g[0] = bf16_lo(d.x); g[1] = bf16_hi(d.x); g[2] = bf16_lo(d.y); g[3] = bf16_hi(d.y);
         } else {
-          const f32x4_t d = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p.g) + i);
+          const f32x4_t d = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p.g) + at);
 #pragma unroll
           for (int k = 0; k < 4; ++k) g[k] = d[k];
         }
@@ -134,7 +140,8 @@ __global__ __launch_bounds__(256) void muon_sum_kernel(MuonIn p, double* __restr
 #pragma unroll
         for (int k = 0; k < 4; ++k) one(i + k, g[k] * s, m[k]);
       } else {
-        for (int64_t k = i; k < p.n; ++k) one(k, grad1<GBF>(p, k, s), p.m ? p.m[k] : 0.f);
+        for (int64_t k = i; k < p.n && k < i + 4; ++k)
+          one(k, grad1<GBF>(p, grad_at(p, k), s), p.m ? p.m[k] : 0.f);
       }
     }
   }
@@ -174,7 +181,7 @@ __global__ __launch_bounds__(256) void muon_split_kernel(MuonIn p, const double*
       float v = 0.0f;
       if (r0 + r < rows && c0 + c + k < cols) {
         const int64_t at = (r0 + r) * cols + c0 + c + k;
-        const float g = grad1<GBF>(p, at, s);
+        const float g = grad1<GBF>(p, (r0 + r) * p.ldg + c0 + c + k, s);
         v = (p.m ? update1(p, g, p.m[at]) : g) * inv;
       }
       tile[r][c + k] = v;
@@ -202,9 +209,10 @@ struct NsArgs {
   int64_t ldc, ldct;
   float a, b, c;
   float* part;           // kPart: [share][tile pair][T][T]
-  void* o;               // kLast: [orows][ocols]
+  void* o;               // kLast: [orows][ldo]
   int o_bf16, o_t;       // o_t: o holds the transpose
-  int64_t orows, ocols;
+  int64_t orows, ocols, ldo;
+  int o_vec;             // eight elements at a time
   const float* skip;
 };
 
@@ -379,10 +387,10 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
       });
     } else if constexpr (MODE == kLast) {
       const int64_t R = p.orows, C = p.ocols;
-      const bool vec = C % 8 == 0;
+      const bool vec = p.o_vec != 0;
       auto put = [&](int64_t row, int64_t c, const float (&v)[8]) {
         if (row >= R || c >= C) return;
-        const int64_t at = row * C + c;
+        const int64_t at = row * p.ldo + c;
         if (p.o_bf16) {
           const u32x4 d = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                            pack_bf16x2(v[6], v[7])};
@@ -550,8 +558,10 @@ int64_t muon_workspace(int64_t rows, int64_t cols) {
 hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
   const MuonPlan pl = muon_plan(q.rows, q.cols);
   uint8_t* ws = static_cast<uint8_t*>(q.workspace);
-  MuonIn in = {q.g, q.momentum, q.rows * q.cols, q.mu, q.nesterov ? 1 : 0, q.grad_scale, q.grad_coef,
-               q.grad_amax};
+  const bool gvec = reinterpret_cast<uintptr_t>(q.g) % 16 == 0 &&
+                    (q.ldg == q.cols || (q.ldg % 4 == 0 && q.cols % 4 == 0));
+  MuonIn in = {q.g, q.momentum, q.rows * q.cols, q.cols, q.ldg, gvec ? 1 : 0, q.mu, q.nesterov ? 1 : 0,
+               q.grad_scale, q.grad_coef, q.grad_amax};
   double* parts = reinterpret_cast<double*>(ws + pl.parts);
   const int64_t want = (in.n + 1023) / 1024;
   const int nparts = (int)(want < kParts ? want : kParts);
@@ -636,7 +646,9 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
       e = launch_product<kStep>(g, pl.step_tile, tiles, 1, stream);
     } else {
       g.o = q.o; g.o_bf16 = q.o_bf16 ? 1 : 0; g.o_t = pl.tall ? 1 : 0;
-      g.orows = q.rows; g.ocols = q.cols;
+      g.orows = q.rows; g.ocols = q.cols; g.ldo = q.ldo;
+      g.o_vec = q.cols % 8 == 0 && reinterpret_cast<uintptr_t>(q.o) % 16 == 0 &&
+                (q.ldo * (q.o_bf16 ? 2 : 4)) % 16 == 0;
       g.skip = q.grad_amax;
       e = launch_product<kLast>(g, pl.step_tile, tiles, 1, stream);
     }

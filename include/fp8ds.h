@@ -863,7 +863,7 @@ int fp8ds_rmsnorm_sandwich_bwd(const void* dy, fp8ds_dtype xt, int64_t lddy, con
  * significant bits), three products of each, with fp32 sums: o is 2e-5 to 7e-5 (relative, of the
  * whole matrix) from the iteration in 64 bits for Gaussian g, up to 1e-3 where the singular values
  * fall by orders of magnitude.
- *   g          device [rows x cols] of gt, contiguous.
+ *   g          device [rows x cols] of gt, rows ldg apart (a part of a stacked gradient, say).
  *   momentum   device or NULL: [rows x cols] fp32, contiguous, updated in place (zeros before the
  *              first step).
  *   rows,cols  0 .. 2^19 each, 2^34 elements at most.    mu  in [0, 1).
@@ -873,19 +873,20 @@ int fp8ds_rmsnorm_sandwich_bwd(const void* dy, fp8ds_dtype xt, int64_t lddy, con
  *   steps      1 .. FP8DS_MUON_MAX_STEPS (5 as a rule).
  *   coefs      HOST [steps][3] or NULL: a, b, c of each step, finite; NULL: 3.4445, -4.7750, 2.0315.
  *   eps        finite, > 0 (1e-7 as a rule).  A zero U gives a zero o.
- *   o          device [rows x cols] of ot, contiguous; must not overlap the others.
+ *   o          device [rows x cols] of ot, rows ldo apart; must not overlap the others.
  *   workspace  device, at least fp8ds_muon_workspace(rows, cols) bytes; its contents need no
  *              preparation and do not matter afterwards.  About 12 bytes for each element and 8 for
  *              each of min(rows, cols)^2.
- * g, momentum, o and workspace 16-byte aligned.  No atomics: the same inputs give the same bits.
+ * g and o aligned to their elements, momentum and workspace to 16 bytes.  No atomics: the same
+ * inputs give the same bits.
  */
 #define FP8DS_MUON_MAX_STEPS 16
 int64_t fp8ds_muon_workspace(int64_t rows, int64_t cols);
-int fp8ds_muon_direction(const void* g, fp8ds_dtype gt, float* momentum, int64_t rows, int64_t cols,
-                         float mu, int nesterov, float grad_scale, const float* grad_coef,
-                         const float* grad_amax, int steps, const float* coefs, float eps, void* o,
-                         fp8ds_dtype ot, void* workspace, int64_t workspace_bytes,
-                         hipStream_t stream);
+int fp8ds_muon_direction(const void* g, fp8ds_dtype gt, int64_t ldg, float* momentum, int64_t rows,
+                         int64_t cols, float mu, int nesterov, float grad_scale,
+                         const float* grad_coef, const float* grad_amax, int steps,
+                         const float* coefs, float eps, void* o, fp8ds_dtype ot, int64_t ldo,
+                         void* workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /*
  * fp8ds_muon_apply -- the weights' step along a direction, and the FP8 copy of the new weights:

@@ -140,19 +140,20 @@ def test_muon_refusals():
     assert L.fp8ds_muon_workspace(100, 200) == L.fp8ds_muon_workspace(200, 100)
     bad_coefs = (ctypes.c_float * 15)(*([1.0] * 14 + [NAN]))
 
-    def call(g=P, gt=1, m=P, rows=100, cols=200, mu=0.95, nest=1, gs=1.0, coef=None, am=None, steps=5,
-             coefs=None, eps=1e-7, o=P, ot=1, ws=P, n=need):
-        return L.fp8ds_muon_direction(g, gt, m, rows, cols, mu, nest, gs, coef, am, steps, coefs, eps, o, ot,
-                                      ws, n, None)
+    def call(g=P, gt=1, ldg=200, m=P, rows=100, cols=200, mu=0.95, nest=1, gs=1.0, coef=None, am=None,
+             steps=5, coefs=None, eps=1e-7, o=P, ot=1, ldo=200, ws=P, n=need):
+        return L.fp8ds_muon_direction(g, gt, ldg, m, rows, cols, mu, nest, gs, coef, am, steps, coefs, eps,
+                                      o, ot, ldo, ws, n, None)
 
     assert call(gt=2) == -3 and call(ot=-1) == -3
     assert call(rows=-1) == -2 and call(cols=1 << 20) == -2 and call(n=need - 1) == -2
+    assert call(ldg=199) == -2 and call(ldo=199) == -2
     for bad in (dict(mu=1.0), dict(mu=-0.1), dict(mu=NAN), dict(gs=0.0), dict(gs=INF), dict(eps=0.0),
                 dict(eps=NAN), dict(steps=0), dict(steps=17),
                 dict(coefs=ctypes.cast(bad_coefs, ctypes.c_void_p))):
         assert call(**bad) == -7, bad
     assert call(g=None) == -1 and call(o=None) == -1 and call(ws=None) == -1
-    for bad in (dict(g=P + 2), dict(m=P + 4), dict(o=P + 2), dict(ws=P + 8), dict(coef=P + 2), dict(am=P + 1)):
+    for bad in (dict(g=P + 1), dict(m=P + 4), dict(o=P + 2, ot=0), dict(ws=P + 8), dict(coef=P + 2), dict(am=P + 1)):
         assert call(**bad) == -4, bad
     assert call(rows=0, g=None, o=None, ws=None) == 0
 

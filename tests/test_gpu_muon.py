@@ -126,6 +126,20 @@ def test_momentum(gt, nesterov):
         assert far(o, e) <= bound
 
 
+@pytest.mark.parametrize("R,C", [(40, 96), (33, 50), (300, 77)])
+def test_strided_rows(R, C):
+    """Parts of stacked matrices; what lies beside o stays."""
+    for gt, pad in ((BF, 4), (F32, 3), (BF, C)):
+        g = matrix(R, C, "gauss").to(gt)
+        store = torch.full((R, C + pad), 1e30, device=DEV, dtype=gt)
+        store[:, pad:] = g
+        m, m2 = torch.ones(R, C, device=DEV), torch.ones(R, C, device=DEV)
+        o, p = torch.empty(R, C, device=DEV, dtype=BF), torch.full((R, C + pad), 9.0, device=DEV, dtype=BF)
+        dsg.fp8ds_muon_direction(g, o, work(R, C), momentum=m)
+        dsg.fp8ds_muon_direction(store[:, pad:], p[:, :C], work(R, C), momentum=m2)
+        assert torch.equal(m, m2) and torch.equal(p[:, :C], o) and (p[:, C:] == 9).all()
+
+
 def test_scale_free_and_extreme_magnitudes():
     R, C = 50, 90
     g, ws = matrix(R, C, "gauss"), work(R, C)
