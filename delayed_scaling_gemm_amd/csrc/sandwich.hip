@@ -21,40 +21,79 @@
 
 namespace fp8ds {
 
+// A row's last group, where it is not whole, is the row's last eight elements: the first 8 - n of
+// them are the group before's too, computed alike and stored twice with the same bits, and only left
+// out of the sums.  So a ragged row has no element that is loaded or stored by itself (each row
+// waited for those: 8000 x 6999 forward 412 us, so 109; backward 764, 263).  Groups past the row read the same eight, and
+// count for nothing.
+template <bool BF, bool AL>
+__device__ __forceinline__ void take8(const Raw8<BF>& r, int n, float (&v)[8]) {
+  unpack8<BF, AL>(r, AL ? n : 8, v);
+}
+template <bool AL>
+__device__ __forceinline__ void take_gamma(const Raw8<false>& r, bool bf, int n, float (&v)[8]) {
+  unpack_gamma<AL>(r, bf, AL ? n : 8, v);
+}
+// Aligned rows have whole groups only, and groups past the row are kept at zero (`held`: r may be
+// infinite); of others each element is asked whether it counts.
+template <bool AL>
+__device__ __forceinline__ float held(int n, float v) {
+  return !AL || n > 0 ? v : 0.0f;
+}
+template <bool AL>
+__device__ __forceinline__ float counted(int i, int n, float v) {
+  return AL || i >= 8 - n ? v : 0.0f;
+}
+
+// codes8 of a row's groups, each element counted once.
+template <int VPT, bool AL, typename Count>
+__device__ __forceinline__ void cast_row(const float (&v)[VPT][8], float s, bool e5m2, uint32_t amax,
+                                         bool live, const Count& count, u32x2 (&c)[VPT], uint32_t& sat,
+                                         bool want_sat) {
+  uint32_t unused = 0;
+  codes8(v, s, e5m2, amax, c, unused, false);
+  if (want_sat) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int n = live ? count(j) : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sat += i >= 8 - n ? sat1(v[j][i] * s, e5m2) : 0u;
+    }
+  }
+}
+
 // A row's output, from h in registers: y = (h rstd) gamma in place of h, stored and cast as MODE says
 // (norm.hip has these lines in its kernels: as a function they cost its longest rows 5 to 20 times the
 // spilled registers).
 // `given`: the per-tensor scale; amax and sat: this workgroup's, of kQTensor.
-// `col`, `count`: a group's first column and its elements, as the kernel has them.
-template <int TPR, int VPT, int MODE, bool AL, typename Args, typename Col, typename Count>
+// `at`, `count`: where a group is read and its elements, as the kernel has them.
+template <int TPR, int VPT, int MODE, bool AL, typename Args, typename At, typename Count>
 __device__ __forceinline__ void emit_row(const Args& p, const int64_t row, const bool live, const int t,
                                          const float rstd, float (&h)[VPT][8],
                                          const Raw8<false> (&rg)[VPT], const float given,
                                          const bool e5m2, uint32_t& amax, uint32_t& sat, uint32_t* red,
-                                         const Col& col, const Count& count) {
+                                         const At& at, const Count& count) {
   uint32_t mine = 0;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int n = live ? count(j) : 0;
     float g[8];
-    unpack_gamma<AL>(rg[j], p.gamma_bf16, n, g);
-    if (!AL && n > 0 && n < 8) {
-      if (p.gamma_bf16) load_tail<true>(p.gamma, col(j), n, g);
-      else load_tail<false>(p.gamma, col(j), n, g);
-    }
-    // (past the row h is 0, but r may be infinite)
+    take_gamma<AL>(rg[j], p.gamma_bf16, n, g);
+    // (past the row r may be infinite)
+    uint32_t most = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      h[j][k] = k < n ? (h[j][k] * rstd) * g[k] : 0.0f;
-      mine = max(mine, abs_bits(h[j][k]));
+      h[j][k] = (h[j][k] * rstd) * g[k];
+      most = max(most, abs_bits(h[j][k]));
     }
+    mine = max(mine, n > 0 ? most : 0u);
   }
   if (p.y) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       if (!live || count(j) == 0) continue;
-      if (p.y_bf16) store8<true, AL>(p.y, row * p.ldy + col(j), count(j), h[j]);
-      else store8<false, AL>(p.y, row * p.ldy + col(j), count(j), h[j]);
+      if (p.y_bf16) store8<true, AL>(p.y, row * p.ldy + at(j), 8, h[j]);
+      else store8<false, AL>(p.y, row * p.ldy + at(j), 8, h[j]);
     }
   }
   if constexpr (MODE == kQTensor || MODE == kQRow) {
@@ -71,12 +110,11 @@ __device__ __forceinline__ void emit_row(const Args& p, const int64_t row, const
         if (p.amax) p.amax[row] = __uint_as_float(a);
       }
     }
-    // (elements past the row are zeros: they add nothing to the count)
     u32x2 c[VPT];
-    codes8(h, s, e5m2, mine, c, sat, MODE == kQTensor && p.sat);
+    cast_row<VPT, AL>(h, s, e5m2, mine, live, count, c, sat, MODE == kQTensor && p.sat);
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
-      if (live && count(j) > 0) store_codes<AL>(p.q + row * p.ldq + col(j), count(j), c[j]);
+      if (live && count(j) > 0) store_codes<AL>(p.q + row * p.ldq + at(j), 8, c[j]);
   } else if constexpr (MODE == kQMx) {
     // a block of 32 is 4 consecutive lanes (AL only; C is a multiple of 32)
 #pragma unroll
@@ -86,7 +124,7 @@ __device__ __forceinline__ void emit_row(const Args& p, const int64_t row, const
       for (int k = 0; k < 8; ++k) a = max(a, abs_bits(h[j][k]));
       a = max(a, (uint32_t)__shfl_xor((int)a, 1));
       a = max(a, (uint32_t)__shfl_xor((int)a, 2));
-      const int64_t c0 = col(j);
+      const int64_t c0 = at(j);
       if (!live || count(j) == 0) continue;
       const uint32_t code = mx_code(a, p.fmt == kE2M1 ? 2u : e5m2 ? 15u : 8u);
       if ((t & 3) == 0) p.mx_scales[row * p.ldms + c0 / 32] = (uint8_t)code;
@@ -172,11 +210,7 @@ __device__ __forceinline__ void load_param(const void* g, bool bf, int t, int64_
   for (int j = 0; j < VPT; ++j) {
     const int64_t c = ((int64_t)t + TPR * j) * 8, left = C - c;
     const int n = left <= 0 ? 0 : AL || left >= 8 ? 8 : (int)left;
-    unpack_gamma<AL>(gamma8<AL>(g, bf, c + 8 <= C ? c : C - 8), bf, n, v[j]);
-    if (!AL && n > 0 && n < 8) {
-      if (bf) load_tail<true>(g, c, n, v[j]);
-      else load_tail<false>(g, c, n, v[j]);
-    }
+    take_gamma<AL>(gamma8<AL>(g, bf, c + 8 <= C ? c : C - 8), bf, n, v[j]);
   }
 }
 
@@ -263,36 +297,34 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_fwd_kernel(San
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int n = live ? count(j) : 0;
-      unpack8<XBF, AL>(now.x[j], n, h[j]);
-      if (!AL && n > 0 && n < 8) load_tail<XBF>(p.x, row * p.ldx + col(j), n, h[j]);
+      take8<XBF, AL>(now.x[j], n, h[j]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += h[j][i] * h[j][i];
+      for (int i = 0; i < 8; ++i) ss += counted<AL>(i, n, h[j][i] * h[j][i]);
     }
     ss = row_sum<TPR>(ss, reinterpret_cast<float*>(red));
     const float r1 = norm_rstd(ss, C, p.post_eps);
     if (p.post_rstd && live && t == 0) p.post_rstd[row] = r1;
     if constexpr (kFull) load_k<TPR, VPT, AL>(p, t, C, k);
+    const float r1t = r1 * now.t;
     ss = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int n = live ? count(j) : 0;
       float r[8];
-      unpack8<HBF, AL>(now.res[j], n, r);
-      if (!AL && n > 0 && n < 8) load_tail<HBF>(p.res, row * p.ldr + col(j), n, r);
+      take8<HBF, AL>(now.res[j], n, r);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        // (past the row x is 0, but r1 may be infinite)
-        h[j][i] = i < n ? r[i] + ((h[j][i] * r1) * k[j][i]) * now.t : 0.0f;
+        h[j][i] = held<AL>(n, __builtin_fmaf(h[j][i], r1t * k[j][i], r[i]));
         if constexpr (HBF) h[j][i] = bf16_round(h[j][i]);
-        ss += h[j][i] * h[j][i];
+        ss += counted<AL>(i, n, h[j][i] * h[j][i]);
       }
-      if (n > 0) store8<HBF, AL>(p.h, row * p.ldh + col(j), n, h[j]);
+      if (n > 0) store8<HBF, AL>(p.h, row * p.ldh + at(j), 8, h[j]);
     }
     ss = row_sum<TPR>(ss, reinterpret_cast<float*>(red));
     const float rstd = norm_rstd(ss, C, p.eps);
     if (p.rstd && live && t == 0) p.rstd[row] = rstd;
     if constexpr (kFull) load_gamma();
-    emit_row<TPR, VPT, MODE, AL>(p, row, live, t, rstd, h, rg, given, e5m2, amax, sat, red, col,
+    emit_row<TPR, VPT, MODE, AL>(p, row, live, t, rstd, h, rg, given, e5m2, amax, sat, red, at,
                                  count);
     if constexpr (kAhead) {
       now = next;
@@ -320,7 +352,8 @@ __global__ __launch_bounds__(1024) void sandwich_fwd_long_kernel(SandwichArgs p,
   const float tok = p.row_gate ? p.row_gate[row] : 1.0f;
   mine = 0.0;
   for (int64_t c = t; c < C; c += 1024) {
-    float v = load1<HBF>(p.res, row * p.ldr + c) + ((load1<XBF>(p.x, row * p.ldx + c) * r1) * k1(p, c)) * tok;
+    float v = __builtin_fmaf(load1<XBF>(p.x, row * p.ldx + c), (r1 * tok) * k1(p, c),
+                             load1<HBF>(p.res, row * p.ldr + c));
     if constexpr (HBF) v = bf16_round(v);
     store1<HBF>(p.h, row * p.ldh + c, v);
     mine = fma((double)v, (double)v, mine);
@@ -342,6 +375,11 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_bwd_kernel(San
   constexpr int RPB = NT / TPR;
   __shared__ uint32_t red[2 * (NT / 64)];
   __shared__ float part_lds[RPB > 1 ? TPR * VPT * 8 : 1];
+  // Rows of 8192 to 16384 columns, 1024 threads of 128 registers: the column sums are kept in LDS, the
+  // parameters read again for each row, dres and x only when h and dy have been taken (7404 x 9063 in
+  // 512 threads, all in registers: 1442 us, so 377; 4096 x 16384 526, 218).
+  constexpr bool kLean = TPR == 1024;
+  __shared__ float acc_lds[kLean ? 2 * TPR * VPT * 8 : 1];
   const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
   const int64_t C = p.cols;
   auto col = [&](int j) -> int64_t { return ((int64_t)t + TPR * j) * 8; };
@@ -356,40 +394,60 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_bwd_kernel(San
     s = *p.scale_in;
     if (p.scale_used && blockIdx.x == 0 && threadIdx.x == 0) *p.scale_used = s;
   }
-  float acc2[VPT][8], acc1[VPT][8];
+  float acc2[kLean ? 1 : VPT][8], acc1[kLean ? 1 : VPT][8];
+  auto sum2 = [&](int j, int i) -> float& {
+    if constexpr (kLean) return acc_lds[(j * 8 + i) * TPR + t];
+    else return acc2[j][i];
+  };
+  auto sum1 = [&](int j, int i) -> float& {
+    if constexpr (kLean) return acc_lds[((VPT + j) * 8 + i) * TPR + t];
+    else return acc1[j][i];
+  };
 #pragma unroll
   for (int j = 0; j < VPT; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc2[j][i] = acc1[j][i] = 0.0f;
+    for (int i = 0; i < 8; ++i) sum2(j, i) = sum1(j, i) = 0.0f;
   uint32_t amax = 0, sat = 0;
   struct RowData {
     Raw8<HBF> h[VPT], dr[VPT];
     Raw8<XBF> dy[VPT], x[VPT];
     float r1, r2, t;
   };
-  auto load_row = [&](int64_t row, RowData& d) {
+  auto load_first = [&](int64_t row, RowData& d) {
     row = row < p.rows ? row : p.rows - 1;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) d.h[j] = load8<HBF, AL>(p.h, row * p.ldh + at(j));
 #pragma unroll
     for (int j = 0; j < VPT; ++j) d.dy[j] = load8<XBF, AL>(p.dy, row * p.lddy + at(j));
+    d.r1 = p.post_rstd[row];
+    d.r2 = p.rstd[row];
+    d.t = p.row_gate ? p.row_gate[row] : 1.0f;
+  };
+  auto load_second = [&](int64_t row, RowData& d) {
+    row = row < p.rows ? row : p.rows - 1;
     if (p.dres) {
 #pragma unroll
       for (int j = 0; j < VPT; ++j) d.dr[j] = load8<HBF, AL>(p.dres, row * p.lddr + at(j));
     }
 #pragma unroll
     for (int j = 0; j < VPT; ++j) d.x[j] = load8<XBF, AL>(p.x, row * p.ldx + at(j));
-    d.r1 = p.post_rstd[row];
-    d.r2 = p.rstd[row];
-    d.t = p.row_gate ? p.row_gate[row] : 1.0f;
   };
-  float k[VPT][8];
-  load_k<TPR, VPT, AL>(p, t, C, k);
-  Raw8<false> rg[VPT];
+  auto load_row = [&](int64_t row, RowData& d) {
+    load_first(row, d);
+    if constexpr (!kLean) load_second(row, d);
+  };
+  float k[kLean ? 1 : VPT][8];
+  Raw8<false> rg[kLean ? 1 : VPT];
+  if constexpr (!kLean) {
+    load_k<TPR, VPT, AL>(p, t, C, k);
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) rg[j] = gamma8<AL>(p.gamma, p.gamma_bf16, at(j));
+    for (int j = 0; j < VPT; ++j) rg[j] = gamma8<AL>(p.gamma, p.gamma_bf16, at(j));
+  }
+  auto param8 = [&](const void* v, bool bf, int j, int n, float (&out)[8]) {
+    take_gamma<AL>(gamma8<AL>(v, bf, at(j)), bf, n, out);
+  };
   const int64_t step = (int64_t)gridDim.x * RPB;
-  constexpr bool kAhead = VPT * ((HBF ? 8 : 16) + (XBF ? 8 : 16)) <= 32;
+  constexpr bool kAhead = !kLean && VPT * ((HBF ? 8 : 16) + (XBF ? 8 : 16)) <= 32;
   RowData now;
   if constexpr (kAhead) load_row((int64_t)blockIdx.x * RPB + slot, now);
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < p.rows; r0 += step) {
@@ -404,23 +462,20 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_bwd_kernel(San
     for (int j = 0; j < VPT; ++j) {
       const int n = live ? count(j) : 0;
       float gm[8];
-      unpack8<HBF, AL>(now.h[j], n, xh[j]);
-      unpack8<XBF, AL>(now.dy[j], n, g[j]);
-      unpack_gamma<AL>(rg[j], p.gamma_bf16, n, gm);
-      if (!AL && n > 0 && n < 8) {
-        load_tail<HBF>(p.h, row * p.ldh + col(j), n, xh[j]);
-        load_tail<XBF>(p.dy, row * p.lddy + col(j), n, g[j]);
-        if (p.gamma_bf16) load_tail<true>(p.gamma, col(j), n, gm);
-        else load_tail<false>(p.gamma, col(j), n, gm);
-      }
+      take8<HBF, AL>(now.h[j], n, xh[j]);
+      take8<XBF, AL>(now.dy[j], n, g[j]);
+      if constexpr (kLean) param8(p.gamma, p.gamma_bf16, j, n, gm);
+      else take_gamma<AL>(rg[j], p.gamma_bf16, n, gm);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        xh[j][i] = i < n ? xh[j][i] * now.r2 : 0.0f;  // (r2 may be infinite)
-        acc2[j][i] += g[j][i] * xh[j][i];
+        xh[j][i] = held<AL>(n, xh[j][i] * now.r2);
+        // (an unaligned row past the end holds the last one's values)
+        sum2(j, i) += AL || n > 0 ? g[j][i] * xh[j][i] : 0.0f;
         g[j][i] *= gm[i];
-        dot += g[j][i] * xh[j][i];
+        dot += counted<AL>(i, n, g[j][i] * xh[j][i]);
       }
     }
+    if constexpr (kLean) load_second(row, now);
     const float mean2 = row_sum<TPR>(dot, reinterpret_cast<float*>(red)) / (float)C;
     // dh in place of g, the branch's xh in place of the stream's
     const float at1 = p.alpha * now.t;
@@ -430,21 +485,34 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_bwd_kernel(San
       const int n = live ? count(j) : 0;
       float dr[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
       if (p.dres) {
-        unpack8<HBF, AL>(now.dr[j], n, dr);
-        if (!AL && n > 0 && n < 8) load_tail<HBF>(p.dres, row * p.lddr + col(j), n, dr);
+        take8<HBF, AL>(now.dr[j], n, dr);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        g[j][i] = i < n ? now.r2 * (g[j][i] - xh[j][i] * mean2) + dr[i] : 0.0f;
-      if (n > 0) store8<HBF, AL>(p.dh, row * p.lddh + col(j), n, g[j]);
-      unpack8<XBF, AL>(now.x[j], n, xh[j]);
-      if (!AL && n > 0 && n < 8) load_tail<XBF>(p.x, row * p.ldx + col(j), n, xh[j]);
+        g[j][i] = held<AL>(n, now.r2 * (g[j][i] - xh[j][i] * mean2) + dr[i]);
+      if (n > 0) store8<HBF, AL>(p.dh, row * p.lddh + at(j), 8, g[j]);
+      take8<XBF, AL>(now.x[j], n, xh[j]);
+      float kj[8];
+      if constexpr (kLean) {
+        param8(p.post_gamma, p.post_gamma_bf16, j, n, kj);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) kj[i] *= p.alpha;
+        if (p.gate) {
+          float gt[8];
+          param8(p.gate, p.gate_bf16, j, n, gt);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) kj[i] *= gt[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) kj[i] = k[j][i];
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        xh[j][i] = i < n ? xh[j][i] * now.r1 : 0.0f;
-        acc1[j][i] += (at1 * g[j][i]) * xh[j][i];
-        g[j][i] = i < n ? g[j][i] * k[j][i] : 0.0f;
-        dot += g[j][i] * xh[j][i];
+        xh[j][i] = held<AL>(n, xh[j][i] * now.r1);
+        sum1(j, i) += AL || n > 0 ? (at1 * g[j][i]) * xh[j][i] : 0.0f;
+        g[j][i] *= kj[i];
+        dot += counted<AL>(i, n, g[j][i] * xh[j][i]);
       }
     }
     dot = row_sum<TPR>(dot, reinterpret_cast<float*>(red));
@@ -454,27 +522,29 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_bwd_kernel(San
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int n = live ? count(j) : 0;
+      uint32_t most = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        g[j][i] = i < n ? rt * (g[j][i] - xh[j][i] * mean1) : 0.0f;
-        mine = max(mine, abs_bits(g[j][i]));
+        g[j][i] = rt * (g[j][i] - xh[j][i] * mean1);
+        most = max(most, abs_bits(g[j][i]));
       }
-      if (p.dx && n > 0) store8<XBF, AL>(p.dx, row * p.lddx + col(j), n, g[j]);
+      mine = max(mine, n > 0 ? most : 0u);
+      if (p.dx && n > 0) store8<XBF, AL>(p.dx, row * p.lddx + at(j), 8, g[j]);
     }
     if (p.q) {
       amax = max(amax, mine);
       u32x2 c[VPT];
-      codes8(g, s, e5m2, mine, c, sat, p.sat != nullptr);
+      cast_row<VPT, AL>(g, s, e5m2, mine, live, count, c, sat, p.sat != nullptr);
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
-        if (live && count(j) > 0) store_codes<AL>(p.q + row * p.ldq + col(j), count(j), c[j]);
+        if (live && count(j) > 0) store_codes<AL>(p.q + row * p.ldq + at(j), 8, c[j]);
     }
     if constexpr (kAhead) now = next;
   }
   // partial rows: the slots of a workgroup one after the other
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    float (&acc)[VPT][8] = which ? acc1 : acc2;
+    auto acc = [&](int j, int i) { return which ? sum1(j, i) : sum2(j, i); };
     float* out = p.work + ((int64_t)which * gridDim.x + blockIdx.x) * C;
     if constexpr (RPB > 1) {
       for (int w = 0; w < RPB; ++w) {
@@ -484,7 +554,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_bwd_kernel(San
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               float* d = &part_lds[(j * 8 + i) * TPR + t];
-              *d = w == 0 ? acc[j][i] : *d + acc[j][i];
+              *d = w == 0 ? acc(j, i) : *d + acc(j, i);
             }
         }
         __syncthreads();
@@ -494,7 +564,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_bwd_kernel(San
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (i < count(j)) out[col(j) + i] = part_lds[(j * 8 + i) * TPR + t];
+            if (i >= 8 - count(j)) out[at(j) + i] = part_lds[(j * 8 + i) * TPR + t];
       }
       __syncthreads();
     } else {
@@ -502,7 +572,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_bwd_kernel(San
       for (int j = 0; j < VPT; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (i < count(j)) out[col(j) + i] = acc[j][i];
+          if (i >= 8 - count(j)) out[at(j) + i] = acc(j, i);
     }
   }
   if (p.q) commit(amax, sat, p.amax, p.sat, red);
@@ -648,7 +718,7 @@ static RowShape bwd_shape(int64_t cols) {
   const int64_t g = (cols + 7) / 8;
   if (cols < 8) return {1024, 0};
   if (g <= 1024) return row_shape(cols);
-  if (g <= 2048) return {512, 4};
+  if (g <= 2048) return {1024, 2};
   return {1024, 0};
 }
 
@@ -675,7 +745,7 @@ static hipError_t launch_bwd(const SandwichBwdArgs& a, RowShape sh, int parts, h
   FP8DS_NORM_CASE(256, 1)
   FP8DS_NORM_CASE(256, 2)
   FP8DS_NORM_CASE(256, 4)
-  FP8DS_NORM_CASE(512, 4)
+  FP8DS_NORM_CASE(1024, 2)
 #undef FP8DS_NORM_CASE
   hipLaunchKernelGGL((sandwich_bwd_long_kernel<XBF, HBF>), dim3((unsigned)parts), dim3(1024), 0,
                      stream, a);
