@@ -21,11 +21,13 @@
 
 namespace fp8ds {
 
-// A row's last group, where it is not whole, is the row's last eight elements: the first 8 - n of
-// them are the group before's too, computed alike and stored twice with the same bits, and only left
-// out of the sums.  So a ragged row has no element that is loaded or stored by itself (each row
-// waited for those: 8000 x 6999 forward 412 us, so 109; backward 764, 263).  Groups past the row read the same eight, and
-// count for nothing.
+// A row's last group, where it is not whole, is read as the row's last eight elements: the first 8 - n
+// of them are the group before's too and only left out of the sums, so a ragged row has no element that
+// is loaded by itself (each row waited for those: 8000 x 6999 forward 412 us, so 116; backward 764,
+// 282).  Those 8 - n are not stored either, nor in a maximum: where the output is an input's storage the
+// group before may have stored its own before this group's loads have come back (a barrier of a workgroup
+// does not wait for loads), so what is worked out for them may be anything.  Groups past the row read the
+// same eight, and count for nothing.
 template <bool BF, bool AL>
 __device__ __forceinline__ void take8(const Raw8<BF>& r, int n, float (&v)[8]) {
   unpack8<BF, AL>(r, AL ? n : 8, v);
@@ -43,6 +45,32 @@ __device__ __forceinline__ float held(int n, float v) {
 template <bool AL>
 __device__ __forceinline__ float counted(int i, int n, float v) {
   return AL || i >= 8 - n ? v : 0.0f;
+}
+
+// A group's own elements; i is where its eight stand (`at`).
+template <bool BF, bool AL>
+__device__ __forceinline__ void store_own(void* p, int64_t i, int n, const float (&v)[8]) {
+  if (AL || n == 8) {
+    store8<BF, AL>(p, i, 8, v);
+    return;
+  }
+#pragma unroll
+  for (int k = 1; k < 8; ++k)
+    if (k >= 8 - n) store1<BF>(p, i + k, v[k]);
+}
+template <bool AL>
+__device__ __forceinline__ void store_own_codes(uint8_t* p, int n, const u32x2& c) {
+  if (AL || n == 8) {
+    store_codes<AL>(p, 8, c);
+    return;
+  }
+#pragma unroll
+  for (int k = 1; k < 8; ++k)
+    if (k >= 8 - n) p[k] = (uint8_t)(c[k >> 2] >> (8 * (k & 3)));
+}
+template <bool AL>
+__device__ __forceinline__ uint32_t counted_bits(int i, int n, float v) {
+  return AL || i >= 8 - n ? abs_bits(v) : 0u;
 }
 
 // codes8 of a row's groups, each element counted once.
@@ -84,7 +112,7 @@ __device__ __forceinline__ void emit_row(const Args& p, const int64_t row, const
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       h[j][k] = (h[j][k] * rstd) * g[k];
-      most = max(most, abs_bits(h[j][k]));
+      most = max(most, counted_bits<AL>(k, n, h[j][k]));
     }
     mine = max(mine, n > 0 ? most : 0u);
   }
@@ -92,8 +120,8 @@ __device__ __forceinline__ void emit_row(const Args& p, const int64_t row, const
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       if (!live || count(j) == 0) continue;
-      if (p.y_bf16) store8<true, AL>(p.y, row * p.ldy + at(j), 8, h[j]);
-      else store8<false, AL>(p.y, row * p.ldy + at(j), 8, h[j]);
+      if (p.y_bf16) store_own<true, AL>(p.y, row * p.ldy + at(j), count(j), h[j]);
+      else store_own<false, AL>(p.y, row * p.ldy + at(j), count(j), h[j]);
     }
   }
   if constexpr (MODE == kQTensor || MODE == kQRow) {
@@ -114,7 +142,7 @@ __device__ __forceinline__ void emit_row(const Args& p, const int64_t row, const
     cast_row<VPT, AL>(h, s, e5m2, mine, live, count, c, sat, MODE == kQTensor && p.sat);
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
-      if (live && count(j) > 0) store_codes<AL>(p.q + row * p.ldq + at(j), 8, c[j]);
+      if (live && count(j) > 0) store_own_codes<AL>(p.q + row * p.ldq + at(j), count(j), c[j]);
   } else if constexpr (MODE == kQMx) {
     // a block of 32 is 4 consecutive lanes (AL only; C is a multiple of 32)
 #pragma unroll
@@ -318,7 +346,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_fwd_kernel(San
         if constexpr (HBF) h[j][i] = bf16_round(h[j][i]);
         ss += counted<AL>(i, n, h[j][i] * h[j][i]);
       }
-      if (n > 0) store8<HBF, AL>(p.h, row * p.ldh + at(j), 8, h[j]);
+      if (n > 0) store_own<HBF, AL>(p.h, row * p.ldh + at(j), n, h[j]);
     }
     ss = row_sum<TPR>(ss, reinterpret_cast<float*>(red));
     const float rstd = norm_rstd(ss, C, p.eps);
@@ -377,7 +405,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_bwd_kernel(San
   __shared__ float part_lds[RPB > 1 ? TPR * VPT * 8 : 1];
   // Rows of 8192 to 16384 columns, 1024 threads of 128 registers: the column sums are kept in LDS, the
   // parameters read again for each row, dres and x only when h and dy have been taken (7404 x 9063 in
-  // 512 threads, all in registers: 1442 us, so 377; 4096 x 16384 526, 218).
+  // 512 threads, all in registers: 1442 us, so 489; 4096 x 16384 526, 218).
   constexpr bool kLean = TPR == 1024;
   __shared__ float acc_lds[kLean ? 2 * TPR * VPT * 8 : 1];
   const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
@@ -490,7 +518,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_bwd_kernel(San
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         g[j][i] = held<AL>(n, now.r2 * (g[j][i] - xh[j][i] * mean2) + dr[i]);
-      if (n > 0) store8<HBF, AL>(p.dh, row * p.lddh + at(j), 8, g[j]);
+      if (n > 0) store_own<HBF, AL>(p.dh, row * p.lddh + at(j), n, g[j]);
       take8<XBF, AL>(now.x[j], n, xh[j]);
       float kj[8];
       if constexpr (kLean) {
@@ -526,10 +554,10 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_bwd_kernel(San
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         g[j][i] = rt * (g[j][i] - xh[j][i] * mean1);
-        most = max(most, abs_bits(g[j][i]));
+        most = max(most, counted_bits<AL>(i, n, g[j][i]));
       }
       mine = max(mine, n > 0 ? most : 0u);
-      if (p.dx && n > 0) store8<XBF, AL>(p.dx, row * p.lddx + at(j), 8, g[j]);
+      if (p.dx && n > 0) store_own<XBF, AL>(p.dx, row * p.lddx + at(j), n, g[j]);
     }
     if (p.q) {
       amax = max(amax, mine);
@@ -537,7 +565,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_bwd_kernel(San
       cast_row<VPT, AL>(g, s, e5m2, mine, live, count, c, sat, p.sat != nullptr);
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
-        if (live && count(j) > 0) store_codes<AL>(p.q + row * p.ldq + at(j), 8, c[j]);
+        if (live && count(j) > 0) store_own_codes<AL>(p.q + row * p.ldq + at(j), count(j), c[j]);
     }
     if constexpr (kAhead) now = next;
   }

@@ -342,3 +342,36 @@ def test_many_rows_go_round_the_grid():
     want, tol = backward64(dy, h, r2, d, r1, 0.5, None)
     for k in ("dgamma", "dpost_gamma", "dgate"):
         assert ((o[k].double() - want[k]).abs() <= tol[k]).all(), k
+
+
+@pytest.mark.parametrize("types", list(TYPES))
+@pytest.mark.parametrize("R,C", [(700, 33), (700, 777), (600, 2049), (300, 5003), (300, 9063)])
+def test_ragged_rows_in_place_are_the_others(R, C, types):
+    """Many ragged rows, every output that may lie over an input doing so: the same bits."""
+    d = inputs(R, C, types, True, True, seed=5)
+    h, r1, r2 = run_forward(d, 0.5)
+    over = d["res"].clone()
+    am, am2 = torch.zeros(1, device=DEV), torch.zeros(1, device=DEV)
+    s = torch.full((1,), 20.0, device=DEV)
+    q, q2 = (torch.empty(R, C, dtype=U8, device=DEV) for _ in range(2))
+    run_forward(d, 0.5, fmt=dsg.E4M3, scale=s, q=q, amax=am)
+    dsg.fp8ds_rmsnorm_sandwich(d["x"], d["pg"], EPS1, over, d["ga"], EPS2, over, alpha=0.5, gate=d["gate"],
+                               row_gate=d["t"], fmt=dsg.E4M3, scale=s, q=q2, amax=am2)
+    assert torch.equal(over, h) and torch.equal(q, q2) and torch.equal(am, am2)
+    g = torch.Generator(device=DEV).manual_seed(C)
+    dy = torch.randn(R, C, generator=g, device=DEV).to(d["x"].dtype)
+    dres = torch.randn(R, C, generator=g, device=DEV).to(h.dtype)
+    dx = torch.empty_like(dy)
+    am, am2 = torch.zeros(1, device=DEV), torch.zeros(1, device=DEV)
+    got = run_backward(d, h, r1, r2, dy, 0.5, dres, dx=dx, scale=s, q=q, amax=am)
+    dy2, d2 = dy.clone(), dres.clone()
+    o = {k: torch.empty_like(v) for k, v in got.items()}
+    ws = torch.empty(dsg.fp8ds_rmsnorm_sandwich_bwd_workspace(R, C), dtype=U8, device=DEV)
+    dsg.fp8ds_rmsnorm_sandwich_bwd(dy2, h, r2, d["ga"], d["x"], r1, d["pg"], d2, o["dgamma"],
+                                   o["dpost_gamma"], ws, alpha=0.5, gate=d["gate"], row_gate=d["t"],
+                                   dgate=o["dgate"], drow_gate=o["drow_gate"], dres=d2, dx=dy2, scale=s,
+                                   q=q2, amax=am2)
+    o["dh"] = d2
+    for name, v in got.items():
+        assert torch.equal(v, o[name]), name
+    assert torch.equal(dx, dy2) and torch.equal(q, q2) and torch.equal(am, am2)
