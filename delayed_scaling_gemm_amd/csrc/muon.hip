@@ -203,7 +203,7 @@ constexpr int kLast = 4;   // the result
 struct NsArgs {
   const uint8_t *P, *Q;  // pair matrices of the same K
   int ld;                // bytes of a row of both
-  int nk;                // stages of 32 columns of a share (even)
+  int nk;                // stages of 32 columns of a share (a multiple of 4, but for the whole of K)
   int tiles_m, tiles_n;
   uint8_t *C, *Ct;       // pair matrices: the result and its transpose
   int64_t ldc, ldct;
@@ -224,9 +224,15 @@ __device__ __forceinline__ void pair_of(int i, int& tm, int& tn) {
   tn = i - tm * (tm + 1) / 2;
 }
 
-template <int T, int GM, int GN, int MODE>
+// NBUF stages in LDS.  Two where a CU has a tile of 256 x 256, or two of 128 x 128 that hide each
+// other's loads; four where it has one small tile, whose stage is shorter than a load takes
+// (916 x 2368: 387 us with two, 231 with four and the accumulators below).
+template <int T, int GM, int GN, int NBUF, int MODE>
 __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
   constexpr int NW = GM * GN, WM = T / GM, WN = T / GN, MI = WM / 32, NI = WN / 32;
+  // a block of its own gets an accumulator for each of its three products: they need not wait for
+  // one another
+  constexpr int NA = MI * NI == 1 ? 3 : 1;
   constexpr bool SYM = MODE == kGram || MODE == kPart || MODE == kPoly;
   constexpr int kA = T * 128, kBuf = 2 * kA;
   // the waves' sums on their way out, 32 rows of fp32 each, take the stages' place
@@ -234,6 +240,8 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
   static_assert(kOutWaves * 2 >= NW, "two stages hold every wave's part");
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[kBuf];
   __shared__ __attribute__((aligned(1024))) uint8_t lds1[kBuf];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds2[NBUF == 4 ? kBuf : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds3[NBUF == 4 ? kBuf : 16];
   if (MODE == kLast && skipped(p.skip)) return;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int r = lane & 31, h = lane >> 5;
@@ -256,13 +264,17 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int l = 0; l < 2; ++l) of[s][l] = chunk_off<128>(r, 4 * l + 2 * s + h);
-  v16f acc[MI][NI];
+  v16f acc[MI][NI], more[2];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NI; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+  if constexpr (NA == 3) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) more[0][e] = more[1][e] = 0.0f;
+  }
 
   auto issue = [&](int k, uint8_t* dst) {  // (zeros past the last stage)
     la.issue((share + k) * 128, p.ld, dst);
@@ -290,22 +302,24 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < NI; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+        for (int j = 0; j < NI; ++j) {
+          v16f& c = NA == 3 && q < 2 ? more[q] : acc[i][j];
+          c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
               __builtin_bit_cast(v8bf, fb[s][j][q == 0 ? 1 : 0]),
-              __builtin_bit_cast(v8bf, fa[s][i][q == 1 ? 1 : 0]), acc[i][j], 0, 0, 0);
+              __builtin_bit_cast(v8bf, fa[s][i][q == 1 ? 1 : 0]), c, 0, 0, 0);
+        }
   };
   using std::integral_constant;
   constexpr integral_constant<int, 0> k0th{};
   constexpr integral_constant<int, 1> k1st{};
   // Stage k from its barrier on: a step's fragments are read while the step before it is
-  // multiplied, so the previous stage's second step comes first here; the next stage's loads go
-  // into the buffer that this barrier freed.
+  // multiplied, so the previous stage's second step comes first here; the loads of stage
+  // k + NBUF - 1 go into the buffer that this barrier freed.
   constexpr int kMf = 3 * MI * NI, kReads = 2 * (MI + NI);
   auto stage = [&](int k, const uint8_t* rd, uint8_t* wr) {
-    stage_barrier<0>();
+    stage_barrier<(NBUF - 2) * kLoads>();  // all but the loads of later stages have arrived
     frags(rd, k0th);
-    issue(k + 1, wr);
+    issue(k + NBUF - 1, wr);
     mfmas(k1st);
     frags(rd, k1st);
     mfmas(k0th);
@@ -319,12 +333,29 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
 #pragma unroll
     for (int j = 0; j < NI; ++j) fb[1][j][l] = u32x4{0u, 0u, 0u, 0u};
   }
+  // (a last turn is filled up with stages of zeros: a row ends with its last stage, and shares of K
+  // are whole turns)
   issue(0, lds0);
-  for (int k = 0; k < p.nk; k += 2) {
-    stage(k, lds0, lds1);
-    stage(k + 1, lds1, lds0);
+  if constexpr (NBUF == 2) {
+    for (int k = 0; k < p.nk; k += 2) {
+      stage(k, lds0, lds1);
+      stage(k + 1, lds1, lds0);
+    }
+  } else {
+    issue(1, lds1);
+    issue(2, lds2);
+    for (int k = 0; k < p.nk; k += 4) {
+      stage(k, lds0, lds3);
+      stage(k + 1, lds1, lds0);
+      stage(k + 2, lds2, lds1);
+      stage(k + 3, lds3, lds2);
+    }
   }
   mfmas(k1st);
+  if constexpr (NA == 3) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[0][0][e] += more[0][e] + more[1][e];
+  }
 
   // Out through LDS, 32 rows of a wave at a time in fp32, chunk c of 16 bytes of row r at
   // c ^ swz32(r): lane (r, h) holds, of block (i, j), row r and columns 8 q + 4 h + {0..3} in
@@ -513,7 +544,7 @@ MuonPlan muon_plan(int64_t rows, int64_t cols) {
   const int64_t st = p.m / p.sym_tile, pairs = st * (st + 1) / 2, stages = p.n / 32;
   int64_t shares = 1;
   while (pairs * shares * 2 <= kCus && stages / (shares * 2) >= 16) shares *= 2;
-  p.share_stages = (int)((stages + 2 * shares - 1) / (2 * shares) * 2);  // (the last may be shorter)
+  p.share_stages = (int)(shares == 1 ? stages : (stages + 4 * shares - 1) / (4 * shares) * 4);
   p.shares = (int)shares;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -541,11 +572,13 @@ MuonPlan muon_plan(int64_t rows, int64_t cols) {
 template <int MODE>
 hipError_t launch_product(const NsArgs& a, int tile, unsigned grid, unsigned shares, hipStream_t stream) {
   if (tile == 256)
-    hipLaunchKernelGGL((muon_gemm_kernel<256, 4, 2, MODE>), dim3(grid, shares), dim3(512), 0, stream, a);
+    hipLaunchKernelGGL((muon_gemm_kernel<256, 4, 2, 2, MODE>), dim3(grid, shares), dim3(512), 0, stream, a);
+  else if (tile == 128 && (int64_t)grid * shares > kCus)
+    hipLaunchKernelGGL((muon_gemm_kernel<128, 2, 2, 2, MODE>), dim3(grid, shares), dim3(256), 0, stream, a);
   else if (tile == 128)
-    hipLaunchKernelGGL((muon_gemm_kernel<128, 2, 2, MODE>), dim3(grid, shares), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((muon_gemm_kernel<128, 2, 2, 4, MODE>), dim3(grid, shares), dim3(256), 0, stream, a);
   else
-    hipLaunchKernelGGL((muon_gemm_kernel<64, 2, 2, MODE>), dim3(grid, shares), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((muon_gemm_kernel<64, 2, 2, 4, MODE>), dim3(grid, shares), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
