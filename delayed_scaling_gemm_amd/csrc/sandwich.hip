@@ -280,9 +280,12 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_fwd_kernel(San
     const int64_t left = C - col(j);
     return left <= 0 ? 0 : AL || left >= 8 ? 8 : (int)left;
   };
+  // Rows of more than 16384 columns: parameters again for each row and group, the stream's group
+  // when x has been taken (4096 x 20480: 463 us with all of them held, 278).
+  constexpr bool kFull = TPR == 1024 && VPT == 4;
   struct RowData {
     Raw8<XBF> x[VPT];
-    Raw8<HBF> res[VPT];
+    Raw8<HBF> res[kFull ? 1 : VPT];
     float t;
   };
   // a row's loads; rows past the end read the last one, and are not used
@@ -290,16 +293,17 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_fwd_kernel(San
     row = row < p.rows ? row : p.rows - 1;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) d.x[j] = load8<XBF, AL>(p.x, row * p.ldx + at(j));
+    if constexpr (!kFull) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) d.res[j] = load8<HBF, AL>(p.res, row * p.ldr + at(j));
+      for (int j = 0; j < VPT; ++j) d.res[j] = load8<HBF, AL>(p.res, row * p.ldr + at(j));
+    }
     d.t = p.row_gate ? p.row_gate[row] : 1.0f;
   };
   const int64_t step = (int64_t)gridDim.x * RPB;
-  constexpr bool kFull = TPR == 1024 && VPT == 4;  // (parameters again for each row: norm.hip)
   constexpr bool kAhead = !kFull && VPT * (XBF ? 4 : 8) + VPT * (HBF ? 4 : 8) <= 32;
   RowData now;
   load_row((int64_t)blockIdx.x * RPB + slot, now);
-  float k[VPT][8];
+  float k[kFull ? 1 : VPT][8];
   Raw8<false> rg[VPT];
   auto load_gamma = [&] {
 #pragma unroll
@@ -332,17 +336,29 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_fwd_kernel(San
     ss = row_sum<TPR>(ss, reinterpret_cast<float*>(red));
     const float r1 = norm_rstd(ss, C, p.post_eps);
     if (p.post_rstd && live && t == 0) p.post_rstd[row] = r1;
-    if constexpr (kFull) load_k<TPR, VPT, AL>(p, t, C, k);
     const float r1t = r1 * now.t;
     ss = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int n = live ? count(j) : 0;
       float r[8];
-      take8<HBF, AL>(now.res[j], n, r);
+      const int jk = kFull ? 0 : j;
+      if constexpr (kFull) {
+        now.res[0] = load8<HBF, AL>(p.res, (live ? row : p.rows - 1) * p.ldr + at(j));
+        take_gamma<AL>(gamma8<AL>(p.post_gamma, p.post_gamma_bf16, at(j)), p.post_gamma_bf16, n, k[0]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) k[0][i] *= p.alpha;
+        if (p.gate) {
+          float g[8];
+          take_gamma<AL>(gamma8<AL>(p.gate, p.gate_bf16, at(j)), p.gate_bf16, n, g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) k[0][i] *= g[i];
+        }
+      }
+      take8<HBF, AL>(now.res[jk], n, r);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        h[j][i] = held<AL>(n, __builtin_fmaf(h[j][i], r1t * k[j][i], r[i]));
+        h[j][i] = held<AL>(n, __builtin_fmaf(h[j][i], r1t * k[jk][i], r[i]));
         if constexpr (HBF) h[j][i] = bf16_round(h[j][i]);
         ss += counted<AL>(i, n, h[j][i] * h[j][i]);
       }
