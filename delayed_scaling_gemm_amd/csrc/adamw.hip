@@ -235,6 +235,44 @@ __global__ __launch_bounds__(256) void adamw_transpose_kernel(AdamWLaunch p) {
     }
     __syncthreads();
     tile_store_qt<4>(tile, p.qt, rows, r0, c0, tid);
+  } else if constexpr (APPLY) {
+    // A ragged tile: a wave takes 64 consecutive elements of a row, eight such at a time so that their
+    // loads are in flight together, then 64 of a column (27 x 122: element by element along a thread's
+    // half row 27.5 us, so 8.5; 4097 x 4099: 925, 55).  A row's columns are stored XORed with
+    // 4 (row mod 32): a column's reads meet no bank twice.
+    auto slot = [&](int row, int col) { return row * T + (col ^ ((row & 31) << 2)); };
+    const int lane = tid & (T - 1), half = tid / T;
+#pragma unroll 1
+    for (int i = 0; i < T; i += 16) {
+      if (r0 + i >= rows) break;
+      float w[8], g[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t r = r0 + i + 2 * k + half, c = c0 + lane;
+        const int64_t o = r < rows && c < cols ? r * cols + c : 0;  // (others read the first, unused)
+        w[k] = p.w[o];
+        g[k] = GBF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.g)[o] << 16)
+                     : static_cast<const float*>(p.g)[o];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int tr = i + 2 * k + half;
+        const int64_t r = r0 + tr, c = c0 + lane;
+        if (r < rows && c < cols) {
+          const float wn = skip ? w[k] : apply_elem(w[k], g[k], p.c);
+          const uint8_t code = (uint8_t)cast1<FMT>(wn, s, amax, sat);
+          if (!skip) p.w[r * cols + c] = wn;
+          p.q[r * cols + c] = code;
+          tile[slot(tr, lane)] = code;
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int i = 0; i < T; i += 2) {
+      const int tc = i + half;
+      if (c0 + tc < cols && r0 + lane < rows) p.qt[(c0 + tc) * rows + r0 + lane] = tile[slot(lane, tc)];
+    }
   } else {
     const int tr = tid >> 1;        // row within the tile
     const int tc = (tid & 1) * 64;  // first of this thread's 64 columns
