@@ -230,7 +230,8 @@ __device__ __forceinline__ void pair_of(int i, int& tm, int& tn) {
 
 // NBUF stages in LDS.  Two where a CU has a tile of 256 x 256, or two of 128 x 128 that hide each
 // other's loads; four where it has one small tile, whose stage is shorter than a load takes
-// (916 x 2368: 387 us with two, 231 with four and the accumulators below).
+// (916 x 2368: 387 us with two, 231 with four and the accumulators below, 236 with eight; 333 x 130:
+// 95 with four, 111 with eight, whose turns end in more stages of zeros).
 template <int T, int GM, int GN, int NBUF, int MODE>
 __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
   constexpr int NW = GM * GN, WM = T / GM, WN = T / GN, MI = WM / 32, NI = WN / 32;
