@@ -23,7 +23,7 @@
 // all sizes are padded with zeros to whole tiles, so no tile has an edge.
 // 4096 x 14336, five steps: 6.8 ms.  In 256 x 256 tiles the steps' products run at 1.3 to 1.4 PFLOP/s
 // of BF16 (matrix unit 80 to 88% busy), the symmetric ones of 4096^3 at 1.1 (136 tiles for 256 CUs);
-// momentum with the norm's sum 0.13 ms and the split 0.24 are passes over memory.  333 x 130: 95 us,
+// momentum with the norm's sum 0.13 ms and the split 0.16 are passes over memory.  333 x 130: 95 us,
 // twenty launches of 4 to 5 us, each a chain of load - product - store.
 
 #include "tile_common.h"
@@ -166,6 +166,39 @@ __global__ __launch_bounds__(256) void muon_split_kernel(MuonIn p, const double*
                                                          int64_t ldxt) {
   __shared__ float tile[64][65];
   __shared__ double red[4];
+  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
+  const int c = (threadIdx.x & 15) * 4;
+  // all loads before the norm's sum, those past the matrix from its last row and column (one by one, each
+  // under its own branch: 235 us at 4096 x 14336, so 162)
+  float g[4][4], m[4][4];
+  const bool quads = p.vec && cols % 4 == 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = min(r0 + (threadIdx.x >> 4) + 16 * i, rows - 1);
+    if (quads) {
+      const int64_t col = min(c0 + c, cols - 4);
+      if constexpr (GBF) {
+        const u32x2 d = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p.g) + row * p.ldg + col);
+        g[i][0] = bf16_lo(d.x); g[i][1] = bf16_hi(d.x); g[i][2] = bf16_lo(d.y); g[i][3] = bf16_hi(d.y);
+      } else {
+        const f32x4_t d = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p.g) + row * p.ldg + col);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) g[i][k] = d[k];
+      }
+      if (p.m) {
+        const f32x4_t d = *reinterpret_cast<const f32x4_t*>(p.m + row * cols + col);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[i][k] = d[k];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t col = min(c0 + c + k, cols - 1);
+        g[i][k] = grad1<GBF>(p, row * p.ldg + col, 1.0f);
+        if (p.m) m[i][k] = p.m[row * cols + col];
+      }
+    }
+  }
   double sum = 0.0;
   for (int i = threadIdx.x; i < nparts; i += 256) sum += parts[i];
 #pragma unroll
@@ -175,20 +208,14 @@ __global__ __launch_bounds__(256) void muon_split_kernel(MuonIn p, const double*
   const double norm = sqrt(((red[0] + red[1]) + red[2]) + red[3]);
   const float inv = (float)(1.0 / (norm + (double)eps));
   const float s = p.grad_coef ? p.grad_scale * *p.grad_coef : p.grad_scale;
-  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
-  const int c = (threadIdx.x & 15) * 4;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = (threadIdx.x >> 4) + 16 * i;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      float v = 0.0f;
-      if (r0 + r < rows && c0 + c + k < cols) {
-        const int64_t at = (r0 + r) * cols + c0 + c + k;
-        const float g = grad1<GBF>(p, (r0 + r) * p.ldg + c0 + c + k, s);
-        v = (p.m ? update1(p, g, p.m[at]) : g) * inv;
-      }
-      tile[r][c + k] = v;
+      const bool in = r0 + r < rows && c0 + c + k < cols;
+      const float gs = g[i][k] * s;
+      tile[r][c + k] = in ? (p.m ? update1(p, gs, m[i][k]) : gs) * inv : 0.0f;
     }
   }
   __syncthreads();
