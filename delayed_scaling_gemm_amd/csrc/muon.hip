@@ -205,8 +205,9 @@ __global__ __launch_bounds__(256) void muon_split_kernel(MuonIn p, const double*
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
   __syncthreads();
-  const double norm = sqrt(((red[0] + red[1]) + red[2]) + red[3]);
-  const float inv = (float)(1.0 / (norm + (double)eps));
+  // (in 64 bits up to the product: the reciprocal of a tiny eps is beyond fp32's range, that of a norm
+  // above 2^126 below its normal numbers)
+  const double inv = 1.0 / (sqrt(((red[0] + red[1]) + red[2]) + red[3]) + (double)eps);
   const float s = p.grad_coef ? p.grad_scale * *p.grad_coef : p.grad_scale;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -215,7 +216,7 @@ __global__ __launch_bounds__(256) void muon_split_kernel(MuonIn p, const double*
     for (int k = 0; k < 4; ++k) {
       const bool in = r0 + r < rows && c0 + c + k < cols;
       const float gs = g[i][k] * s;
-      tile[r][c + k] = in ? (p.m ? update1(p, gs, m[i][k]) : gs) * inv : 0.0f;
+      tile[r][c + k] = in ? (float)((double)(p.m ? update1(p, gs, m[i][k]) : gs) * inv) : 0.0f;
     }
   }
   __syncthreads();

@@ -856,7 +856,7 @@ int fp8ds_rmsnorm_sandwich_bwd(const void* dy, fp8ds_dtype xt, int64_t lddy, con
  * the update's singular values near 1.
  *   g' = g * fl32(grad_scale * (*grad_coef)),   m = mu m + g'
  *   U = g' + mu m (nesterov) or m;  U = g' without a momentum
- *   X = U / (|U|_F + eps)                 the norm in 64 bits
+ *   X = U / (|U|_F + eps)                 in 64 bits, rounded to fp32 once
  *   per step, with its own a, b, c:  A = X X^T,  X = a X + (b A + c A A) X
  *   o = X                                 (on the transpose where rows > cols)
  * m and U: each operation one fp32 rounding.  The products take their operands as pairs of BF16 (16
