@@ -10,9 +10,16 @@
 // Precision.  A step multiplies small singular values by a = 3.4, five steps by 485, and what the
 // operands' rounding adds to the weak directions grows with them: with X, A and B rounded once to
 // BF16 the result was 1e-2 (Gaussian matrices) to 1e-1 (a few strong directions over weak ones)
-// off the one in 64 bits, once to F16 1e-3 to 1e-2.  So every operand is a pair of BF16, hi + lo
-// (16 significant bits, fp32's range), and a product is hi hi + hi lo + lo hi in fp32: 2e-5 to 7e-5,
-// below the rounding of a BF16 result, at three times the matrix instructions.
+// off the one in 64 bits, once to F16 1e-3 to 1e-2.  So every operand is a pair of F16, hi + lo (22
+// significant bits), and a product is hi hi + hi lo + lo hi in fp32, at three times the matrix
+// instructions: 7e-7 to 6e-6 (Gaussian) and up to 3.4e-5 (decaying singular values), where the same
+// iteration in fp32 is as far off.  (Pairs of BF16, 16 bits: 1.5e-5 to 3.5e-5 and up to 8e-4; 3%
+// faster at 4096 x 14336.)
+// F16's range: a matrix is stored times a power of two that brings its largest singular value, which
+// bounds its elements, to 2^14 .. 2^15; what F16 cannot hold is then 2^-39 of that.  The bounds follow
+// from the coefficients (poly_max, step_max), from |X| <= 1 on; twice of them still fits, and a bound's
+// rounding errors are far less (a polynomial of degree 5 has a slope of at most 25 times its bound, so
+// errors of 2^-21 of the operands stay such).
 //
 // Design for gfx950: the products are bound by the matrix cores.  All of them are C = P Q^T over
 // K-contiguous pair matrices: X and its transpose are both kept (A and B are symmetric), so no
@@ -21,8 +28,8 @@
 // block pair from 8 fragment reads, half of what single operands would read per instruction.  A and
 // B are computed for the tiles on and below the diagonal only and stored with their mirror image;
 // all sizes are padded with zeros to whole tiles, so no tile has an edge.
-// 4096 x 14336, five steps: 6.8 ms.  In 256 x 256 tiles the steps' products run at 1.3 to 1.4 PFLOP/s
-// of BF16 (matrix unit 80 to 88% busy), the symmetric ones of 4096^3 at 1.1 (136 tiles for 256 CUs);
+// 4096 x 14336, five steps: 6.9 ms.  In 256 x 256 tiles the steps' products run at 1.3 to 1.4 PFLOP/s
+// of F16 (matrix unit 80 to 88% busy), the symmetric ones of 4096^3 at 1.1 (136 tiles for 256 CUs);
 // momentum with the norm's sum 0.13 ms and the split 0.16 are passes over memory.  333 x 130: 95 us,
 // twenty launches of 4 to 5 us, each a chain of load - product - store.
 
@@ -37,6 +44,7 @@ namespace {
 // Byte offset of column c of a pair row (lo: 64 bytes further).
 __device__ __forceinline__ int64_t pair_at(int64_t c) { return (c >> 5) * 128 + (c & 31) * 2; }
 
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 struct Pair8 {
   u32x4 hi, lo;
 };
@@ -44,9 +52,10 @@ __device__ __forceinline__ Pair8 split8(const float (&v)[8]) {
   Pair8 p;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t h = pack_bf16x2(v[2 * k], v[2 * k + 1]);
-    p.hi[k] = h;
-    p.lo[k] = pack_bf16x2(v[2 * k] - bf16_lo(h), v[2 * k + 1] - bf16_hi(h));
+    const v2h h = {(_Float16)v[2 * k], (_Float16)v[2 * k + 1]};
+    const v2h l = {(_Float16)(v[2 * k] - (float)h.x), (_Float16)(v[2 * k + 1] - (float)h.y)};
+    p.hi[k] = __builtin_bit_cast(uint32_t, h);
+    p.lo[k] = __builtin_bit_cast(uint32_t, l);
   }
   return p;
 }
@@ -160,8 +169,9 @@ __global__ __launch_bounds__(256) void muon_sum_kernel(MuonIn p, double* __restr
 // matrix.
 template <bool GBF>
 __global__ __launch_bounds__(256) void muon_split_kernel(MuonIn p, const double* __restrict__ parts,
-                                                         int nparts, float eps, int64_t rows,
-                                                         int64_t cols, uint8_t* __restrict__ x,
+                                                         int nparts, float eps, float scale,
+                                                         int64_t rows, int64_t cols,
+                                                         uint8_t* __restrict__ x,
                                                          int64_t ldx, uint8_t* __restrict__ xt,
                                                          int64_t ldxt) {
   __shared__ float tile[64][65];
@@ -207,7 +217,7 @@ __global__ __launch_bounds__(256) void muon_split_kernel(MuonIn p, const double*
   __syncthreads();
   // (in 64 bits up to the product: the reciprocal of a tiny eps is beyond fp32's range, that of a norm
   // above 2^126 below its normal numbers)
-  const double inv = 1.0 / (sqrt(((red[0] + red[1]) + red[2]) + red[3]) + (double)eps);
+  const double inv = (double)scale / (sqrt(((red[0] + red[1]) + red[2]) + red[3]) + (double)eps);
   const float s = p.grad_coef ? p.grad_scale * *p.grad_coef : p.grad_scale;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -239,7 +249,8 @@ struct NsArgs {
   int tiles_m, tiles_n;
   uint8_t *C, *Ct;       // pair matrices: the result and its transpose
   int64_t ldc, ldct;
-  float a, b, c;
+  float a, b, c;         // kPoly, with the scales of A and B in them
+  float f;               // of the sums: the result's scale over the operands'
   float* part;           // kPart: [share][tile pair][T][T]
   void* o;               // kLast: [orows][ldo]
   int o_bf16, o_t;       // o_t: o holds the transpose
@@ -337,9 +348,9 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
           v16f& c = NA == 3 && q < 2 ? more[q] : acc[i][j];
-          c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              __builtin_bit_cast(v8bf, fb[s][j][q == 0 ? 1 : 0]),
-              __builtin_bit_cast(v8bf, fa[s][i][q == 1 ? 1 : 0]), c, 0, 0, 0);
+          c = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+              __builtin_bit_cast(v8h, fb[s][j][q == 0 ? 1 : 0]),
+              __builtin_bit_cast(v8h, fa[s][i][q == 1 ? 1 : 0]), c, 0, 0, 0);
         }
   };
   using std::integral_constant;
@@ -401,6 +412,7 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
     return reinterpret_cast<float*>(out + row * (WN * 4) + (((c >> 2) ^ swz32(row)) << 4) + (c & 3) * 4);
   };
   constexpr int UPR = WN / 8, RPT = 64 / UPR;  // lanes of a row, rows of a turn
+  const float f = MODE == kPart || MODE == kPoly ? 1.0f : p.f;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     if (i > 0) {
@@ -426,7 +438,7 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
         for (int k = 0; k < 8; k += 4) {
           const f32x4_t d = *reinterpret_cast<const f32x4_t*>(place(row, c + k));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[k + e] = d[e];
+          for (int e = 0; e < 4; ++e) v[k + e] = d[e] * f;
         }
         body(row, c, v);
       }
@@ -438,7 +450,7 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
         const int c = t * 16 + (lane & 15), row = (lane >> 4) * 8;
         float v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = *place(row + k, c);
+        for (int k = 0; k < 8; ++k) v[k] = *place(row + k, c) * f;
         body(row, c, v);
       }
     };
@@ -487,8 +499,9 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
           const u32x4 hi = *reinterpret_cast<const u32x4*>(a), lo = *reinterpret_cast<const u32x4*>(a + 64);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float x = k & 1 ? bf16_hi(hi[k >> 1]) + bf16_hi(lo[k >> 1])
-                                  : bf16_lo(hi[k >> 1]) + bf16_lo(lo[k >> 1]);
+            const uint32_t wh = hi[k >> 1], wl = lo[k >> 1];  // (a bit_cast of the element itself takes [0])
+            const v2h xh = __builtin_bit_cast(v2h, wh), xl = __builtin_bit_cast(v2h, wl);
+            const float x = (float)xh[k & 1] + (float)xl[k & 1];
             v[k] = p.c * v[k] + p.b * x;
             if (mi + row == nw + c + k) v[k] += p.a;
           }
@@ -516,7 +529,8 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
 // A from the shares of K: 64 x 64 of a tile pair per workgroup, the shares in order.
 template <int T>
 __global__ __launch_bounds__(256) void muon_join_kernel(const float* __restrict__ part, int shares,
-                                                        int pairs, uint8_t* __restrict__ A, int64_t ld) {
+                                                        int pairs, float f, uint8_t* __restrict__ A,
+                                                        int64_t ld) {
   __shared__ float tile[64][65];
   constexpr int N = T / 64;
   const int pair = blockIdx.x / (N * N), sub = blockIdx.x % (N * N), sr = sub / N * 64, sc = sub % N * 64;
@@ -534,7 +548,7 @@ __global__ __launch_bounds__(256) void muon_join_kernel(const float* __restrict_
       for (int k = 0; k < 4; ++k) v[k] += d[k];
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) tile[r][c + k] = v[k];
+    for (int k = 0; k < 4; ++k) tile[r][c + k] = v[k] * f;
   }
   __syncthreads();
   const int64_t m0 = (int64_t)tm * T + sr, n0 = (int64_t)tn * T + sc;
@@ -615,6 +629,42 @@ hipError_t launch_product(const NsArgs& a, int tile, unsigned grid, unsigned sha
   return hipGetLastError();
 }
 
+// Largest |a + b t + c t^2| of 0 <= t <= top, and largest |s (a + b s^2 + c s^4)| of 0 <= s <= top: what a
+// step makes of singular values up to there.
+double poly_max(const float* abc, double top) {
+  const double a = abc[0], b = abc[1], c = abc[2];
+  auto at = [&](double t) { return std::fabs(a + t * (b + t * c)); };
+  double m = std::fmax(at(0.0), at(top));
+  if (c != 0.0) {
+    const double t = -b / (2.0 * c);
+    if (t > 0.0 && t < top) m = std::fmax(m, at(t));
+  }
+  return m;
+}
+double step_max(const float* abc, double top) {
+  const double a = abc[0], b = abc[1], c = abc[2];
+  auto at = [&](double t) { return std::sqrt(t) * std::fabs(a + t * (b + t * c)); };
+  double m = at(top * top);
+  auto root = [&](double t) {  // of a + 3 b t + 5 c t^2
+    if (t > 0.0 && t < top * top) m = std::fmax(m, at(t));
+  };
+  const double d = 9.0 * b * b - 20.0 * a * c;
+  if (c != 0.0 && d >= 0.0) {
+    root((-3.0 * b + std::sqrt(d)) / (10.0 * c));
+    root((-3.0 * b - std::sqrt(d)) / (10.0 * c));
+  } else if (c == 0.0 && b != 0.0) {
+    root(-a / (3.0 * b));
+  }
+  return m;
+}
+// The power of two that brings a matrix of this largest singular value to 2^14 .. 2^15.
+double scale_of(double bound) {
+  int e = 0;
+  if (std::isfinite(bound) && std::frexp(bound, &e) == 0.5) --e;  // (a zero stays as it is)
+  if (!std::isfinite(bound) || e > 80) e = 80;
+  return std::ldexp(1.0, 15 - (e < -80 ? -80 : e));
+}
+
 }  // namespace
 
 int64_t muon_workspace(int64_t rows, int64_t cols) {
@@ -643,21 +693,28 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
   const int64_t ld_is = pl.tall ? ldxt : ldx, ld_turned = pl.tall ? ldx : ldxt;
   const int64_t prows = pl.tall ? pl.n : pl.m, pcols = pl.tall ? pl.m : pl.n;
   const dim3 grid((unsigned)(pcols / 64), (unsigned)(prows / 64));
+  double xb = 1.0, xs = scale_of(xb);  // X: a bound of its singular values, the scale it is stored with
   if (q.g_bf16)
     hipLaunchKernelGGL((muon_split_kernel<true>), grid, dim3(256), 0, stream, in, parts, nparts, q.eps,
-                       q.rows, q.cols, as_is, ld_is, turned, ld_turned);
+                       (float)xs, q.rows, q.cols, as_is, ld_is, turned, ld_turned);
   else
     hipLaunchKernelGGL((muon_split_kernel<false>), grid, dim3(256), 0, stream, in, parts, nparts, q.eps,
-                       q.rows, q.cols, as_is, ld_is, turned, ld_turned);
+                       (float)xs, q.rows, q.cols, as_is, ld_is, turned, ld_turned);
   e = hipGetLastError();
 
   const int st = (int)(pl.m / pl.sym_tile), pairs = st * (st + 1) / 2;
-  // C = P Q^T over m columns, symmetric
-  auto symmetric = [&](auto mode_tag, const uint8_t* P, const uint8_t* Q, uint8_t* C, const float* abc) {
+  // C = P Q^T over m columns, symmetric; ps, qs, cs: their scales
+  auto symmetric = [&](auto mode_tag, const uint8_t* P, double ps, const uint8_t* Q, double qs, uint8_t* C,
+                       double cs, const float* abc) {
     NsArgs g = {};
     g.P = P; g.Q = Q; g.ld = (int)ldxt; g.nk = (int)(pl.m / 32);
     g.C = g.Ct = C; g.ldc = g.ldct = ldxt;
-    if (abc) { g.a = abc[0]; g.b = abc[1]; g.c = abc[2]; }
+    g.f = (float)(cs / (ps * qs));
+    if (abc) {
+      g.a = (float)(abc[0] * cs);
+      g.b = (float)(abc[1] * (cs / ps));
+      g.c = (float)(abc[2] * (cs / (ps * ps)));
+    }
     if (e == hipSuccess) e = launch_product<decltype(mode_tag)::value>(g, pl.sym_tile, pairs, 1, stream);
   };
   const std::integral_constant<int, kGram> product{};
@@ -668,6 +725,8 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
     NsArgs g = {};
     g.P = g.Q = x; g.ld = (int)ldx; g.nk = pl.share_stages;
     g.C = g.Ct = a; g.ldc = g.ldct = ldxt;
+    double as = scale_of(xb * xb);
+    g.f = (float)(as / (xs * xs));
     if (pl.shares > 1) {
       g.part = reinterpret_cast<float*>(ws + pl.share);
       e = launch_product<kPart>(g, pl.sym_tile, pairs, pl.shares, stream);
@@ -675,11 +734,11 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
       const int sub = pl.sym_tile / 64;
       const dim3 jg((unsigned)(pairs * sub * sub));
       if (pl.sym_tile == 256)
-        hipLaunchKernelGGL((muon_join_kernel<256>), jg, dim3(256), 0, stream, g.part, pl.shares, pairs, a, ldxt);
+        hipLaunchKernelGGL((muon_join_kernel<256>), jg, dim3(256), 0, stream, g.part, pl.shares, pairs, g.f, a, ldxt);
       else if (pl.sym_tile == 128)
-        hipLaunchKernelGGL((muon_join_kernel<128>), jg, dim3(256), 0, stream, g.part, pl.shares, pairs, a, ldxt);
+        hipLaunchKernelGGL((muon_join_kernel<128>), jg, dim3(256), 0, stream, g.part, pl.shares, pairs, g.f, a, ldxt);
       else
-        hipLaunchKernelGGL((muon_join_kernel<64>), jg, dim3(256), 0, stream, g.part, pl.shares, pairs, a, ldxt);
+        hipLaunchKernelGGL((muon_join_kernel<64>), jg, dim3(256), 0, stream, g.part, pl.shares, pairs, g.f, a, ldxt);
       e = hipGetLastError();
     } else {
       e = launch_product<kGram>(g, pl.sym_tile, pairs, 1, stream);
@@ -690,27 +749,44 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
     const int size = !pl.grouped ? 1 : q.steps - k < (k ? 3 : 2) ? q.steps - k : (k ? 3 : 2);
     uint8_t *const b0 = ws + pl.b[0], *const b1 = ws + pl.b[1], *const b2 = ws + pl.b[2];
     uint8_t *last = b0, *sofar = b0;  // B of the last step, the product of all
-    symmetric(poly, a, a, b0, q.coefs + 3 * k);
+    const float* abc = q.coefs + 3 * k;
+    double bound = poly_max(abc, xb * xb), after = step_max(abc, xb);  // of B so far, of X after the steps
+    double ls = scale_of(bound), js = ls;                             // scales of `last` and `sofar`
+    symmetric(poly, a, as, a, as, b0, ls, abc);
     for (int i = 1; i < size; ++i) {  // (three steps at most: b0 and then b1 are free again by then)
-      symmetric(product, last, a, ws + pl.t, nullptr);
-      symmetric(product, ws + pl.t, last, a, nullptr);
+      const double ts = scale_of(xb * after), next = scale_of(after * after);  // (B A is s (s p(s^2)))
+      symmetric(product, last, ls, a, as, ws + pl.t, ts, nullptr);
+      symmetric(product, ws + pl.t, ts, last, ls, a, next, nullptr);
+      as = next;
+      xb = after;
       uint8_t *fresh = i == 1 ? b1 : b0, *joined = i == 1 ? b2 : b1;
-      symmetric(poly, a, a, fresh, q.coefs + 3 * (k + i));
-      symmetric(product, fresh, sofar, joined, nullptr);
+      abc += 3;
+      const double more = poly_max(abc, xb * xb);
+      bound *= more;
+      ls = scale_of(more);
+      symmetric(poly, a, as, a, as, fresh, ls, abc);
+      symmetric(product, fresh, ls, sofar, js, joined, scale_of(bound), nullptr);
+      js = scale_of(bound);
+      after = step_max(abc, xb);
       last = fresh;
       sofar = joined;
     }
     k += size;
+    xb = after;
     if (e != hipSuccess) return e;
     g = NsArgs{};
     g.P = sofar; g.Q = xt; g.ld = (int)ldxt; g.nk = (int)(pl.m / 32);
     g.tiles_m = (int)(pl.m / pl.step_tile); g.tiles_n = (int)(pl.n / pl.step_tile);
     const unsigned tiles = (unsigned)(g.tiles_m * g.tiles_n);
     if (k < q.steps) {
+      const double scale = scale_of(xb);
+      g.f = (float)(scale / (js * xs));
+      xs = scale;
       g.C = x; g.ldc = ldx;
       g.Ct = ws + pl.xt[(turn + 1) & 1]; g.ldct = ldxt;
       e = launch_product<kStep>(g, pl.step_tile, tiles, 1, stream);
     } else {
+      g.f = (float)(1.0 / (js * xs));
       g.o = q.o; g.o_bf16 = q.o_bf16 ? 1 : 0; g.o_t = pl.tall ? 1 : 0;
       g.orows = q.rows; g.ocols = q.cols; g.ldo = q.ldo;
       g.o_vec = q.cols % 8 == 0 && reinterpret_cast<uintptr_t>(q.o) % 16 == 0 &&

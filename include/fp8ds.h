@@ -859,10 +859,11 @@ int fp8ds_rmsnorm_sandwich_bwd(const void* dy, fp8ds_dtype xt, int64_t lddy, con
  *   X = U / (|U|_F + eps)                 in 64 bits, rounded to fp32 once
  *   per step, with its own a, b, c:  A = X X^T,  X = a X + (b A + c A A) X
  *   o = X                                 (on the transpose where rows > cols)
- * m and U: each operation one fp32 rounding.  The products take their operands as pairs of BF16 (16
- * significant bits), three products of each, with fp32 sums: o is 2e-5 to 7e-5 (relative, of the
- * whole matrix) from the iteration in 64 bits for Gaussian g, up to 1e-3 where the singular values
- * fall by orders of magnitude.
+ * m and U: each operation one fp32 rounding.  The products take their operands as pairs of F16 (22
+ * significant bits; what is below 2^-39 of |U|_F is lost), three products of each, with fp32 sums: o
+ * is up to 1e-5 (relative, of the whole matrix) from the iteration in 64 bits for Gaussian g, up to
+ * 1e-4 where a few directions are far stronger than the rest or the singular values fall by orders of
+ * magnitude, as the iteration in fp32 is.
  *   g          device [rows x cols] of gt, rows ldg apart (a part of a stacked gradient, say).
  *   momentum   device or NULL: [rows x cols] fp32, contiguous, updated in place (zeros before the
  *              first step).
