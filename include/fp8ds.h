@@ -876,8 +876,10 @@ int fp8ds_rmsnorm_sandwich_bwd(const void* dy, fp8ds_dtype xt, int64_t lddy, con
  *   eps        finite, > 0 (1e-7 as a rule).  A zero U gives a zero o.
  *   o          device [rows x cols] of ot, rows ldo apart; must not overlap the others.
  *   workspace  device, at least fp8ds_muon_workspace(rows, cols) bytes; its contents need no
- *              preparation and do not matter afterwards.  About 12 bytes for each element and 8 for
- *              each of min(rows, cols)^2.
+ *              preparation and do not matter afterwards.  With either side rounded up to 64, 128 or 256
+ *              (64 at least, no side to twice itself): 12 bytes for each element, 8 for each of
+ *              min(rows, cols)^2, 20 where one side is 1.5 times the other or more, and up to
+ *              4 MB of partial sums.
  * g and o aligned to their elements, momentum and workspace to 16 bytes.  No atomics: the same
  * inputs give the same bits.
  */

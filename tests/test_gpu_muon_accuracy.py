@@ -89,3 +89,8 @@ def test_coefficients_of_other_sizes(R, C):
             A = x @ x.t()
             x = a * x + (b * A + c * (A @ A)) @ x
         check(R, C, "gauss", len(coefs), coefs, err / float(x.norm()))
+
+
+@pytest.mark.parametrize("R,C", [(1, 33000), (8, 40001), (40000, 64), (100, 33000), (20000, 129)])
+def test_long_thin_matrices(R, C):
+    check(R, C, "gauss")
