@@ -526,16 +526,13 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
   }
 }
 
-// A from the shares of K: 64 x 64 of a tile pair per workgroup, the shares in order.
-template <int T>
+// A from the shares of K: a tile pair per workgroup, the shares in order.
 __global__ __launch_bounds__(256) void muon_join_kernel(const float* __restrict__ part, int shares,
                                                         int pairs, float f, uint8_t* __restrict__ A,
                                                         int64_t ld) {
   __shared__ float tile[64][65];
-  constexpr int N = T / 64;
-  const int pair = blockIdx.x / (N * N), sub = blockIdx.x % (N * N), sr = sub / N * 64, sc = sub % N * 64;
   int tm, tn;
-  pair_of(pair, tm, tn);
+  pair_of(blockIdx.x, tm, tn);
   const int c = (threadIdx.x & 15) * 4;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -543,7 +540,7 @@ __global__ __launch_bounds__(256) void muon_join_kernel(const float* __restrict_
     f32x4_t v = {0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s < shares; ++s) {
       const f32x4_t d = *reinterpret_cast<const f32x4_t*>(
-          part + (((int64_t)s * pairs + pair) * T + sr + r) * T + sc + c);
+          part + (((int64_t)s * pairs + blockIdx.x) * 64 + r) * 64 + c);
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] += d[k];
     }
@@ -551,13 +548,15 @@ __global__ __launch_bounds__(256) void muon_join_kernel(const float* __restrict_
     for (int k = 0; k < 4; ++k) tile[r][c + k] = v[k] * f;
   }
   __syncthreads();
-  const int64_t m0 = (int64_t)tm * T + sr, n0 = (int64_t)tn * T + sc;
+  const int64_t m0 = (int64_t)tm * 64, n0 = (int64_t)tn * 64;
   write_pairs64(tile, false, A, ld, m0, n0);
   if (tm != tn) write_pairs64(tile, true, A, ld, n0, m0);
 }
 
 // ------------------------------------------------------------------ host
 
+// gfx950's, and not the current device's: the workspace must not depend on which device is current when
+// its size is asked for.
 constexpr int kCus = 256;
 
 // The largest tiles that still give most of the CUs one, but none that the shorter side (m) fills to
@@ -586,12 +585,13 @@ MuonPlan muon_plan(int64_t rows, int64_t cols) {
   p.m = pad(m);
   p.n = pad(n);
   p.sym_tile = tile_for(p.m, p.m, true, p.step_tile);
-  // X X^T with few tiles and a long K: shares of K, of 16 stages and more, up to a tile per CU.
+  // X X^T with few tiles and a long K: shares of K, of 16 stages and more, up to a tile per CU.  Tiles of
+  // 128 and 256 are taken from 128 tile pairs on, which leaves no CU for a second share.
   // (Shares that even out 136 tiles over 256 CUs, 3 or 7, were no faster at 4096 x 14336: the CUs
   // that work run at a higher clock.)
   const int64_t st = p.m / p.sym_tile, pairs = st * (st + 1) / 2, stages = p.n / 32;
   int64_t shares = 1;
-  while (pairs * shares * 2 <= kCus && stages / (shares * 2) >= 16) shares *= 2;
+  while (p.sym_tile == 64 && pairs * shares * 2 <= kCus && stages / (shares * 2) >= 16) shares *= 2;
   p.share_stages = (int)(shares == 1 ? stages : (stages + 4 * shares - 1) / (4 * shares) * 4);
   p.shares = (int)shares;
   int64_t at = 0;
@@ -618,15 +618,15 @@ MuonPlan muon_plan(int64_t rows, int64_t cols) {
 }
 
 template <int MODE>
-hipError_t launch_product(const NsArgs& a, int tile, unsigned grid, unsigned shares, hipStream_t stream) {
+hipError_t launch_product(const NsArgs& a, int tile, unsigned grid, hipStream_t stream) {
   if (tile == 256)
-    hipLaunchKernelGGL((muon_gemm_kernel<256, 4, 2, 2, MODE>), dim3(grid, shares), dim3(512), 0, stream, a);
-  else if (tile == 128 && (int64_t)grid * shares > kCus)
-    hipLaunchKernelGGL((muon_gemm_kernel<128, 2, 2, 2, MODE>), dim3(grid, shares), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((muon_gemm_kernel<256, 4, 2, 2, MODE>), dim3(grid), dim3(512), 0, stream, a);
+  else if (tile == 128 && grid > kCus)
+    hipLaunchKernelGGL((muon_gemm_kernel<128, 2, 2, 2, MODE>), dim3(grid), dim3(256), 0, stream, a);
   else if (tile == 128)
-    hipLaunchKernelGGL((muon_gemm_kernel<128, 2, 2, 4, MODE>), dim3(grid, shares), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((muon_gemm_kernel<128, 2, 2, 4, MODE>), dim3(grid), dim3(256), 0, stream, a);
   else
-    hipLaunchKernelGGL((muon_gemm_kernel<64, 2, 2, 4, MODE>), dim3(grid, shares), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((muon_gemm_kernel<64, 2, 2, 4, MODE>), dim3(grid), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -716,7 +716,7 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
       g.b = (float)(abc[1] * (cs / ps));
       g.c = (float)(abc[2] * (cs / (ps * ps)));
     }
-    if (e == hipSuccess) e = launch_product<decltype(mode_tag)::value>(g, pl.sym_tile, pairs, 1, stream);
+    if (e == hipSuccess) e = launch_product<decltype(mode_tag)::value>(g, pl.sym_tile, pairs, stream);
   };
   const std::integral_constant<int, kGram> product{};
   const std::integral_constant<int, kPoly> poly{};
@@ -730,19 +730,15 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
     g.f = (float)(as / (xs * xs));
     if (pl.shares > 1) {
       g.part = reinterpret_cast<float*>(ws + pl.share);
-      e = launch_product<kPart>(g, pl.sym_tile, pairs, pl.shares, stream);
+      hipLaunchKernelGGL((muon_gemm_kernel<64, 2, 2, 4, kPart>), dim3(pairs, pl.shares), dim3(256), 0,
+                         stream, g);
+      e = hipGetLastError();
       if (e != hipSuccess) return e;
-      const int sub = pl.sym_tile / 64;
-      const dim3 jg((unsigned)(pairs * sub * sub));
-      if (pl.sym_tile == 256)
-        hipLaunchKernelGGL((muon_join_kernel<256>), jg, dim3(256), 0, stream, g.part, pl.shares, pairs, g.f, a, ldxt);
-      else if (pl.sym_tile == 128)
-        hipLaunchKernelGGL((muon_join_kernel<128>), jg, dim3(256), 0, stream, g.part, pl.shares, pairs, g.f, a, ldxt);
-      else
-        hipLaunchKernelGGL((muon_join_kernel<64>), jg, dim3(256), 0, stream, g.part, pl.shares, pairs, g.f, a, ldxt);
+      hipLaunchKernelGGL(muon_join_kernel, dim3(pairs), dim3(256), 0, stream, g.part, pl.shares, pairs,
+                         g.f, a, ldxt);
       e = hipGetLastError();
     } else {
-      e = launch_product<kGram>(g, pl.sym_tile, pairs, 1, stream);
+      e = launch_product<kGram>(g, pl.sym_tile, pairs, stream);
     }
     // A group of steps is one product with X: with B_0 of A_0 = X X^T, the next step's A_1 is
     // B_0 A_0 B_0, and X becomes (B_1 B_0) X.  Every factor is a polynomial of A_0, so all of them
@@ -785,7 +781,7 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
       xs = scale;
       g.C = x; g.ldc = ldx;
       g.Ct = ws + pl.xt[(turn + 1) & 1]; g.ldct = ldxt;
-      e = launch_product<kStep>(g, pl.step_tile, tiles, 1, stream);
+      e = launch_product<kStep>(g, pl.step_tile, tiles, stream);
     } else {
       g.f = (float)(1.0 / (js * xs));
       g.o = q.o; g.o_bf16 = q.o_bf16 ? 1 : 0; g.o_t = pl.tall ? 1 : 0;
@@ -793,7 +789,7 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
       g.o_vec = q.cols % 8 == 0 && reinterpret_cast<uintptr_t>(q.o) % 16 == 0 &&
                 (q.ldo * (q.o_bf16 ? 2 : 4)) % 16 == 0;
       g.skip = q.grad_amax;
-      e = launch_product<kLast>(g, pl.step_tile, tiles, 1, stream);
+      e = launch_product<kLast>(g, pl.step_tile, tiles, stream);
     }
   }
   return e;
