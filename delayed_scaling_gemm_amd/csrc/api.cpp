@@ -1162,7 +1162,7 @@ static int gated_common(const char* who, bool bwd, int64_t M, int64_t F, int64_t
   p.scale_used = scale_used; p.amax = amax; p.sat = sat_count;
   p.vec = F % 16 == 0 && (!gu || (aligned16(gu) && ldgu % 8 == 0)) &&
           (!y || (aligned16(y) && ldy * ysz % 16 == 0)) && (!q || (aligned16(q) && ldq % 16 == 0));
-  const bool exact = mma == FP8DS_MMA_EXACT;
+  const bool exact = mma == FP8DS_MMA_EXACT || M <= fp8ds::kGatedFewRows;
   return hip_status(bwd ? fp8ds::launch_gated_bwd(p, (int)fa, exact, num_cus(), stream)
                         : fp8ds::launch_gated_fwd(p, exact, num_cus(), stream),
                     who);

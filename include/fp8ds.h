@@ -766,8 +766,8 @@ int fp8ds_gated_gemm(int64_t M, int64_t F, int64_t K, const uint8_t* A, fp8ds_fo
  *   q          device or NULL: the same in FP8 (E5M2 as a rule), rows ldq apart, with scale,
  *              scale_used, amax and sat_count as fp8ds_gated_gemm.  One scale for both halves, so
  *              dX = [dg du] W^T and dW = X^T [dg du] are single fp8ds_gemm calls.
- * Other arguments, sizes and alignment as fp8ds_gated_gemm.  At least one of dgu and q; neither may
- * overlap gu.
+ * Other arguments, sizes, alignment and mma as fp8ds_gated_gemm.  At least one of dgu and q; neither
+ * may overlap gu.
  */
 int fp8ds_gated_gemm_bwd(int64_t M, int64_t F, int64_t H, const uint8_t* A, fp8ds_format fa,
                          int64_t lda, const float* scale_a, const uint8_t* B, fp8ds_format fb,
