@@ -658,12 +658,13 @@ double step_max(const float* abc, double top) {
   }
   return m;
 }
-// The power of two that brings a matrix of this largest singular value to 2^14 .. 2^15.
+// The power of two that brings a matrix of this largest singular value to 2^14 .. 2^15: within 2^-400 ..
+// 2^400, so that A of any X that fp32 holds has one, and a product's three scales are finite here.
 double scale_of(double bound) {
   int e = 0;
   if (std::isfinite(bound) && std::frexp(bound, &e) == 0.5) --e;  // (a zero stays as it is)
-  if (!std::isfinite(bound) || e > 80) e = 80;
-  return std::ldexp(1.0, 15 - (e < -80 ? -80 : e));
+  if (!std::isfinite(bound) || e > 400) e = 400;
+  return std::ldexp(1.0, 15 - (e < -400 ? -400 : e));
 }
 
 }  // namespace

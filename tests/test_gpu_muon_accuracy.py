@@ -94,3 +94,13 @@ def test_coefficients_of_other_sizes(R, C):
 @pytest.mark.parametrize("R,C", [(1, 33000), (8, 40001), (40000, 64), (100, 33000), (20000, 129)])
 def test_long_thin_matrices(R, C):
     check(R, C, "gauss")
+
+
+@pytest.mark.parametrize("R,C", [(70, 90), (130, 700)])
+@pytest.mark.parametrize("coefs", [[(1e36, 0.0, 0.0)], [(0.0, -1e36, 2e36)], [(1e30, -1e30, 1e30), (1e-30, 0.0, 0.0)],
+                                   [(1e-30, 0.0, 0.0)], [(0.0, 0.0, 1e-28)],
+                                   [(1e-25, -1e-25, 0.0), (1e25, 0.0, 0.0), (3.0, -3.0, 1.0)]])
+def test_coefficients_near_the_ends_of_the_range(R, C, coefs):
+    """The scales take any X that fp32 holds, and its A.  Elements of X are above 2^-24 of its norm but for a
+    few: those of the results are normal numbers down to coefficients of 1e-30; sums as elsewhere."""
+    check(R, C, "gauss", len(coefs), coefs)
