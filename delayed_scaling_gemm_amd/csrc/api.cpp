@@ -1405,6 +1405,8 @@ static int check_muon_shape(const char* who, int64_t rows, int64_t cols) {
   return FP8DS_OK;
 }
 
+static_assert(fp8ds::kMuonMaxSteps == FP8DS_MUON_MAX_STEPS, "the launcher's limit is the header's");
+
 int64_t fp8ds_muon_workspace(int64_t rows, int64_t cols) {
   if (check_muon_shape("fp8ds_muon_workspace", rows, cols)) return FP8DS_ERR_SHAPE;
   ok();

@@ -71,6 +71,7 @@ hipError_t launch_adamw(const AdamWLaunch& a, hipStream_t stream);
 hipError_t launch_muon_apply(const AdamWLaunch& a, hipStream_t stream);
 
 // Muon's direction: momentum, then Newton-Schulz steps on the normalised update.
+constexpr int kMuonMaxSteps = 16;
 struct MuonLaunch {
   const void* g;           // [rows][ldg]
   bool g_bf16;

@@ -33,6 +33,8 @@
 // with the norm's sum 0.13 ms and the split 0.16 are passes over memory.  333 x 130: 95 us, twenty
 // launches of 3 to 6.5 us, each a chain of load - product - store.
 
+#include <algorithm>
+
 #include "tile_common.h"
 
 namespace fp8ds {
@@ -115,6 +117,23 @@ __device__ __forceinline__ float update1(const MuonIn& p, float g, float m) {
 
 constexpr int kParts = 2048;  // partial sums of squares, one per workgroup
 
+// Where U is small beside eps, X = U / (|U| + eps) is far below its bound of 1 and would leave F16's range.
+// With rho = |U| / (|U| + eps), known on the device alone, X is stored times a further 2^e, the largest
+// that its bound allows: after some steps |X| <= growth rho, and e = floor(log2(limit / rho)) >= 0 with
+// limit the bound over the growth.  e is 0 where |U| is above eps.
+constexpr int kMaxGroups = kMuonMaxSteps;
+struct XScales {
+  int groups;                // products with X
+  double limit[kMaxGroups];  // of X before each
+  float* mul;                // [groups][2]: what the extra scales leave to do in X X^T, and in the next X
+};
+__device__ __forceinline__ int extra_scale(double limit, double rho) {
+  const double q = limit / rho;
+  if (!(q >= 2.0)) return 0;  // (NaN too)
+  const int e = (int)((__double_as_longlong(q) >> 52) & 0x7FF) - 1023;
+  return e < 200 ? e : 200;   // (fp32's range of U against the largest eps: 277; what is below is 0)
+}
+
 // m, and sum U^2 in 64 bits: a share of the elements per workgroup, four at a time.
 template <bool GBF>
 __global__ __launch_bounds__(256) void muon_sum_kernel(MuonIn p, double* __restrict__ parts) {
@@ -170,7 +189,7 @@ __global__ __launch_bounds__(256) void muon_sum_kernel(MuonIn p, double* __restr
 template <bool GBF>
 __global__ __launch_bounds__(256) void muon_split_kernel(MuonIn p, const double* __restrict__ parts,
                                                          int nparts, float eps, float scale,
-                                                         int64_t rows, int64_t cols,
+                                                         XScales xs, int64_t rows, int64_t cols,
                                                          uint8_t* __restrict__ x,
                                                          int64_t ldx, uint8_t* __restrict__ xt,
                                                          int64_t ldxt) {
@@ -217,7 +236,14 @@ __global__ __launch_bounds__(256) void muon_split_kernel(MuonIn p, const double*
   __syncthreads();
   // (in 64 bits up to the product: the reciprocal of a tiny eps is beyond fp32's range, that of a norm
   // above 2^126 below its normal numbers)
-  const double inv = (double)scale / (sqrt(((red[0] + red[1]) + red[2]) + red[3]) + (double)eps);
+  const double norm = sqrt(((red[0] + red[1]) + red[2]) + red[3]);
+  const double rho = norm > 0.0 ? norm / (norm + (double)eps) : 1.0;
+  const double inv = ldexp((double)scale, extra_scale(xs.limit[0], rho)) / (norm + (double)eps);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && (int)threadIdx.x < xs.groups) {
+    const int k = threadIdx.x, e = extra_scale(xs.limit[k], rho);
+    xs.mul[2 * k] = (float)ldexp(1.0, -2 * e);
+    xs.mul[2 * k + 1] = (float)ldexp(1.0, (k + 1 < xs.groups ? extra_scale(xs.limit[k + 1], rho) : 0) - e);
+  }
   const float s = p.grad_coef ? p.grad_scale * *p.grad_coef : p.grad_scale;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -251,6 +277,7 @@ struct NsArgs {
   int64_t ldc, ldct;
   float a, b, c;         // kPoly, with the scales of A and B in them
   float f;               // of the sums: the result's scale over the operands'
+  const float* mul;      // or null: a further factor
   float* part;           // kPart: [share][tile pair][T][T]
   void* o;               // kLast: [orows][ldo]
   int o_bf16, o_t;       // o_t: o holds the transpose
@@ -413,6 +440,7 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
   };
   constexpr int UPR = WN / 8, RPT = 64 / UPR;  // lanes of a row, rows of a turn
   const float f = MODE == kPart || MODE == kPoly ? 1.0f : p.f;
+  const float f2 = MODE != kPart && MODE != kPoly && p.mul ? *p.mul : 1.0f;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     if (i > 0) {
@@ -438,7 +466,7 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
         for (int k = 0; k < 8; k += 4) {
           const f32x4_t d = *reinterpret_cast<const f32x4_t*>(place(row, c + k));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[k + e] = d[e] * f;
+          for (int e = 0; e < 4; ++e) v[k + e] = d[e] * f * f2;
         }
         body(row, c, v);
       }
@@ -450,7 +478,7 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
         const int c = t * 16 + (lane & 15), row = (lane >> 4) * 8;
         float v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = *place(row + k, c) * f;
+        for (int k = 0; k < 8; ++k) v[k] = *place(row + k, c) * f * f2;
         body(row, c, v);
       }
     };
@@ -528,8 +556,8 @@ __global__ __launch_bounds__(64 * GM * GN, 2) void muon_gemm_kernel(NsArgs p) {
 
 // A from the shares of K: a tile pair per workgroup, the shares in order.
 __global__ __launch_bounds__(256) void muon_join_kernel(const float* __restrict__ part, int shares,
-                                                        int pairs, float f, uint8_t* __restrict__ A,
-                                                        int64_t ld) {
+                                                        int pairs, float f, const float* __restrict__ mul,
+                                                        uint8_t* __restrict__ A, int64_t ld) {
   __shared__ float tile[64][65];
   int tm, tn;
   pair_of(blockIdx.x, tm, tn);
@@ -545,7 +573,7 @@ __global__ __launch_bounds__(256) void muon_join_kernel(const float* __restrict_
       for (int k = 0; k < 4; ++k) v[k] += d[k];
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) tile[r][c + k] = v[k] * f;
+    for (int k = 0; k < 4; ++k) tile[r][c + k] = v[k] * f * *mul;
   }
   __syncthreads();
   const int64_t m0 = (int64_t)tm * 64, n0 = (int64_t)tn * 64;
@@ -574,7 +602,7 @@ struct MuonPlan {
   int64_t m, n;         // padded sizes of X
   int step_tile, sym_tile, shares, share_stages;
   bool grouped;         // steps in groups (launch_muon_direction)
-  int64_t parts, x, xt[2], a, t, b[3], share, total;  // offsets in the workspace, bytes
+  int64_t parts, mul, x, xt[2], a, t, b[3], share, total;  // offsets in the workspace, bytes
 };
 MuonPlan muon_plan(int64_t rows, int64_t cols) {
   MuonPlan p = {};
@@ -601,6 +629,7 @@ MuonPlan muon_plan(int64_t rows, int64_t cols) {
     return o;
   };
   p.parts = take(kParts * (int64_t)sizeof(double));
+  p.mul = take(kMaxGroups * 2 * (int64_t)sizeof(float));
   p.x = take(p.m * p.n * 4);
   p.xt[0] = take(p.m * p.n * 4);
   p.xt[1] = take(p.m * p.n * 4);
@@ -695,13 +724,27 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
   const int64_t ld_is = pl.tall ? ldxt : ldx, ld_turned = pl.tall ? ldx : ldxt;
   const int64_t prows = pl.tall ? pl.n : pl.m, pcols = pl.tall ? pl.m : pl.n;
   const dim3 grid((unsigned)(pcols / 64), (unsigned)(prows / 64));
-  double xb = 1.0, xs = scale_of(xb);  // X: a bound of its singular values, the scale it is stored with
+  // X: a bound of its singular values, the scale it is stored with (times its extra scale), and how often it
+  // may have become its first self.
+  double xb = 1.0, xs = scale_of(xb), growth = 1.0;
+  XScales extra = {};
+  extra.mul = reinterpret_cast<float*>(ws + pl.mul);
+  auto group_size = [&](int k) { return !pl.grouped ? 1 : std::min(q.steps - k, k ? 3 : 2); };
+  for (int k = 0, n; k < q.steps; k += n) {
+    extra.limit[extra.groups++] = xb / growth;
+    n = group_size(k);
+    for (int i = 0; i < n; ++i) {
+      growth *= poly_max(q.coefs + 3 * (k + i), xb * xb);
+      xb = step_max(q.coefs + 3 * (k + i), xb);
+    }
+  }
+  xb = 1.0;
   if (q.g_bf16)
     hipLaunchKernelGGL((muon_split_kernel<true>), grid, dim3(256), 0, stream, in, parts, nparts, q.eps,
-                       (float)xs, q.rows, q.cols, as_is, ld_is, turned, ld_turned);
+                       (float)xs, extra, q.rows, q.cols, as_is, ld_is, turned, ld_turned);
   else
     hipLaunchKernelGGL((muon_split_kernel<false>), grid, dim3(256), 0, stream, in, parts, nparts, q.eps,
-                       (float)xs, q.rows, q.cols, as_is, ld_is, turned, ld_turned);
+                       (float)xs, extra, q.rows, q.cols, as_is, ld_is, turned, ld_turned);
   e = hipGetLastError();
 
   const int st = (int)(pl.m / pl.sym_tile), pairs = st * (st + 1) / 2;
@@ -729,6 +772,7 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
     g.C = g.Ct = a; g.ldc = g.ldct = ldxt;
     double as = scale_of(xb * xb);
     g.f = (float)(as / (xs * xs));
+    g.mul = extra.mul + 2 * turn;
     if (pl.shares > 1) {
       g.part = reinterpret_cast<float*>(ws + pl.share);
       hipLaunchKernelGGL((muon_gemm_kernel<64, 2, 2, 4, kPart>), dim3(pairs, pl.shares), dim3(256), 0,
@@ -736,7 +780,7 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
       e = hipGetLastError();
       if (e != hipSuccess) return e;
       hipLaunchKernelGGL(muon_join_kernel, dim3(pairs), dim3(256), 0, stream, g.part, pl.shares, pairs,
-                         g.f, a, ldxt);
+                         g.f, g.mul, a, ldxt);
       e = hipGetLastError();
     } else {
       e = launch_product<kGram>(g, pl.sym_tile, pairs, stream);
@@ -744,7 +788,7 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
     // A group of steps is one product with X: with B_0 of A_0 = X X^T, the next step's A_1 is
     // B_0 A_0 B_0, and X becomes (B_1 B_0) X.  Every factor is a polynomial of A_0, so all of them
     // are symmetric and commute.
-    const int size = !pl.grouped ? 1 : q.steps - k < (k ? 3 : 2) ? q.steps - k : (k ? 3 : 2);
+    const int size = group_size(k);
     uint8_t *const b0 = ws + pl.b[0], *const b1 = ws + pl.b[1], *const b2 = ws + pl.b[2];
     uint8_t *last = b0, *sofar = b0;  // B of the last step, the product of all
     const float* abc = q.coefs + 3 * k;
@@ -774,6 +818,7 @@ hipError_t launch_muon_direction(const MuonLaunch& q, hipStream_t stream) {
     if (e != hipSuccess) return e;
     g = NsArgs{};
     g.P = sofar; g.Q = xt; g.ld = (int)ldxt; g.nk = (int)(pl.m / 32);
+    g.mul = extra.mul + 2 * turn + 1;
     g.tiles_m = (int)(pl.m / pl.step_tile); g.tiles_n = (int)(pl.n / pl.step_tile);
     const unsigned tiles = (unsigned)(g.tiles_m * g.tiles_n);
     if (k < q.steps) {

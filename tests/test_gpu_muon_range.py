@@ -49,3 +49,22 @@ def test_large_norms(power):
     """Norms up to 2^130: above 2^126 the reciprocal is no normal number of fp32."""
     g = gauss().clamp_(-7, 7)
     assert torch.equal(direction(g * 2.0 ** power, 1e-7), direction(g, 1e-30))
+
+
+@pytest.mark.parametrize("eps,size", [(1e-7, 1e-8), (1e-7, 1e-12), (1e-7, 1e-20), (1e-7, 1e-28), (1.0, 1e-3),
+                                      (1.0, 1e-9), (1e20, 1e-5)])
+@pytest.mark.parametrize("rows,cols", [(50, 90), (64, 900), (2000, 300)])
+@pytest.mark.parametrize("steps", [5, 8])
+def test_updates_far_below_eps(rows, cols, steps, eps, size):
+    """X is then far below 1 and grows by 3.4445 a step at most: the contract's 1e-5 of the result."""
+    g = size * torch.randn(rows, cols, generator=torch.Generator(device=DEV).manual_seed(4), device=DEV)
+    o = torch.empty(rows, cols, device=DEV)
+    ws = torch.full((dsg.fp8ds_muon_workspace(rows, cols),), 0xFF, dtype=torch.uint8, device=DEV)
+    dsg.fp8ds_muon_direction(g, o, ws, eps=eps, steps=steps)
+    x = g.double() / (g.double().norm() + torch.tensor(eps, dtype=torch.float32).double())
+    x = x.t().contiguous() if rows > cols else x
+    for _ in range(steps):
+        A = x @ x.t()
+        x = 3.4445 * x + (-4.7750 * A + 2.0315 * (A @ A)) @ x
+    x = x.t() if rows > cols else x
+    assert (o.double() - x).norm() <= 1e-5 * x.norm()
