@@ -269,11 +269,73 @@ __device__ __forceinline__ float k1(const Args& p, int64_t c) {
 
 // ------------------------------------------------------------------ forward
 
+// h = res + (x r1) t k in 64 bits, rounded to fp32 once (rows of 8 to 16384 columns).  In fp32 its error of a
+// unit or so put one BF16 value in 190000 on the other side of a border; memory's time hides the 64-bit
+// arithmetic, which has fp32's rate (16384 x 4096 in BF16: 86 us with either; 8192 x 8192: 90, 86 in fp32;
+// 4096 x 16384 with an FP32 stream: 138, 168).  k in 64 bits is kept in LDS: in registers it would take the
+// room of the next row's loads.  Squares are added in pairs in fp32, whose errors average out, and in 64
+// bits from there on.
+typedef double v2d __attribute__((ext_vector_type(2)));
+template <int CTRL>
+__device__ __forceinline__ double add_dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 15, 15, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 15, 15, false);
+  return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+template <int W>  // lanes W apart, 16 or 32
+__device__ __forceinline__ double add_swapped(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t l = (uint32_t)b, h = (uint32_t)(b >> 32);
+  const auto p = W == 16 ? __builtin_amdgcn_permlane16_swap(l, l, false, false)
+                         : __builtin_amdgcn_permlane32_swap(l, l, false, false);
+  const auto q = W == 16 ? __builtin_amdgcn_permlane16_swap(h, h, false, false)
+                         : __builtin_amdgcn_permlane32_swap(h, h, false, false);
+  return __builtin_bit_cast(double, (uint64_t)q[0] << 32 | p[0]) +
+         __builtin_bit_cast(double, (uint64_t)q[1] << 32 | p[1]);
+}
+// Sum over the TPR threads of a row, as row_sum, but within a wave without LDS's way there and back
+// (8192 x 8192: 92 us with shuffles of both words, 90).
+template <int TPR>
+__device__ __forceinline__ double row_sum64(double v, double* red) {
+  v = add_dpp<0xB1>(v);   // lanes 1 apart
+  v = add_dpp<0x4E>(v);   // 2
+  v = add_dpp<0x141>(v);  // the halves of 8 lanes, mirrored
+  v = add_dpp<0x140>(v);  // of 16
+  if constexpr (TPR > 16) v = add_swapped<32>(add_swapped<16>(v));
+  if constexpr (TPR > 64) {
+    constexpr int NW = TPR / 64;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double t = 0.0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) t += red[w];
+    __syncthreads();
+    v = t;
+  }
+  return v;
+}
+// 1 / sqrt(mean + eps): the hardware's, 2^-26 and better, and one step that squares the error.
+__device__ __forceinline__ double rstd64(double mean, float eps) {
+  const double v = mean + (double)eps, y = __builtin_amdgcn_rsq(v);
+  const double e = __builtin_fma(-v * y, y, 1.0);
+  return fabs(e) < 1.0 ? __builtin_fma(0.5 * e, y, y) : y;  // (0, infinite, NaN: as it came)
+}
+template <typename Args>
+__device__ __forceinline__ double k64(const Args& p, float post_gamma, float gate) {
+  return (double)p.alpha * (double)post_gamma * (double)gate;
+}
+
+// BF16 rows of 2049 to 4096 columns fit into 128 registers, four waves a SIMD, which the compiler has to be
+// told (16384 x 4096 with a scale per row: 94 us with three, 88; with an FP32 x or stream it would spill).
 template <bool XBF, bool HBF, int TPR, int VPT, int MODE, bool AL>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_fwd_kernel(SandwichArgs p) {
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256, XBF && HBF && TPR == 256 && VPT == 2 ? 4 : 1)
+void sandwich_fwd_kernel(SandwichArgs p) {
   constexpr int NT = TPR > 256 ? TPR : 256;
   constexpr int RPB = NT / TPR;
-  __shared__ uint32_t red[2 * (NT / 64)];
+  __shared__ __attribute__((aligned(8))) uint32_t red[2 * (NT / 64)];
+  constexpr bool kFull = TPR == 1024 && VPT == 4;
+  __shared__ v2d k_lds[kFull ? 1 : TPR * VPT * 4];  // k of every column
   const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
   const int64_t C = p.cols;
   auto col = [&](int j) -> int64_t { return ((int64_t)t + TPR * j) * 8; };
@@ -283,8 +345,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_fwd_kernel(San
     return left <= 0 ? 0 : AL || left >= 8 ? 8 : (int)left;
   };
   // Rows of more than 16384 columns: parameters again for each row and group, the stream's group
-  // when x has been taken (4096 x 20480: 463 us with all of them held, 278).
-  constexpr bool kFull = TPR == 1024 && VPT == 4;
+  // when x has been taken (4096 x 20480: 463 us with all of them held, 245).
   struct RowData {
     Raw8<XBF> x[VPT];
     Raw8<HBF> res[kFull ? 1 : VPT];
@@ -305,17 +366,28 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_fwd_kernel(San
   constexpr bool kAhead = !kFull && VPT * (XBF ? 4 : 8) + VPT * (HBF ? 4 : 8) <= 32;
   RowData now;
   load_row((int64_t)blockIdx.x * RPB + slot, now);
-  float k[kFull ? 1 : VPT][8];
   Raw8<false> rg[VPT];
   auto load_gamma = [&] {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) rg[j] = gamma8<AL>(p.gamma, p.gamma_bf16, at(j));
   };
   if constexpr (!kFull) {
-    load_k<TPR, VPT, AL>(p, t, C, k);
+    if (slot == 0) {
+      float pg[VPT][8], g[VPT][8];
+      load_param<TPR, VPT, AL>(p.post_gamma, p.post_gamma_bf16, t, C, pg);
+      if (p.gate) load_param<TPR, VPT, AL>(p.gate, p.gate_bf16, t, C, g);
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2)
+          k_lds[(j * 4 + i / 2) * TPR + t] = v2d{k64(p, pg[j][i], p.gate ? g[j][i] : 1.0f),
+                                                 k64(p, pg[j][i + 1], p.gate ? g[j][i + 1] : 1.0f)};
+    }
     load_gamma();
+    __syncthreads();
   }
   const bool e5m2 = p.fmt == kE5M2;
+  const double inv_c = 1.0 / (double)C;
   const float given = MODE == kQTensor ? *p.scale_in : 1.0f;
   if (MODE == kQTensor && p.scale_used && blockIdx.x == 0 && threadIdx.x == 0) *p.scale_used = given;
   uint32_t amax = 0, sat = 0;
@@ -327,46 +399,51 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_fwd_kernel(San
       if (r0 + step < p.rows) load_row(row + step, next);
     }
     float h[VPT][8];
-    float ss = 0.0f;
+    double sx = 0.0;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int n = live ? count(j) : 0;
       take8<XBF, AL>(now.x[j], n, h[j]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += counted<AL>(i, n, h[j][i] * h[j][i]);
+      for (int i = 0; i < 8; i += 2)
+        sx += (double)(counted<AL>(i, n, h[j][i] * h[j][i]) + counted<AL>(i + 1, n, h[j][i + 1] * h[j][i + 1]));
     }
-    ss = row_sum<TPR>(ss, reinterpret_cast<float*>(red));
-    const float r1 = norm_rstd(ss, C, p.post_eps);
-    if (p.post_rstd && live && t == 0) p.post_rstd[row] = r1;
-    const float r1t = r1 * now.t;
-    ss = 0.0f;
+    const double r1 = rstd64(row_sum64<TPR>(sx, reinterpret_cast<double*>(red)) * inv_c, p.post_eps);
+    if (p.post_rstd && live && t == 0) p.post_rstd[row] = (float)r1;
+    const double r1t = r1 * (double)now.t;
+    float ss = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int n = live ? count(j) : 0;
       float r[8];
-      const int jk = kFull ? 0 : j;
+      float k[8];
       if constexpr (kFull) {
         now.res[0] = load8<HBF, AL>(p.res, (live ? row : p.rows - 1) * p.ldr + at(j));
-        take_gamma<AL>(gamma8<AL>(p.post_gamma, p.post_gamma_bf16, at(j)), p.post_gamma_bf16, n, k[0]);
+        take_gamma<AL>(gamma8<AL>(p.post_gamma, p.post_gamma_bf16, at(j)), p.post_gamma_bf16, n, k);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) k[0][i] *= p.alpha;
+        for (int i = 0; i < 8; ++i) k[i] *= p.alpha;
         if (p.gate) {
           float g[8];
           take_gamma<AL>(gamma8<AL>(p.gate, p.gate_bf16, at(j)), p.gate_bf16, n, g);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) k[0][i] *= g[i];
+          for (int i = 0; i < 8; ++i) k[i] *= g[i];
         }
       }
-      take8<HBF, AL>(now.res[jk], n, r);
+      take8<HBF, AL>(now.res[kFull ? 0 : j], n, r);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        h[j][i] = held<AL>(n, __builtin_fmaf(h[j][i], r1t * k[jk][i], r[i]));
+        if constexpr (kFull) {
+          h[j][i] = held<AL>(n, __builtin_fmaf(h[j][i], (float)r1t * k[i], r[i]));
+        } else {
+          const double k2 = k_lds[(j * 4 + i / 2) * TPR + t][i & 1];
+          h[j][i] = held<AL>(n, (float)__builtin_fma((double)h[j][i], r1t * k2, (double)r[i]));
+        }
         if constexpr (HBF) h[j][i] = bf16_round(h[j][i]);
         ss += counted<AL>(i, n, h[j][i] * h[j][i]);
       }
       if (n > 0) store_own<HBF, AL>(p.h, row * p.ldh + at(j), n, h[j]);
     }
-    ss = row_sum<TPR>(ss, reinterpret_cast<float*>(red));
+    ss = (float)row_sum64<TPR>((double)ss, reinterpret_cast<double*>(red));
     const float rstd = norm_rstd(ss, C, p.eps);
     if (p.rstd && live && t == 0) p.rstd[row] = rstd;
     if constexpr (kFull) load_gamma();

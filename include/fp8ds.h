@@ -782,7 +782,8 @@ int fp8ds_gated_gemm_bwd(int64_t M, int64_t F, int64_t H, const uint8_t* A, fp8d
  *   r1 = 1 / sqrt(sum_c x[c]^2 / cols + post_eps)
  *   h[c] = residual[c] + t (x[c] r1) (alpha gate[c] post_gamma[c])    rounded to ht
  *   r2 = 1 / sqrt(sum_c h[c]^2 / cols + eps),   y[c] = (h[c] r2) gamma[c]
- * with everything in fp32, and y cast as fp8ds_rmsnorm, _rowwise and _mx cast theirs.
+ * with h in 64 bits, rounded to fp32 and then to ht (rows of 8 to 16384 columns; others in fp32), the
+ * rest in fp32, and y cast as fp8ds_rmsnorm, _rowwise and _mx cast theirs.
  *   x, residual, h, y, gamma, eps, rstd (r2) and the cast's arguments: as those calls; residual and
  *              h are required here.  h may be residual itself.
  *   post_gamma device [cols] of pt.          post_eps  finite, >= 0.
