@@ -28,9 +28,9 @@
 // block pair from 8 fragment reads, half of what single operands would read per instruction.  A and
 // B are computed for the tiles on and below the diagonal only and stored with their mirror image;
 // all sizes are padded with zeros to whole tiles, so no tile has an edge.
-// 4096 x 14336, five steps: 6.9 ms.  In 256 x 256 tiles the steps' products run at 1.3 PFLOP/s of F16
+// 4096 x 14336, five steps: 6.9 to 7.0 ms.  In 256 x 256 tiles the steps' products run at 1.3 PFLOP/s of F16
 // (matrix unit 83 to 91% busy), the symmetric ones of 4096^3 at 1.1 (136 tiles for 256 CUs); momentum
-// with the norm's sum 0.13 ms and the split 0.16 are passes over memory.  333 x 130: 95 us, twenty
+// with the norm's sum 0.13 ms and the split 0.16 are passes over memory.  333 x 130: 96 us, twenty
 // launches of 3 to 6.5 us, each a chain of load - product - store.
 
 #include <algorithm>
